@@ -66,6 +66,7 @@ extern "C" {
 #define MOEQ8_MAX_EXCHANGE_RANKS 64  /* ranks one exchange sum takes */
 #define MOEQ8_EXCHANGE_BLOCK_BYTES 36
 #define MOEQ8_Q4_BLOCK_BYTES 18
+#define MOEQ8_MAX_I8_K 131071      /* values of one gemm_i8 sum: exact in int32 */
 
 enum moeq8_status {
     MOEQ8_OK = 0,
@@ -523,6 +524,84 @@ int moe_grouped_mmvq_q4(int32_t stage, const void* w_a, const void* w_b,
  * Strides >= k/32*18 bytes, pointers and strides multiples of 4 bytes. */
 int q4_pack64_rows(const void* src, int64_t n_rows, int64_t k, int64_t src_row_stride_bytes,
                    void* dst, int64_t dst_row_stride_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around the expert layer: the norm in front of it, the dense int8
+ * products beside it and the rules on the logits behind it.
+ *
+ * Rows are fp32, fp16 or bf16 (enum moeq8_dtype) at the alignment of their
+ * elements, row strides in elements (>= the row's length); any row length is
+ * accepted where none is named.  Arithmetic is fp32 unless stated; a value is
+ * rounded to its output type once, to the nearest even.  Outputs must not
+ * overlap inputs, except where a call says so.  Values that are not finite
+ * have the results given at each call.
+ * ------------------------------------------------------------------------- */
+enum moeq8_dtype {
+    MOEQ8_F32 = 0,
+    MOEQ8_F16 = 1,
+    MOEQ8_BF16 = 2
+};
+
+/* RMS norm with the residual's addition and 8-bit outputs:
+ *   s = fp32(x) + fp32(residual)                       (s = x without a residual)
+ *   y = (s * inv) * w,  inv = fp32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits
+ *   residual_out = dtype(s)
+ *   scale, q     int8 rows:  scale = max|y| / 127 over the row, q = roundf(y / scale)
+ *                on the fp32 quotient (halves away from zero), within +-127
+ *   xq           q8_1 blocks [n_rows][k/32], contiguous: q8_1_quantize_rows of y
+ *   x, residual, residual_out  dtype [n_rows][...]; w dtype [k]
+ * q and scale go together, as do residual and residual_out; q, xq or both are
+ * wanted; xq needs k % 32 == 0.  residual_out may be x or residual itself (the
+ * same rows).  A row or block of zeros has the scale 0 and zero codes.  A NaN
+ * or an infinity in a row makes its scale NaN and its codes 0 (in xq: for
+ * every block of the row); a finite row whose sum passes fp32 counts as such. */
+int rms_norm_q8(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
+                void* residual_out, int64_t residual_out_row_stride, const void* w, int32_t dtype,
+                int64_t n_rows, int64_t k, double eps, int8_t* q, int64_t q_row_stride, float* scale,
+                void* xq, void* stream);
+
+/* int8 rows with a scale each, by the rule of rms_norm_q8's q and scale on the
+ * values of x itself.  A row with an infinity has the scale inf and zero codes,
+ * one with a NaN the scale NaN and zero codes. */
+int i8_quantize_rows(const void* x, int32_t dtype, int64_t n_rows, int64_t k, int64_t x_row_stride,
+                     int8_t* q, int64_t q_row_stride, float* scale, void* stream);
+
+/* Product of int8 rows with token and channel scales:
+ *   out[i][j] = out_dtype((fp32(sum_k a[i][k] * b[j][k]) * sa[i]) * sb[j] + bias[j])
+ *   a    int8 [m][a_row_stride], sa fp32 [m]          (rows of i8_quantize_rows or rms_norm_q8)
+ *   b    int8 [n][b_row_stride], sb fp32 [n]          (weights, a scale per output channel)
+ *   bias fp32 [n] or NULL
+ *   out  out_dtype [m][out_row_stride]
+ * The sum is exact in int32; k <= MOEQ8_MAX_I8_K.  A row's result depends on
+ * its own row of a alone, not on m.  All 256 codes are allowed. */
+int gemm_i8(const int8_t* a, int64_t a_row_stride, const float* sa, const int8_t* b, int64_t b_row_stride,
+            const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, int32_t out_dtype,
+            void* out, int64_t out_row_stride, void* stream);
+
+/* Sampling rules on logits.  For row r, with its tokens tokens[begin[r] ..
+ * end[r]), those from prompt_end[r] on written by the model, in this order,
+ * each operation rounded in fp32:
+ *   seen tokens:     z = z > 0 ? z / repetition[r] : z * repetition[r]
+ *   written tokens:  z = z - (count * frequency[r] + presence[r])
+ *   biased tokens:   z = z + bias_values[i] for each i in bias_offsets[r] ..
+ *                    bias_offsets[r + 1) with bias_ids[i] the token, in order
+ *   masked tokens:   z = -inf where bit v % 32 of mask[r][v / 32] is 0
+ *   logits, out  dtype [n_rows][...]; out may be logits itself (the same rows)
+ *   tokens       int32 [n_tokens] or NULL (no penalties); rows may share lists
+ *   begin, end, prompt_end   int64 [n_rows]; prompt_end NULL: begin
+ *   repetition, frequency, presence   fp32 [n_rows]; NULL: 1, 0, 0
+ *   bias_ids int32, bias_values fp32 [n_bias], bias_offsets int64 [n_rows + 1],
+ *                or all NULL
+ *   mask         int32 [n_rows][mask_row_stride] or NULL
+ * Ids outside [0, vocab) are skipped; offsets are taken within their lists.
+ * Values that are not finite follow IEEE arithmetic; a masked token is -inf
+ * whatever its logit.  n_tokens < 2^30, vocab < 2^31. */
+int logits_process(const void* logits, int64_t logits_row_stride, int32_t dtype, int64_t n_rows, int64_t vocab,
+                   const int32_t* tokens, int64_t n_tokens, const int64_t* begin, const int64_t* end,
+                   const int64_t* prompt_end, const float* repetition, const float* frequency,
+                   const float* presence, const int32_t* bias_ids, const float* bias_values, int64_t n_bias,
+                   const int64_t* bias_offsets, const int32_t* mask, int64_t mask_row_stride, void* out,
+                   int64_t out_row_stride, void* stream);
 
 #ifdef __cplusplus
 }

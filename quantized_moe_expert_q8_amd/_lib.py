@@ -10,6 +10,7 @@ from .build import LIB_PATH
 
 c_i32, c_i64, c_u32, c_u64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
 c_vp, c_fp, c_size = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t
+c_f64 = ctypes.c_double
 
 # name -> (restype, argtypes); one entry per declaration in include/moeq8.h and
 # include/moeq8_synth.h
@@ -59,6 +60,13 @@ SIGNATURES = {
     "moe_route_topk_wide": (ctypes.c_int, [c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp,
                                            c_vp]),
     "moe_group_routes": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i64, c_vp, c_vp]),
+    "rms_norm_q8": (ctypes.c_int, [c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i32, c_i64, c_i64, c_f64,
+                                   c_vp, c_i64, c_vp, c_vp, c_vp]),
+    "i8_quantize_rows": (ctypes.c_int, [c_vp, c_i32, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp]),
+    "gemm_i8": (ctypes.c_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_i64, c_i32, c_vp,
+                               c_i64, c_vp]),
+    "logits_process": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]),
     "moeq8_synth_stream_key": (c_u64, [c_u32, c_u32, c_u32, c_u32]),
     "moeq8_synth_q8_0_fill": (ctypes.c_int, [c_vp, c_i64, c_i64, c_i64, c_u32, c_u32, c_u32,
                                              c_u32, c_vp]),

@@ -1,0 +1,354 @@
+// RMS norm with the residual's addition and 8-bit outputs, and the same 8-bit
+// rows without the norm.
+//
+//   s = f32(x) + f32(residual)          residual_out = T(s)
+//   y = (s * inv) * w                   inv = f32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits
+//   i8 rows:   d = max|y| / 127 over the row, codes roundf(y / d) on the fp32 quotient
+//   q8_1 rows: the block rule of q8_1_quantize_rows on y
+//
+// The sum of squares is held in 64 bits: a code is decided by one rounding of
+// y / d, and with a sum in 32 bits its order would move codes that lie next to
+// a half.  One pass over the data: a thread keeps its 8-value vectors of s in
+// registers between the two row reductions, so x and the residual are read
+// once.  What bounds it is the memory traffic, for few rows the launch.
+#include "moeq8_types.hpp"
+#include "moeq8_host.hpp"
+
+namespace moeq8 {
+namespace {
+
+struct NormArgs {
+    const void* x; int64_t x_stride;
+    const void* res; int64_t res_stride;          // null: no residual
+    void* res_out; int64_t res_out_stride;
+    const void* w;
+    int64_t rows, k;
+    double eps;
+    int8_t* q; int64_t q_stride;                  // null: no i8 rows
+    float* scale;
+    uint8_t* xq;                                  // null: no q8_1 rows
+};
+
+constexpr int VEC = 8;                            // values a thread takes at a time: a quarter of a block
+
+// Larger of two magnitudes, NaN if either is.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    return (a != a || b != b) ? __builtin_nanf("") : fmaxf(a, b);
+}
+
+template <typename V, typename F>
+__device__ __forceinline__ V wave_reduce(V v, F op) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v = op(v, __shfl_xor(v, m));
+    return v;
+}
+
+// Over the TPR threads of a row, in a fixed order; every thread gets the value.
+template <int TPR, typename V, typename F>
+__device__ __forceinline__ V row_reduce(V v, V* lds, F op) {
+    v = wave_reduce(v, op);
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64;
+        if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = lds[0];
+#pragma unroll
+        for (int i = 1; i < W; ++i) v = op(v, lds[i]);
+    }
+    return v;
+}
+
+// Codes of 8 values of scale d, packed; their sum.  d = 0 and a d that is not
+// finite give zeros (the scale says which).  The codes stay within 127: below
+// the normal range d is so coarse that a quotient may round past it.
+__device__ __forceinline__ uint2 codes8(const float (&y)[VEC], float d, int& sum) {
+    uint2 o = {0u, 0u};
+    sum = 0;
+    if (d > 0.0f && d < __builtin_inff()) {
+        const float rd = q8_code_rcp(d);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            int c = q8_code(y[i], d, rd);
+            c = c > 127 ? 127 : (c < -127 ? -127 : c);
+            sum += c;
+            const uint32_t b = ((uint32_t)c & 0xffu) << (8 * (i & 3));
+            if (i < 4) o.x |= b; else o.y |= b;
+        }
+    }
+    return o;
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[VEC], const T* p, int n) {
+    T t[VEC];
+    if (n >= VEC) {
+        load_vec(t, p);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = to_f32(t[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+    }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[VEC], int n) {
+    T t[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) from_f32(t[i], v[i]);
+    if (n >= VEC) {
+        store_vec(p, t);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i)
+            if (i < n) p[i] = t[i];
+    }
+}
+
+// s of vector i (n valid values) of row r.
+template <typename T>
+__device__ __forceinline__ void load_sum(float (&v)[VEC], const NormArgs& a, int64_t r, int64_t i, int n) {
+    load8(v, (const T*)a.x + r * a.x_stride + i * VEC, n);
+    if (a.res) {
+        float u[VEC];
+        load8(u, (const T*)a.res + r * a.res_stride + i * VEC, n);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) v[j] += u[j];
+    }
+}
+
+__device__ __forceinline__ float inv_rms(double sum, int64_t k, double eps) {
+    return (float)(1.0 / sqrt(sum / (double)k + eps));
+}
+
+// Outputs of one vector: y, with d the row's scale when i8 rows are wanted.
+__device__ __forceinline__ void store_codes(const NormArgs& a, const float (&y)[VEC], int64_t r, int64_t i, int n,
+                                            float d) {
+    int sum;
+    if (a.q) {
+        const uint2 c = codes8(y, d, sum);
+        int8_t* o = a.q + r * a.q_stride + i * VEC;
+        if (n >= VEC) {
+            *reinterpret_cast<u32x2b*>(o) = u32x2b{c.x, c.y};
+        } else {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if (j < n) o[j] = (int8_t)((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+        }
+    }
+    if (a.xq) {                                    // k % 32 == 0: the 4 lanes of a block are all here
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) m = max_or_nan(m, fabsf(y[j]));
+        m = max_or_nan(m, __shfl_xor(m, 1));
+        m = max_or_nan(m, __shfl_xor(m, 2));
+        const float db = m / 127.0f;
+        const uint2 c = codes8(y, db, sum);
+        sum += __shfl_xor(sum, 1);
+        sum += __shfl_xor(sum, 2);
+        uint32_t* o = reinterpret_cast<uint32_t*>(a.xq + (r * (a.k / QK) + i / 4) * Q81_BYTES);
+        if ((i & 3) == 0)
+            o[0] = float_to_half_bits(db) | (float_to_half_bits(materialize_f32(db * (float)sum)) << 16);
+        o[1 + 2 * (i & 3)] = c.x;
+        o[2 + 2 * (i & 3)] = c.y;
+    }
+}
+
+// TPR threads hold a row, NV vectors each (vector i of a thread is vector
+// i * TPR + thread of the row, so a wave's loads are contiguous).
+template <typename T, bool NORM, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_q8(NormArgs a) {
+    __shared__ double lds_sum[TPR / 64];
+    __shared__ float lds_max[TPR / 64];
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    const int t = threadIdx.x & (TPR - 1);
+    const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
+    if (r >= a.rows) return;                       // whole waves; with barriers a block is one row
+    float v[NV][VEC];
+    double sq = 0.0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t at = (int64_t)i * TPR + t;
+        const int64_t left = a.k - at * VEC;
+        const int n = left < VEC ? (left < 0 ? 0 : (int)left) : VEC;
+        load_sum<T>(v[i], a, r, n > 0 ? at : 0, n);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t at = (int64_t)i * TPR + t;
+        const int64_t left = a.k - at * VEC;
+        const int n = left < VEC ? (left < 0 ? 0 : (int)left) : VEC;
+        if (a.res) store8((T*)a.res_out + r * a.res_out_stride + at * VEC, v[i], n);
+        if constexpr (NORM) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sq += (double)v[i][j] * (double)v[i][j];
+        }
+    }
+    float m = 0.0f;
+    if constexpr (NORM) {
+        sq = row_reduce<TPR>(sq, lds_sum, [](double p, double q) { return p + q; });
+        const float inv = inv_rms(sq, a.k, a.eps);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int64_t at = (int64_t)i * TPR + t;
+            const int64_t left = a.k - at * VEC;
+            const int n = left < VEC ? (left < 0 ? 0 : (int)left) : VEC;
+            float w[VEC];
+            load8(w, (const T*)a.w + (n > 0 ? at * VEC : 0), n);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[i][j] = (v[i][j] * inv) * w[j];
+        }
+    }
+    float d = 0.0f;
+    if (a.q) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) m = max_or_nan(m, fabsf(v[i][j]));
+        }
+        m = row_reduce<TPR>(m, lds_max, [](float p, float q) { return max_or_nan(p, q); });
+        d = m / 127.0f;
+        if (t == 0) a.scale[r] = d;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int64_t at = (int64_t)i * TPR + t;
+        const int64_t left = a.k - at * VEC;
+        const int n = left < VEC ? (left < 0 ? 0 : (int)left) : VEC;
+        if (n > 0) store_codes(a, v[i], r, at, n, d);
+    }
+}
+
+// Rows longer than the registers of one block hold: three passes over the
+// row.  Each thread comes back to its own vectors, and residual_out is written
+// in the last pass, so it may be the residual or x itself.
+template <typename T, bool NORM>
+__global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {
+    __shared__ double lds_sum[16];
+    __shared__ float lds_max[16];
+    const int64_t r = blockIdx.x;
+    const int64_t nvec = (a.k + VEC - 1) / VEC;
+    float inv = 1.0f;
+    if constexpr (NORM) {
+        double sq = 0.0;
+        for (int64_t at = threadIdx.x; at < nvec; at += 1024) {
+            float v[VEC];
+            const int n = (int)(a.k - at * VEC < VEC ? a.k - at * VEC : VEC);
+            load_sum<T>(v, a, r, at, n);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) sq += (double)v[j] * (double)v[j];
+        }
+        sq = row_reduce<1024>(sq, lds_sum, [](double p, double q) { return p + q; });
+        inv = inv_rms(sq, a.k, a.eps);
+    }
+    auto row_y = [&](float (&v)[VEC], int64_t at, int n) {
+        load_sum<T>(v, a, r, at, n);
+        if constexpr (NORM) {
+            float w[VEC];
+            load8(w, (const T*)a.w + at * VEC, n);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) v[j] = (v[j] * inv) * w[j];
+        }
+    };
+    float d = 0.0f;
+    if (a.q) {
+        float m = 0.0f;
+        for (int64_t at = threadIdx.x; at < nvec; at += 1024) {
+            float v[VEC];
+            const int n = (int)(a.k - at * VEC < VEC ? a.k - at * VEC : VEC);
+            row_y(v, at, n);
+#pragma unroll
+            for (int j = 0; j < VEC; ++j) m = max_or_nan(m, fabsf(v[j]));
+        }
+        m = row_reduce<1024>(m, lds_max, [](float p, float q) { return max_or_nan(p, q); });
+        d = m / 127.0f;
+        if (threadIdx.x == 0) a.scale[r] = d;
+    }
+    for (int64_t at = threadIdx.x; at < nvec; at += 1024) {
+        float v[VEC], s[VEC];
+        const int n = (int)(a.k - at * VEC < VEC ? a.k - at * VEC : VEC);
+        row_y(v, at, n);
+        if (a.res) {
+            load_sum<T>(s, a, r, at, n);
+            store8((T*)a.res_out + r * a.res_out_stride + at * VEC, s, n);
+        }
+        store_codes(a, v, r, at, n, d);
+    }
+}
+
+template <typename T, bool NORM, int TPR, int NV>
+int launch(const NormArgs& a, hipStream_t stream) {
+    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    const int64_t blocks = (a.rows + RPB - 1) / RPB;
+    if (blocks > 0x7fffffff) return MOEQ8_EUNSUPPORTED;
+    hipLaunchKernelGGL((k_norm_q8<T, NORM, TPR, NV>), dim3((uint32_t)blocks), dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
+    return check_launch();
+}
+
+template <typename T, bool NORM>
+int launch_rows(const NormArgs& a, hipStream_t stream) {
+    if (a.k <= 512) return launch<T, NORM, 64, 1>(a, stream);
+    if (a.k <= 2048) return launch<T, NORM, 256, 1>(a, stream);
+    if (a.k <= 4096) return launch<T, NORM, 256, 2>(a, stream);
+    if (a.k <= 8192) return launch<T, NORM, 256, 4>(a, stream);
+    if (a.k <= 16384) return launch<T, NORM, 1024, 2>(a, stream);
+    if (a.k <= 32768) return launch<T, NORM, 1024, 4>(a, stream);
+    if (a.rows > 0x7fffffff) return MOEQ8_EUNSUPPORTED;
+    hipLaunchKernelGGL((k_norm_q8_long<T, NORM>), dim3((uint32_t)a.rows), dim3(1024), 0, stream, a);
+    return check_launch();
+}
+
+template <bool NORM>
+int launch_dtype(int32_t dtype, const NormArgs& a, void* stream) {
+    switch (dtype) {
+        case MOEQ8_F32: return launch_rows<float, NORM>(a, (hipStream_t)stream);
+        case MOEQ8_F16: return launch_rows<f16_t, NORM>(a, (hipStream_t)stream);
+        default: return launch_rows<bf16_t, NORM>(a, (hipStream_t)stream);
+    }
+}
+
+// Whether two row ranges overlap otherwise than by being the same rows (each
+// thread reads its own elements before it writes them, so in place is fine).
+bool clash(const void* p, int64_t p_stride, const void* o, int64_t o_stride, int64_t rows, int64_t k, int es) {
+    if (p == o && p_stride == o_stride) return false;
+    return ranges_overlap(p, ((rows - 1) * p_stride + k) * es, o, ((rows - 1) * o_stride + k) * es);
+}
+
+}  // namespace
+}  // namespace moeq8
+
+extern "C" int rms_norm_q8(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
+                           void* residual_out, int64_t residual_out_row_stride, const void* w, int32_t dtype,
+                           int64_t n_rows, int64_t k, double eps, int8_t* q, int64_t q_row_stride, float* scale,
+                           void* xq, void* stream) {
+    using namespace moeq8;
+    if (dtype < MOEQ8_F32 || dtype > MOEQ8_BF16 || n_rows < 0 || k <= 0 || !(eps >= 0.0)) return MOEQ8_EINVAL;
+    if (!x || !w || (!q && !xq) || !q != !scale || !residual != !residual_out) return MOEQ8_EINVAL;
+    if (x_row_stride < k || (residual && (residual_row_stride < k || residual_out_row_stride < k)) ||
+        (q && q_row_stride < k) || (xq && k % QK != 0))
+        return MOEQ8_EINVAL;
+    const int es = dtype_bytes(dtype);
+    if (((uintptr_t)x | (uintptr_t)w | (uintptr_t)residual | (uintptr_t)residual_out) & (uintptr_t)(es - 1))
+        return MOEQ8_EALIGN;
+    if (((uintptr_t)scale | (uintptr_t)xq) & 3u) return MOEQ8_EALIGN;
+    if (n_rows == 0) return MOEQ8_OK;
+    if (residual && (clash(x, x_row_stride, residual_out, residual_out_row_stride, n_rows, k, es) ||
+                     clash(residual, residual_row_stride, residual_out, residual_out_row_stride, n_rows, k, es)))
+        return MOEQ8_EINVAL;
+    NormArgs a{x, x_row_stride, residual, residual_row_stride, residual_out, residual_out_row_stride, w,
+               n_rows, k, eps, q, q_row_stride, scale, (uint8_t*)xq};
+    return launch_dtype<true>(dtype, a, stream);
+}
+
+extern "C" int i8_quantize_rows(const void* x, int32_t dtype, int64_t n_rows, int64_t k, int64_t x_row_stride,
+                                int8_t* q, int64_t q_row_stride, float* scale, void* stream) {
+    using namespace moeq8;
+    if (dtype < MOEQ8_F32 || dtype > MOEQ8_BF16 || n_rows < 0 || k <= 0 || !x || !q || !scale ||
+        x_row_stride < k || q_row_stride < k)
+        return MOEQ8_EINVAL;
+    if ((uintptr_t)x & (uintptr_t)(dtype_bytes(dtype) - 1)) return MOEQ8_EALIGN;
+    if ((uintptr_t)scale & 3u) return MOEQ8_EALIGN;
+    if (n_rows == 0) return MOEQ8_OK;
+    NormArgs a{x, x_row_stride, nullptr, 0, nullptr, 0, nullptr, n_rows, k, 0.0, q, q_row_stride, scale, nullptr};
+    return launch_dtype<false>(dtype, a, stream);
+}

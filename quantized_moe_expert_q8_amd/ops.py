@@ -9,6 +9,7 @@ library's kernels; torch only provides memory and the stream.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -769,6 +770,228 @@ def moe_combine(y: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
         _need(shared, "shared", ncols * n * 4)
         call("moe_combine_shared", _ptr(y), _ptr(ids), _ptr(weights), ncols, topk, n, _ptr(shared),
              _ptr(out), _stream(y))
+    return out
+
+
+# ---------------------------------------------------------------------------
+# around the expert layer: norm, int8 products, logits
+# ---------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}       # enum moeq8_dtype
+NORM_FMTS = ("i8", "q8_1", "both")
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if code is None:
+        raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor")
+    return code
+
+
+def _matrix(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
+    """Checks a device matrix [rows, cols] of rows whose elements lie together;
+    returns its row stride."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor, on the same device as the others")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit inner stride")
+    return stride if rows > 1 else cols
+
+
+def _vector(t: torch.Tensor, name: str, dtype, dev: int, n: int) -> int:
+    """Checks a contiguous device vector of n elements; returns its address."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
+        raise ValueError(f"{name} must be a device tensor, on the same device as the others")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be contiguous [{n}], got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _on(t: torch.Tensor, name: str) -> int:
+    """Device index of a 2-D device tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    return t.get_device()
+
+
+def _current_stream(dev: int) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+class NormQ8(NamedTuple):
+    """Outputs of rms_norm_q8; None where not wanted."""
+    q: torch.Tensor | None             # int8 [rows, k]
+    scale: torch.Tensor | None         # fp32 [rows]
+    xq: torch.Tensor | None            # q8_1 blocks, uint8 [rows, k/32*36]
+    residual: torch.Tensor | None      # x + residual, x's dtype [rows, k]
+
+
+def rms_norm_q8(x: torch.Tensor, w: torch.Tensor, *, eps: float = 1e-6, residual: torch.Tensor | None = None,
+                residual_out: torch.Tensor | None = None, fmt: str = "i8", q: torch.Tensor | None = None,
+                scale: torch.Tensor | None = None, xq: torch.Tensor | None = None) -> NormQ8:
+    """RMS norm of x (+ residual) [rows, k] (fp32, fp16 or bf16) with weight
+    w [k], to int8 rows with a scale each (fmt "i8"), to q8_1 rows ("q8_1", k a
+    multiple of 32) or to both.  Given outputs are written, missing ones made;
+    residual_out may be x or residual (updated in place)."""
+    dev = _on(x, "x")
+    code = _dtype_code(x, "x")
+    if fmt not in NORM_FMTS:
+        raise ValueError(f"fmt must be one of {NORM_FMTS}, got {fmt!r}")
+    rows, k = x.shape
+    dt = x.dtype
+    xs = _matrix(x, "x", dt, dev, rows, k)
+    wp = _vector(w, "w", dt, dev, k)
+    rs = ros = qs = 0
+    if residual is not None:
+        rs = _matrix(residual, "residual", dt, dev, rows, k)
+        if residual_out is None:
+            residual_out = torch.empty((rows, k), dtype=dt, device=x.device)
+        ros = _matrix(residual_out, "residual_out", dt, dev, rows, k)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    if fmt != "q8_1":
+        if q is None:
+            q = torch.empty((rows, k), dtype=torch.int8, device=x.device)
+        if scale is None:
+            scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+        qs = _matrix(q, "q", torch.int8, dev, rows, k)
+        _vector(scale, "scale", torch.float32, dev, rows)
+    else:
+        q = scale = None
+    if fmt != "i8":
+        if k % QK:
+            raise ValueError(f"q8_1 rows need k to be a multiple of {QK}, got {k}")
+        nb = k // QK * Q8_1_BLOCK_BYTES
+        if xq is None:
+            xq = torch.empty((rows, nb), dtype=torch.uint8, device=x.device)
+        if _matrix(xq, "xq", torch.uint8, dev, rows, nb) != nb:
+            raise ValueError("xq rows must be contiguous")
+    else:
+        xq = None
+    if rows:
+        call("rms_norm_q8", x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
+             None if residual_out is None else residual_out.data_ptr(), ros, wp, code, rows, k, eps,
+             None if q is None else q.data_ptr(), qs, None if scale is None else scale.data_ptr(),
+             None if xq is None else xq.data_ptr(), _current_stream(dev))
+    return NormQ8(q, scale, xq, residual_out)
+
+
+def i8_quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None,
+                     scale: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """x [rows, k] (fp32, fp16 or bf16) -> int8 rows [rows, k] and their fp32
+    scales [rows]: scale = max|x| / 127, codes rounded, halves away from zero."""
+    dev = _on(x, "x")
+    code = _dtype_code(x, "x")
+    rows, k = x.shape
+    xs = _matrix(x, "x", x.dtype, dev, rows, k)
+    if q is None:
+        q = torch.empty((rows, k), dtype=torch.int8, device=x.device)
+    if scale is None:
+        scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    qs = _matrix(q, "q", torch.int8, dev, rows, k)
+    sp = _vector(scale, "scale", torch.float32, dev, rows)
+    if rows:
+        call("i8_quantize_rows", x.data_ptr(), code, rows, k, xs, q.data_ptr(), qs, sp, _current_stream(dev))
+    return q, scale
+
+
+def gemm_i8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, *,
+            bias: torch.Tensor | None = None, out: torch.Tensor | None = None,
+            out_dtype: torch.dtype = torch.float32) -> torch.Tensor:
+    """out [m, n] = (a . b^T) * sa[:, None] * sb + bias, for int8 rows a [m, k]
+    with a scale each (rms_norm_q8, i8_quantize_rows) and int8 weights b [n, k]
+    with a scale per channel.  The sums are exact.  out's dtype (out_dtype if
+    out is made here) is float32, float16 or bfloat16."""
+    dev = _on(a, "a")
+    _on(b, "b")
+    (m, k), n = a.shape, b.shape[0]
+    as_ = _matrix(a, "a", torch.int8, dev, m, k)
+    bs = _matrix(b, "b", torch.int8, dev, n, k)
+    sap = _vector(sa, "sa", torch.float32, dev, m)
+    sbp = _vector(sb, "sb", torch.float32, dev, n)
+    bp = None if bias is None else _vector(bias, "bias", torch.float32, dev, n)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=a.device)
+    code = _dtype_code(out, "out")
+    os_ = _matrix(out, "out", out.dtype, dev, m, n)
+    if m and n:
+        call("gemm_i8", a.data_ptr(), as_, sap, b.data_ptr(), bs, sbp, bp, m, n, k, code, out.data_ptr(), os_,
+             _current_stream(dev))
+    return out
+
+
+def logits_process(logits: torch.Tensor, *, tokens: torch.Tensor | None = None, begin: torch.Tensor | None = None,
+                   end: torch.Tensor | None = None, prompt_end: torch.Tensor | None = None,
+                   repetition: torch.Tensor | None = None, frequency: torch.Tensor | None = None,
+                   presence: torch.Tensor | None = None, bias_ids: torch.Tensor | None = None,
+                   bias_values: torch.Tensor | None = None, bias_offsets: torch.Tensor | None = None,
+                   mask: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Penalties, biases and a grammar mask on logits [rows, vocab] (fp32, fp16
+    or bf16), in that order, into out (may be logits).
+
+    Row r's tokens are tokens[begin[r]:end[r]] (int32; rows may share lists),
+    those from prompt_end[r] on written by the model; repetition divides
+    positive and multiplies other logits of every token seen, frequency (times
+    its count) and presence are subtracted from the written ones.  Row r's
+    biases are entries bias_offsets[r]:bias_offsets[r + 1] of bias_ids (int32)
+    and bias_values.  mask int32 [rows, ceil(vocab / 32)]: bit v % 32 of word
+    v // 32 allows token v.  begin, end, prompt_end and bias_offsets are int64,
+    the penalties fp32."""
+    dev = _on(logits, "logits")
+    code = _dtype_code(logits, "logits")
+    rows, vocab = logits.shape
+    zs = _matrix(logits, "logits", logits.dtype, dev, rows, vocab)
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    os_ = _matrix(out, "out", logits.dtype, dev, rows, vocab)
+    tp = bp = ep = pp = rp = fp = sp = ip = vp = op = mp = None
+    nt = nb = ms = 0
+    if tokens is not None:
+        if begin is None or end is None:
+            raise ValueError("tokens need begin and end")
+        nt = tokens.numel()
+        tp = _vector(tokens, "tokens", torch.int32, dev, nt)
+        bp = _vector(begin, "begin", torch.int64, dev, rows)
+        ep = _vector(end, "end", torch.int64, dev, rows)
+        if prompt_end is not None:
+            pp = _vector(prompt_end, "prompt_end", torch.int64, dev, rows)
+        if repetition is not None:
+            rp = _vector(repetition, "repetition", torch.float32, dev, rows)
+        if frequency is not None:
+            fp = _vector(frequency, "frequency", torch.float32, dev, rows)
+        if presence is not None:
+            sp = _vector(presence, "presence", torch.float32, dev, rows)
+        if nt == 0:                                # an empty list has no address
+            tp = bp = ep = pp = rp = fp = sp = None
+    elif not (begin is None and end is None and prompt_end is None and repetition is None and frequency is None
+              and presence is None):
+        raise ValueError("penalties need tokens")
+    if bias_ids is not None:
+        if bias_values is None or bias_offsets is None:
+            raise ValueError("bias_ids, bias_values and bias_offsets go together")
+        nb = bias_ids.numel()
+        ip = _vector(bias_ids, "bias_ids", torch.int32, dev, nb)
+        vp = _vector(bias_values, "bias_values", torch.float32, dev, nb)
+        op = _vector(bias_offsets, "bias_offsets", torch.int64, dev, rows + 1)
+        if nb == 0:
+            ip = vp = op = None
+    elif not (bias_values is None and bias_offsets is None):
+        raise ValueError("bias_ids, bias_values and bias_offsets go together")
+    if mask is not None:
+        ms = _matrix(mask, "mask", torch.int32, dev, rows, (vocab + 31) // 32)
+        mp = mask.data_ptr()
+    if rows and vocab:
+        call("logits_process", logits.data_ptr(), zs, code, rows, vocab, tp, nt, bp, ep, pp, rp, fp, sp, ip, vp, nb,
+             op, mp, ms, out.data_ptr(), os_, _current_stream(dev))
     return out
 
 

@@ -1,0 +1,543 @@
+"""The operators around the expert layer on the GPU, against their numpy forms.
+
+Tolerances count half steps: fp32 operations move a value by at most 2^-24 of
+it each, the output type by eps / 2.  Where the numpy form takes the same fp32
+roundings, results are compared exactly."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_moe_expert_q8_amd as moeq8  # noqa: E402
+from oracle import operators_ref as ref  # noqa: E402
+from _gpu import DEV, say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+ULP = 2.0**-24                       # half a step of fp32, relative
+CANARY = 77
+
+
+def typed(a, dtype):
+    """fp32 numpy values -> (CPU tensor of dtype, the fp32 values it holds)."""
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(dtype)
+    return t, t.float().numpy()
+
+
+def framed(rows, cols, dtype, pad=0, lead=0, fill=CANARY):
+    """A device matrix inside a filled buffer, its rows `pad` elements apart and
+    the first one `lead` elements in; returns (buffer, matrix)."""
+    n = lead + rows * (cols + pad) + 40
+    buf = torch.full((n,), fill, dtype=dtype, device=DEV)
+    return buf, buf[lead:lead + rows * (cols + pad)].view(rows, cols + pad)[:, :cols]
+
+
+def frame_kept(buf, rows, cols, pad, lead, fill=CANARY):
+    a = buf.cpu().clone()
+    a[lead:lead + rows * (cols + pad)].view(rows, cols + pad)[:, :cols] = fill
+    return bool((a == fill).all())
+
+
+def put(t, pad=0, lead=0):
+    """A CPU matrix at the given stride and offset on the device."""
+    buf, m = framed(*t.shape, t.dtype, pad, lead, 0)
+    m.copy_(t)
+    return m
+
+
+def same(a, b):
+    """Equal values, NaN where NaN."""
+    a, b = np.asarray(a), np.asarray(b)
+    return a.shape == b.shape and bool(np.all((a == b) | (np.isnan(a) & np.isnan(b))))
+
+
+def q81_fields(xq, rows):
+    raw = xq.cpu().contiguous().numpy().reshape(rows, -1, 36)
+    return (raw[:, :, 0:2].copy().view(np.float16)[:, :, 0], raw[:, :, 2:4].copy().view(np.float16)[:, :, 0],
+            raw[:, :, 4:].copy().view(np.int8).astype(np.int64))
+
+
+# ---- RMS norm with 8-bit outputs ---------------------------------------------
+
+def check_norm(x, w, res, dtype, fmt, pad=0, lead=0, eps=1e-6, inplace=None):
+    rows, k = x.shape
+    xt, xv = typed(x, dtype)
+    wt, wv = typed(w, dtype)
+    rt, rv = (None, None) if res is None else typed(res, dtype)
+    xd, wd = put(xt, pad, lead), wt.to(DEV)
+    rd = None if res is None else put(rt, pad + 1, lead)
+    ro = None
+    if res is not None:
+        rbuf, ro = framed(rows, k, dtype, pad, lead)
+        if inplace == "residual":
+            ro = rd
+        elif inplace == "x":
+            ro = xd
+    qbuf, q = framed(rows, k, torch.int8, pad, lead)
+    sbuf = torch.full((rows + 2,), float(CANARY), device=DEV)
+    xqbuf = torch.full((rows * (k // 32 * 36) + 8,), CANARY, dtype=torch.uint8, device=DEV)
+    xq = xqbuf[4:4 + rows * (k // 32 * 36)].view(rows, -1) if fmt != "i8" else None
+    got = moeq8.rms_norm_q8(xd, wd, eps=eps, residual=rd, residual_out=ro, fmt=fmt, q=q, scale=sbuf[1:-1], xq=xq)
+    torch.cuda.synchronize()
+    s, y = ref.rms_norm_steps(xv, wv, eps, rv)
+    _, y64 = ref.rms_norm_def(xv, wv, eps, rv)
+    if res is not None:
+        assert torch.equal(got.residual.cpu(), torch.from_numpy(s).to(dtype))
+        if inplace is None:
+            assert frame_kept(rbuf, rows, k, pad, lead)
+            assert torch.equal(xd.cpu(), xt)
+    else:
+        assert got.residual is None
+    if fmt != "q8_1":
+        qs, d = ref.quantize_rows_steps(y)
+        assert same(got.scale.cpu().numpy(), d)
+        assert np.array_equal(got.q.cpu().numpy(), qs)
+        # the definition: s, inv and the two products round once each, the scale a fifth time
+        t64, d64 = ref.quantize_rows_def(y64)
+        assert np.all(np.abs(d - d64) <= 5.01 * ULP * d64)
+        assert np.all(np.abs(qs - t64) <= 0.5 + 127 * 10.01 * ULP)
+        assert frame_kept(qbuf, rows, k, pad, lead)
+    else:
+        assert got.q is None and got.scale is None
+        assert bool((qbuf == CANARY).all()) and bool((sbuf == CANARY).all())
+    assert float(sbuf[0]) == CANARY and float(sbuf[-1]) == CANARY
+    if fmt != "i8":
+        d, bs, bq = q81_fields(got.xq, rows)
+        ed, es, eq = ref.q8_1_steps(y)
+        assert np.array_equal(d.view(np.uint16), ed.view(np.uint16))
+        assert np.array_equal(bs.view(np.uint16), es.view(np.uint16))
+        assert np.array_equal(bq, eq)
+        assert np.array_equal(moeq8.q8_1_quantize_rows(torch.from_numpy(y).to(DEV)).cpu().numpy(),
+                              got.xq.cpu().numpy())
+        ends = torch.cat([xqbuf[:4], xqbuf[-4:]])
+        assert bool((ends == CANARY).all())
+    else:
+        assert got.xq is None
+
+
+def norm_inputs(rows, k, seed, residual):
+    g = np.random.default_rng(seed)
+    loud = 1 + 15 * (g.random(k) < 0.02)
+    return (g.standard_normal((rows, k)) * loud, 1 + 0.1 * g.standard_normal(k),
+            4 * g.standard_normal((rows, k)) * loud if residual else None)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,k", [(1, 1), (3, 7), (5, 8), (2, 33), (9, 200), (4, 512), (3, 513), (2, 1031),
+                                    (5, 2047), (3, 2048), (2, 2049), (1, 4096), (3, 4097), (2, 8192), (2, 8200),
+                                    (1, 16384), (2, 16385), (1, 32768), (2, 32775)])
+def test_norm_i8_lengths(rows, k, dtype):
+    say(f"norm i8 {rows}x{k} {dtype}")
+    x, w, res = norm_inputs(rows, k, k * 31 + rows, residual=k % 2 == 1)
+    check_norm(x, w, res, TYPES[dtype], "i8")
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("fmt", ["q8_1", "both"])
+@pytest.mark.parametrize("rows,k", [(1, 32), (7, 64), (3, 480), (2, 544), (5, 2016), (3, 2080), (5, 4096), (1, 4128),
+                                    (2, 8192), (1, 16384), (1, 32800)])
+def test_norm_q81_lengths(rows, k, fmt, dtype):
+    say(f"norm {fmt} {rows}x{k} {dtype}")
+    x, w, res = norm_inputs(rows, k, k * 17 + rows, residual=rows % 2 == 1)
+    check_norm(x, w, res, TYPES[dtype], fmt)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("k", [96, 576, 2080, 4096, 33024])
+def test_norm_strides_and_in_place(k, dtype):
+    say(f"norm strides {k} {dtype}")
+    x, w, res = norm_inputs(3, k, k, residual=True)
+    check_norm(x, w, res, TYPES[dtype], "both", pad=5, lead=3)
+    for where in ("x", "residual"):
+        check_norm(x, w, res, TYPES[dtype], "both", pad=2, lead=1, inplace=where)
+
+
+@pytest.mark.parametrize("rows", [129, 1000])
+def test_norm_many_rows(rows):
+    say(f"norm rows {rows}")
+    x, w, res = norm_inputs(rows, 288, rows, residual=True)
+    check_norm(x, w, res, torch.bfloat16, "both")
+
+
+def test_norm_extreme_values():
+    """Zero rows, subnormal rows, rows of the largest values, a huge eps, and
+    rows that are not finite beside rows that are."""
+    say("norm extremes")
+    k = 64
+    g = np.random.default_rng(1)
+    x = g.standard_normal((8, k))
+    x[1] = 0
+    x[2] *= 1e-42
+    x[3] = np.where(np.arange(k) % 2, 3e38, -3e38)
+    x[4, 5] = np.nan
+    x[5, 6] = np.inf
+    x[6] *= 1e-20
+    w = 1 + 0.1 * g.standard_normal(k)
+    for eps in (1e-6, 1e30):
+        xt, xv = typed(x, torch.float32)
+        wt, wv = typed(w, torch.float32)
+        got = moeq8.rms_norm_q8(xt.to(DEV), wt.to(DEV), eps=eps, fmt="both")
+        _, y = ref.rms_norm_steps(xv, wv, eps)
+        q, d = ref.quantize_rows_steps(y)
+        assert same(got.scale.cpu().numpy(), d) and np.array_equal(got.q.cpu().numpy(), q)
+        bd, bs, bq = q81_fields(got.xq, 8)
+        ed, es, eq = ref.q8_1_steps(y)
+        assert same(bd, ed) and same(bs, es) and np.array_equal(bq, eq)
+    assert np.isnan(got.scale.cpu().numpy()[[4, 5]]).all()
+
+
+def test_norm_without_rows_and_made_outputs():
+    x, w, res = (torch.randn(2, 64, device=DEV), torch.ones(64, device=DEV), torch.randn(2, 64, device=DEV))
+    out = moeq8.rms_norm_q8(x[:0], w, residual=res[:0], fmt="both")
+    assert out.q.shape == (0, 64) and out.scale.shape == (0,) and out.xq.shape == (0, 72) and out.residual.shape == (0, 64)
+    out = moeq8.rms_norm_q8(x, w, residual=res)
+    assert out.q.dtype == torch.int8 and out.xq is None and torch.equal(out.residual, x + res)
+
+
+# ---- int8 rows -----------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,k,pad,lead", [(1, 1, 0, 0), (2, 5, 3, 1), (6, 64, 0, 0), (300, 100, 0, 0), (3, 511, 0, 1),
+                                             (2, 2047, 0, 0), (5, 4096, 7, 5), (2, 9000, 1, 0), (1, 20001, 0, 0),
+                                             (2, 40000, 0, 3)])
+def test_rows_lengths(rows, k, pad, lead, dtype):
+    say(f"rows {rows}x{k} {dtype}")
+    xt, xv = typed(np.random.default_rng(k).standard_normal((rows, k)) * 3, TYPES[dtype])
+    qbuf, q = framed(rows, k, torch.int8, pad, lead)
+    got, scale = moeq8.i8_quantize_rows(put(xt, pad, lead), q=q)
+    qs, d = ref.quantize_rows_steps(xv)
+    assert np.array_equal(scale.cpu().numpy(), d) and np.array_equal(got.cpu().numpy(), qs)
+    assert frame_kept(qbuf, rows, k, pad, lead)
+
+
+def test_rows_halves_and_extremes():
+    say("rows halves")
+    half = np.arange(-127, 127) + 0.5                  # every half, scale 1
+    x = np.zeros((7, 256), np.float32)
+    x[0, :254], x[0, 254] = half, 127
+    x[1, :254], x[1, 254] = half * 2.0**-100, 127 * 2.0**-100
+    x[2] = 1e-44                                       # a scale of zero steps
+    x[3, 0], x[3, 1] = 190 * 2.0**-149, -190 * 2.0**-149   # a scale rounded down: codes stop at 127
+    x[4, 3] = -np.inf
+    x[5, 3] = np.nan
+    x[6] = 3.4e38
+    q, scale = moeq8.i8_quantize_rows(torch.from_numpy(x).to(DEV))
+    qs, d = ref.quantize_rows_steps(x)
+    assert same(scale.cpu().numpy(), d) and np.array_equal(q.cpu().numpy(), qs)
+
+
+# ---- int8 product ---------------------------------------------------------------
+
+def gemm_inputs(m, n, k, seed, bias):
+    g = np.random.default_rng(seed)
+    a, b = (g.integers(-128, 128, s, dtype=np.int8) for s in ((m, k), (n, k)))
+    sa, sb = (0.01 + 0.03 * g.random(m)).astype(np.float32), (4e-4 + 4e-4 * g.random(n)).astype(np.float32)
+    return a, sa, b, sb, g.standard_normal(n).astype(np.float32) if bias else None
+
+
+def check_gemm(m, n, k, dtype, bias, pads=(0, 0, 0), leads=(0, 0, 0), codes=None):
+    a, sa, b, sb, bi = gemm_inputs(m, n, k, m * 7 + n * 5 + k, bias)
+    if codes is not None:
+        a[:], b[:] = codes
+    ad, bd = put(torch.from_numpy(a), pads[0], leads[0]), put(torch.from_numpy(b), pads[1], leads[1])
+    obuf, out = framed(m, n, dtype, pads[2], leads[2])
+    dev = lambda v: None if v is None else torch.from_numpy(v).to(DEV)
+    got = moeq8.gemm_i8(ad, dev(sa), bd, dev(sb), bias=dev(bi), out=out)
+    torch.cuda.synchronize()
+    steps = torch.from_numpy(ref.gemm_i8_steps(a, sa, b, sb, bi)).to(dtype)
+    assert torch.equal(got.cpu(), steps)
+    v64 = ref.gemm_i8_def(a, sa, b, sb, bi)
+    prod = ref.gemm_i8_def(a, sa, b, sb)
+    half = torch.finfo(dtype).eps / 2 if dtype != torch.float32 else 0.0
+    # the sum's conversion and two products round the product, the bias the sum, then the type
+    bound = (3.01 * ULP * np.abs(prod) + 1.01 * ULP * np.abs(v64)) * (1 + half) + half * np.abs(v64) + 2.0**-25
+    assert np.all(np.abs(got.cpu().double().numpy() - v64) <= bound)
+    assert frame_kept(obuf, m, n, pads[2], leads[2])
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (1, 1, 1), (1, 16, 64), (1, 64, 4096), (1, 1000, 1024), (2, 17, 63), (3, 5, 100), (5, 300, 4096), (8, 128, 192),
+    (15, 33, 65), (16, 64, 512), (16, 256, 8192), (17, 16, 64), (31, 100, 1000), (32, 512, 256), (33, 64, 129),
+    (48, 96, 320), (63, 65, 64), (64, 64, 128), (64, 333, 2048), (65, 130, 17), (100, 1, 640), (128, 128, 1024),
+    (129, 257, 191), (200, 384, 576), (255, 255, 255), (256, 256, 256), (257, 512, 384), (300, 700, 1088),
+    (512, 520, 128), (513, 264, 1025)])
+@pytest.mark.parametrize("dtype,bias", [("f32", False), ("f16", True), ("bf16", True)])
+def test_gemm_sizes(m, n, k, dtype, bias):
+    say(f"gemm {m}x{n}x{k} {dtype} bias={bias}")
+    check_gemm(m, n, k, TYPES[dtype], bias)
+
+
+@pytest.mark.parametrize("m", [1, 6, 16, 40, 130, 300])
+@pytest.mark.parametrize("pads,leads", [((16, 32, 8), (16, 16, 8)), ((1, 0, 0), (0, 0, 0)), ((0, 3, 1), (1, 2, 1)),
+                                        ((4, 4, 2), (4, 8, 4))])
+def test_gemm_strides(m, pads, leads):
+    say(f"gemm strides m={m} {pads} {leads}")
+    check_gemm(m, 144, 512, torch.bfloat16, True, pads, leads)
+    check_gemm(m, 75, 200, torch.float32, False, pads, leads)
+
+
+@pytest.mark.parametrize("m", [1, 20, 70, 260])
+def test_gemm_extreme_codes(m):
+    """All -128 (the largest sums), at k past 65536 and at the longest."""
+    say(f"gemm extreme codes m={m}")
+    check_gemm(m, 40, 4096, torch.float32, False, codes=(-128, -128))
+    check_gemm(m, 24, 4160, torch.float32, False, codes=(-128, 127))
+    if m <= 20:
+        check_gemm(m, 24, 65600, torch.float32, False)
+        check_gemm(m, 3, 131071, torch.float32, False, codes=(-128, -128))
+
+
+def test_gemm_rows_do_not_depend_on_their_number():
+    say("gemm batch invariance")
+    a, sa, b, sb, _ = (torch.from_numpy(v).to(DEV) if v is not None else None
+                       for v in gemm_inputs(300, 200, 1024, 5, False))
+    whole = moeq8.gemm_i8(a, sa, b, sb)
+    for m in (1, 3, 16, 17, 64, 129):
+        assert torch.equal(moeq8.gemm_i8(a[:m], sa[:m], b, sb), whole[:m])
+    assert torch.equal(moeq8.gemm_i8(a, sa, b[:100], sb[:100]), whole[:, :100])
+
+
+def test_gemm_scales_not_finite_and_empty():
+    say("gemm scales")
+    a, sa, b, sb, _ = (torch.from_numpy(v).to(DEV) if v is not None else None
+                       for v in gemm_inputs(20, 40, 64, 6, False))
+    sa[3], sb[7] = float("nan"), float("inf")
+    out = moeq8.gemm_i8(a, sa, b, sb).cpu().numpy()
+    steps = ref.gemm_i8_steps(*(v.cpu().numpy() for v in (a, sa, b, sb)))
+    assert same(out, steps)
+    assert moeq8.gemm_i8(a[:0], sa[:0], b, sb).shape == (0, 40)
+    assert moeq8.gemm_i8(a, sa, b[:0], sb[:0], out_dtype=torch.bfloat16).shape == (20, 0)
+
+
+# ---- logits -----------------------------------------------------------------------
+
+def logits_inputs(rows, vocab, history, seed, biases=3, density=0.5):
+    g = np.random.default_rng(seed)
+    z = (3 * g.standard_normal((rows, vocab))).astype(np.float32)
+    lens = g.integers(max(0, history // 2), history + 1, rows)
+    ends = np.cumsum(lens)
+    tokens = np.minimum((vocab * g.random(int(ends[-1]) + 1) ** 2).astype(np.int32), vocab - 1)
+    begin = ends - lens
+    kw = dict(tokens=tokens, begin=begin, end=ends, prompt_end=begin + lens // 2,
+              repetition=(1 + 0.3 * g.random(rows)).astype(np.float32),
+              frequency=(0.5 * g.random(rows)).astype(np.float32), presence=(0.5 * g.random(rows)).astype(np.float32))
+    bias = [[(int(g.integers(0, vocab)), float(np.float32(5 * g.standard_normal()))) for _ in range(biases)]
+            for _ in range(rows)]
+    bits = g.random((rows, (vocab + 31) // 32, 32)) < density
+    mask = (bits * (1 << np.arange(32, dtype=np.int64))).sum(2).astype(np.uint32).view(np.int32)
+    return z, kw, bias, mask
+
+
+def check_logits(z, dtype, kw, bias, mask, pads=(0, 0), leads=(0, 0), inplace=False):
+    rows, vocab = z.shape
+    zt, zv = typed(z, dtype)
+    d = {}
+    for n, v in kw.items():
+        t = torch.from_numpy(np.asarray(v))
+        d[n] = (t.to(torch.int32) if n == "tokens" else t.to(torch.float32) if n in ("repetition", "frequency", "presence")
+                else t.to(torch.int64)).to(DEV)
+    if bias is not None:
+        flat = [p for row in bias for p in row]
+        d["bias_ids"] = torch.tensor([p[0] for p in flat], dtype=torch.int32, device=DEV)
+        d["bias_values"] = torch.tensor([p[1] for p in flat], dtype=torch.float32, device=DEV)
+        d["bias_offsets"] = torch.tensor(np.cumsum([0] + [len(row) for row in bias]), dtype=torch.int64, device=DEV)
+    if mask is not None:
+        d["mask"] = torch.from_numpy(mask).to(DEV)
+    zd = put(zt, pads[0], leads[0])
+    obuf, out = framed(rows, vocab, dtype, pads[1], leads[1])
+    got = moeq8.logits_process(zd, out=zd if inplace else out, **d)
+    torch.cuda.synchronize()
+    steps = ref.logits_rules(zv, np.float32, bias=bias, mask=mask, **kw)
+    want = torch.from_numpy(steps).to(dtype)
+    assert same(got.cpu().float().numpy(), want.float().numpy())
+    if not inplace:
+        assert frame_kept(obuf, rows, vocab, pads[1], leads[1])
+        assert same(zd.cpu().float().numpy(), zv)
+    return steps, zv
+
+
+def check_logits_def(steps, zv, kw, bias, mask):
+    """The fp32 steps against the definition: each operation rounds by half a
+    step of a value that is at most the sum of the magnitudes met so far."""
+    v64 = ref.logits_rules(zv, np.float64, bias=bias, mask=mask, **kw)
+    ok = np.isfinite(v64)
+    size = np.abs(zv) * 1.3 + 0.5 * (len(kw["tokens"]) + 1) + (0 if bias is None else max(
+        [sum(abs(v) for _, v in row) for row in bias] + [0]))
+    n = 4 + (0 if bias is None else max([len(row) for row in bias] + [0]))
+    assert np.array_equal(np.isneginf(steps), np.isneginf(v64))
+    assert np.all(np.abs(steps[ok] - v64[ok]) <= (n * 1.01 * ULP * size)[ok])
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,vocab,history", [(1, 1, 1), (2, 31, 0), (3, 32, 40), (2, 33, 5), (5, 1000, 700),
+                                                (2, 4095, 64), (2, 4096, 3000), (3, 4097, 100), (2, 8193, 500),
+                                                (1, 20011, 9000), (4, 32000, 600)])
+def test_logits_sizes(rows, vocab, history, dtype):
+    say(f"logits {rows}x{vocab} history {history} {dtype}")
+    z, kw, bias, mask = logits_inputs(rows, vocab, history, vocab + rows)
+    steps, zv = check_logits(z, TYPES[dtype], kw, bias, mask)
+    check_logits_def(steps, zv, kw, bias, mask)
+
+
+@pytest.mark.parametrize("drop", ["tokens", "prompt_end", "repetition", "frequency", "presence", "bias", "mask", "all"])
+def test_logits_each_rule_alone_and_left_out(drop):
+    say(f"logits without {drop}")
+    z, kw, bias, mask = logits_inputs(3, 5001, 300, 11)
+    if drop in ("tokens", "all"):
+        kw = {}
+    elif drop in kw:
+        kw = {n: v for n, v in kw.items() if n != drop}
+    check_logits(z, torch.float32, kw, None if drop in ("bias", "all") else bias,
+                 None if drop in ("mask", "all") else mask)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("pads,leads", [((0, 0), (0, 0)), ((3, 3), (1, 1)), ((1, 2), (3, 5)), ((8, 8), (8, 8))])
+def test_logits_strides_and_in_place(pads, leads, dtype):
+    say(f"logits strides {pads} {leads} {dtype}")
+    z, kw, bias, mask = logits_inputs(3, 9001, 300, 12)
+    check_logits(z, TYPES[dtype], kw, bias, mask, pads, leads)
+    check_logits(z, TYPES[dtype], kw, bias, mask, pads, leads, inplace=True)
+
+
+def test_logits_lists_shared_empty_and_out_of_range():
+    """Columns of one request share its list; lists that are empty, cross their
+    bounds or run backwards; ids outside the vocabulary; biases that repeat."""
+    say("logits lists")
+    z, kw, _, mask = logits_inputs(6, 6000, 50, 13)
+    n = len(kw["tokens"])
+    kw["tokens"][::5] = np.array([-1, 6000, -2**31, 2**31 - 1, 6001])[np.arange(len(kw["tokens"][::5])) % 5]
+    kw["begin"] = np.array([0, 0, 4, -5, n - 2, 9])
+    kw["end"] = np.array([n, n - 1, 4, 3, n + 100, 2])
+    kw["prompt_end"] = np.array([3, -7, 4, 0, n + 50, 2**40])
+    bias = [[(5, 1.5), (5, 2.0**-24), (5, -1.5)], [], [(5999, 3.0), (-1, 9.0), (6000, 9.0)], [(17, 1.0)] * 70,
+            [(0, -2.0), (4096, 1.0), (0, 0.1), (4095, 7.0)], [(i, 0.1 * i) for i in range(400)]]
+    bias = [[(t, float(np.float32(v))) for t, v in row] for row in bias]
+    check_logits(z, torch.float32, kw, bias, mask)
+    check_logits(z, torch.float32, kw, bias, None)
+
+
+def test_logits_empty_lists():
+    z = torch.randn(2, 100, device=DEV)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    at = torch.zeros(2, dtype=torch.int64, device=DEV)
+    out = moeq8.logits_process(z, tokens=none, begin=at, end=at, bias_ids=none, bias_values=none.float(),
+                               bias_offsets=torch.zeros(3, dtype=torch.int64, device=DEV))
+    assert torch.equal(out, z)
+    assert moeq8.logits_process(z[:0]).shape == (0, 100)
+
+
+def test_logits_not_finite_and_masked_out():
+    """-inf and the type's lowest value pass through, NaN and inf in masked
+    places become -inf, a row may be masked out whole."""
+    say("logits not finite")
+    for dtype in TYPES.values():
+        z, kw, bias, mask = logits_inputs(4, 3000, 400, 14)
+        z[0, ::7], z[1, ::5], z[2, ::3] = -np.inf, np.nan, np.inf
+        z[0, 1::7] = torch.finfo(dtype).min
+        mask[3] = 0
+        for m in (mask, None):
+            check_logits(z, dtype, kw, bias, m)
+    out = moeq8.logits_process(torch.full((1, 70), float("nan"), device=DEV),
+                               mask=torch.zeros(1, 3, dtype=torch.int32, device=DEV))
+    assert bool(torch.isneginf(out).all())
+
+
+def test_logits_counts_past_sixteen_bits():
+    say("logits long counts")
+    tokens = np.concatenate([np.full(70000, 3), np.full(40, 2)]).astype(np.int32)
+    kw = dict(tokens=tokens, begin=np.array([0, 65000]), end=np.array([len(tokens)] * 2), prompt_end=np.array([10, 0]),
+              frequency=np.array([0.001, 0.5], np.float32))
+    check_logits(np.ones((2, 10), np.float32), torch.float32, kw, None, None)
+
+
+# ---- all of them: refusals, streams, graphs ------------------------------------------
+
+def test_refusals():
+    say("refusals")
+    x, w = torch.randn(4, 64, device=DEV), torch.ones(64, device=DEV)
+    c, s4 = torch.zeros(4, 64, dtype=torch.int8, device=DEV), torch.ones(4, device=DEV)
+    z, tok = torch.zeros(2, 64, device=DEV), torch.zeros(5, dtype=torch.int32, device=DEV)
+    at = torch.zeros(2, dtype=torch.int64, device=DEV)
+    for err, f in [
+            (ValueError, lambda: moeq8.rms_norm_q8(x.cpu(), w)),
+            (ValueError, lambda: moeq8.rms_norm_q8(x, w.cpu())),
+            (TypeError, lambda: moeq8.rms_norm_q8(x.double(), w)),
+            (TypeError, lambda: moeq8.rms_norm_q8(x, w.half())),
+            (ValueError, lambda: moeq8.rms_norm_q8(x, w[:32])),
+            (ValueError, lambda: moeq8.rms_norm_q8(x.t(), w[:4])),
+            (ValueError, lambda: moeq8.rms_norm_q8(x, w, fmt="q4")),
+            (ValueError, lambda: moeq8.rms_norm_q8(x[:, :40], w[:40], fmt="both")),
+            (ValueError, lambda: moeq8.rms_norm_q8(x, w, residual=x[:2])),
+            (ValueError, lambda: moeq8.rms_norm_q8(x, w, residual_out=x)),
+            (ValueError, lambda: moeq8.rms_norm_q8(x, w, q=c[:, :32])),
+            (moeq8.MoeQ8Error, lambda: moeq8.rms_norm_q8(x, w, eps=-1.0)),
+            (moeq8.MoeQ8Error, lambda: moeq8.rms_norm_q8(x[:1].expand(4, 64), w)),
+            (ValueError, lambda: moeq8.i8_quantize_rows(x[0])),
+            (TypeError, lambda: moeq8.i8_quantize_rows(c)),
+            (ValueError, lambda: moeq8.i8_quantize_rows(x, scale=s4[:2])),
+            (TypeError, lambda: moeq8.gemm_i8(c.to(torch.uint8), s4, c, s4)),
+            (ValueError, lambda: moeq8.gemm_i8(c, s4, c[:, :32], s4)),
+            (ValueError, lambda: moeq8.gemm_i8(c, s4[:2], c, s4)),
+            (ValueError, lambda: moeq8.gemm_i8(c, s4, c, s4, bias=s4[:3])),
+            (TypeError, lambda: moeq8.gemm_i8(c, s4, c, s4, out_dtype=torch.int32)),
+            (ValueError, lambda: moeq8.gemm_i8(c, s4, c, s4, out=x)),
+            (ValueError, lambda: moeq8.logits_process(z, tokens=tok)),
+            (ValueError, lambda: moeq8.logits_process(z, frequency=s4[:2])),
+            (TypeError, lambda: moeq8.logits_process(z, tokens=tok.long(), begin=at, end=at)),
+            (ValueError, lambda: moeq8.logits_process(z, tokens=tok, begin=at[:1], end=at)),
+            (ValueError, lambda: moeq8.logits_process(z, bias_ids=tok)),
+            (ValueError, lambda: moeq8.logits_process(z, mask=tok[:4].view(2, 2)[:, :1])),
+            (TypeError, lambda: moeq8.logits_process(z, out=z.half()))]:
+        with pytest.raises(err):
+            f()
+    torch.cuda.synchronize()
+
+
+def _chain(x, res, w, b, sb, tokens, at, end, out):
+    """The four operators in turn, on buffers made once."""
+    n = moeq8.rms_norm_q8(x, w, residual=res, fmt="both", residual_out=out["res"], q=out["q"], scale=out["scale"],
+                          xq=out["xq"])
+    moeq8.gemm_i8(n.q, n.scale, b, sb, out=out["z"])
+    moeq8.logits_process(out["z"], tokens=tokens, begin=at, end=end, frequency=out["f"], out=out["z2"])
+    moeq8.i8_quantize_rows(out["z2"], q=out["zq"], scale=out["zs"])
+
+
+def test_graph_replays_and_streams_equal_eager():
+    say("operators in a graph")
+    m, k, n = 5, 1024, 2000
+    new = lambda *s, dtype=torch.float32: torch.zeros(s, dtype=dtype, device=DEV)
+    out = dict(res=new(m, k), q=new(m, k, dtype=torch.int8), scale=new(m), xq=new(m, k // 32 * 36, dtype=torch.uint8),
+               z=new(m, n), z2=new(m, n), f=new(m) + 0.5, zq=new(m, n, dtype=torch.int8), zs=new(m))
+    w, b = torch.ones(k, device=DEV), torch.randint(-127, 128, (n, k), dtype=torch.int8, device=DEV)
+    sb = torch.rand(n, device=DEV) * 1e-3
+    tokens = torch.randint(0, n, (400,), dtype=torch.int32, device=DEV)
+    at, end = torch.arange(m, device=DEV) * 10, torch.arange(m, device=DEV) * 50 + 100
+    x, res = torch.randn(m, k, device=DEV), torch.randn(m, k, device=DEV)
+    args = (x, res, w, b, sb, tokens, at, end, out)
+    _chain(*args)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _chain(*args)
+    side = torch.cuda.Stream()
+    for i in range(4):
+        x.copy_(torch.randn(m, k, device=DEV))
+        tokens.copy_(torch.randint(0, n, (400,), dtype=torch.int32, device=DEV))
+        _chain(*args)
+        want = {name: t.clone() for name, t in out.items()}
+        for how in ("replay", "side"):
+            for name, t in out.items():
+                if name != "f":
+                    t.zero_()
+            torch.cuda.synchronize()
+            if how == "replay":
+                g.replay()
+            else:
+                with torch.cuda.stream(side):
+                    _chain(*args)
+            torch.cuda.synchronize()
+            for name, t in out.items():
+                assert torch.equal(t, want[name]), (i, how, name)
