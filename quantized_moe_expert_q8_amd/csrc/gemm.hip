@@ -41,6 +41,7 @@
 //            matrix; both share every activation fragment; SwiGLU-DS4 epilogue.
 //   down:    a wave owns 32 consecutive rows (two 16-row fragments).
 #include "moeq8_device.hpp"
+#include "moeq8_lds.hpp"
 #include "moeq8_host.hpp"
 
 #include <atomic>
@@ -501,27 +502,6 @@ static_assert(S_WG_PER_CU * S_LDS <= 160 * 1024, "LDS of a CU");
 // to S_TICKET_SLOTS calls may be in flight on one device at once.
 constexpr int S_TICKET_SLOTS = 256;
 __device__ uint32_t g_tickets[S_TICKET_SLOTS * XCDS * 32];
-
-// Workgroup barrier over LDS only: waits for this wave's LDS operations, not
-// for its global loads, so a step's loads stay in flight across it (the
-// barrier of __syncthreads also waits for every outstanding global load).
-__device__ __forceinline__ void lds_barrier() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-
-// One wave-wide direct load of 16 bytes a lane from global memory into LDS:
-// lane i writes LDS bytes [lds + 16 i, lds + 16 i + 16).  `lds` is the
-// wave-uniform LDS byte address (the low 32 bits of a shared pointer).  The
-// load has no register results; its completion is tracked by vmcnt alone,
-// which the caller waits for before any wave reads the bytes (issued this
-// way the compiler adds no wait of its own before unrelated LDS reads).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"   // m0 is set here and used by nothing else
-__device__ __forceinline__ void load_lds16(const void* src, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 :: "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
-}
-#pragma clang diagnostic pop
 
 __device__ __forceinline__ void wait_vm0() { __builtin_amdgcn_s_waitcnt(0x0F70); }   // vmcnt(0) alone
 

@@ -1,0 +1,31 @@
+// LDS building blocks of the staged products: a barrier that leaves global
+// loads in flight, and direct global-to-LDS loads.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moeq8 {
+
+// Workgroup barrier over LDS only: waits for this wave's LDS operations, not
+// for its global loads, so a step's loads stay in flight across it (the
+// barrier of __syncthreads also waits for every outstanding global load).
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+// One wave-wide direct load of 16 bytes a lane from global memory into LDS:
+// lane i writes LDS bytes [lds + 16 i, lds + 16 i + 16).  `lds` is the
+// wave-uniform LDS byte address (the low 32 bits of a shared pointer).  The
+// load has no register results; its completion is tracked by vmcnt alone,
+// which the caller waits for before any wave reads the bytes (issued this
+// way the compiler adds no wait of its own before unrelated LDS reads).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"   // m0 is set here and used by nothing else
+__device__ __forceinline__ void load_lds16(const void* src, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :: "v"(src), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+}  // namespace moeq8
