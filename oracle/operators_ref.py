@@ -70,8 +70,8 @@ def rms_norm_def(x, w, eps, residual=None):
 
 
 def gemm_i8_sums(a, b):
-    """Exact integer sums [m, n]."""
-    return np.asarray(a, np.int64) @ np.asarray(b, np.int64).T
+    """Exact integer sums [m, n] (a sum of k <= 131071 products is exact in 64-bit floats)."""
+    return (np.asarray(a, np.float64) @ np.asarray(b, np.float64).T).astype(np.int64)
 
 
 def gemm_i8_steps(a, sa, b, sb, bias=None):

@@ -28,4 +28,20 @@ __device__ __forceinline__ void load_lds16(const void* src, uint32_t lds) {
 }
 #pragma clang diagnostic pop
 
+// load_lds16 from a wave-uniform base and a byte offset of each lane: no vector
+// address arithmetic a load.  The base may come from vector instructions
+// (v_readfirstlane), and a vector memory instruction reads an SGPR that such a
+// one wrote correctly only 5 wait states later; inside asm nothing inserts
+// them.  A scalar move waits by itself, so the load takes its base from one.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+__device__ __forceinline__ void load_lds16_at(const void* base, uint32_t offset, uint32_t lds) {
+    const uint64_t b = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)((uint64_t)base >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(uint64_t)base);
+    uint64_t at;
+    asm volatile("s_mov_b32 m0, %3\n\ts_mov_b64 %0, %2\n\tglobal_load_lds_dwordx4 %1, %0"
+                 : "=&s"(at) : "v"(offset), "s"(b), "s"(__builtin_amdgcn_readfirstlane(lds)) : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
 }  // namespace moeq8

@@ -25,8 +25,8 @@ __device__ __forceinline__ void from_f32(bf16_t& o, float v) {
 // N consecutive elements at any address their type allows, as dword vectors.
 // Rows of an odd length start off 16 bytes; gfx950 global memory takes such
 // vectors whole, so one instruction serves every row.
-typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1)));
-typedef uint32_t u32x2b __attribute__((ext_vector_type(2), aligned(1)));
+typedef uint32_t u32x4b __attribute__((ext_vector_type(4), aligned(1), may_alias));
+typedef uint32_t u32x2b __attribute__((ext_vector_type(2), aligned(1), may_alias));
 
 template <typename T, int N>
 __device__ __forceinline__ void load_vec(T (&v)[N], const T* p) {

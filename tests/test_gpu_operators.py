@@ -269,6 +269,20 @@ def test_gemm_sizes(m, n, k, dtype, bias):
     check_gemm(m, n, k, TYPES[dtype], bias)
 
 
+@pytest.mark.parametrize("m,n,k,dtype", [
+    # tiles of 32 x 64, 64 x 64, 128 x 128 (four stages, two) and 256 x 256, with
+    # aligned rows and with rows that end 1 to 15 bytes into a stage
+    (512, 520, 144, "f32"), (500, 700, 1031, "bf16"), (600, 2000, 1040, "f16"), (600, 2000, 1029, "f32"),
+    (1500, 1500, 1312, "bf16"), (1500, 1500, 1295, "f32"), (2500, 2300, 400, "f32"), (2500, 2300, 393, "f16"),
+    (4090, 4080, 1040, "bf16"), (4080, 4095, 1025, "f32"), (4096, 4096, 2048, "f32"),
+    # few tokens, with k split over 16 waves in one chunk and in more, and over none
+    (16, 300, 8192, "bf16"), (3, 500, 9001, "f32"), (5, 33000, 256, "f32"), (16, 33001, 200, "bf16"),
+    (2, 17000, 500, "f16"), (1, 33000, 20, "f32")])
+def test_gemm_tiles(m, n, k, dtype):
+    say(f"gemm tiles {m}x{n}x{k} {dtype}")
+    check_gemm(m, n, k, TYPES[dtype], k % 2 == 0)
+
+
 @pytest.mark.parametrize("m", [1, 6, 16, 40, 130, 300])
 @pytest.mark.parametrize("pads,leads", [((16, 32, 8), (16, 16, 8)), ((1, 0, 0), (0, 0, 0)), ((0, 3, 1), (1, 2, 1)),
                                         ((4, 4, 2), (4, 8, 4))])
