@@ -595,7 +595,7 @@ int gemm_i8(const int8_t* a, int64_t a_row_stride, const float* sa, const int8_t
  *   mask         int32 [n_rows][mask_row_stride] or NULL
  * Ids outside [0, vocab) are skipped; offsets are taken within their lists.
  * Values that are not finite follow IEEE arithmetic; a masked token is -inf
- * whatever its logit.  n_tokens < 2^30, vocab < 2^31. */
+ * whatever its logit.  n_tokens, n_bias and vocab stay below 2^30. */
 int logits_process(const void* logits, int64_t logits_row_stride, int32_t dtype, int64_t n_rows, int64_t vocab,
                    const int32_t* tokens, int64_t n_tokens, const int64_t* begin, const int64_t* end,
                    const int64_t* prompt_end, const float* repetition, const float* frequency,

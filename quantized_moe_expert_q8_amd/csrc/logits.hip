@@ -9,11 +9,15 @@
 //
 // in that order, in fp32 with each operation rounded, the output rounded once.
 //
-// A block takes one tile of one row's vocabulary.  It counts the row's tokens
-// that fall into its tile in LDS (integer atomics, whose order does not
-// matter), so nothing of vocabulary size is kept in memory: the list is read
-// again by each tile of the row, from L2, which costs far less than the
-// logits as long as it is not much longer than a tile.
+// A block takes one tile of one row's vocabulary.  Its logits, mask words, the
+// first tokens and biases of the row are all loaded before anything waits.  It
+// then marks the row's tokens that fall into the tile in LDS, a bit and a count
+// each (integer atomics, whose order does not matter and whose results no one
+// waits for).  The seen and the biased tokens, few of a tile, get their values
+// one by one in the tile's copy in LDS; the tile is written with the mask
+// applied on the way.  Nothing of vocabulary size is kept in memory: the row's
+// list is read again by each of its tiles, from L2.
+#include "moeq8_lds.hpp"
 #include "moeq8_types.hpp"
 #include "moeq8_host.hpp"
 
@@ -38,81 +42,244 @@ struct LogitsArgs {
     const int32_t* mask; int64_t mask_stride;     // null: no mask
 };
 
-constexpr int THREADS = 256;
-constexpr int TILE = 4096;
-// A tile's word: how often the token was written, and whether it was seen at
-// all or has a bias.
-constexpr uint32_t SEEN = 1u << 31, BIASED = 1u << 30, COUNT = BIASED - 1;
+constexpr int AHEAD = 4;                           // loads of 4 tokens a thread has in flight
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
     return v < lo ? lo : (v > hi ? hi : v);
 }
 
-template <typename T>
-__global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a) {
-    __shared__ uint32_t word[TILE];
-    __shared__ float bias[TILE];
+// VEC elements from 16 bytes at p, of which [from, to) exist.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_part(T (&v)[VEC], const T* p, int from, int to) {
+    if (from <= 0 && to >= VEC) {
+        load_vec(v, p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (j >= from && j < to) v[j] = p[j];
+    }
+}
+
+// Element j stays where bit j is set and becomes -inf elsewhere.
+template <int VEC>
+__device__ __forceinline__ void keep_bits(float (&v)[VEC], uint32_t bits) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v[j] = bits >> j & 1 ? v[j] : -__builtin_inff();
+}
+template <typename H, int VEC>
+__device__ __forceinline__ void keep_bits(H (&v)[VEC], uint32_t bits) {
+    H inf;
+    from_f32(inf, -__builtin_inff());
+#pragma unroll
+    for (int j = 0; j < VEC; j += 2) {             // two elements a dword
+        const uint32_t x = (uint32_t)v[j].bits | (uint32_t)v[j + 1].bits << 16;
+        const uint32_t keep = ((uint32_t)__builtin_amdgcn_sbfe((int)bits, j, 1) & 0xffffu) |
+                              ((uint32_t)__builtin_amdgcn_sbfe((int)bits, j + 1, 1) & 0xffff0000u);
+        const uint32_t y = (x & keep) | (((uint32_t)inf.bits | (uint32_t)inf.bits << 16) & ~keep);
+        v[j].bits = (uint16_t)y;
+        v[j + 1].bits = (uint16_t)(y >> 16);
+    }
+}
+
+template <typename T, int THREADS, int TILE>
+__global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a, uint32_t rows, uint32_t tiles) {
+    constexpr int VEC = 16 / sizeof(T), NV = TILE / VEC / THREADS;
+    static_assert(NV * VEC * THREADS == TILE, "whole vectors");
+    __shared__ __attribute__((aligned(16))) T tile[TILE];
+    __shared__ __attribute__((aligned(16))) uint32_t count[TILE / 2];   // written tokens: 16 bits each, or 32 of half a tile
+    __shared__ uint32_t seen[TILE / 32], biased[TILE / 32];         // a bit each token
     __shared__ int repeated;                       // a token has more than one bias
-    const int64_t tiles = (a.vocab + TILE - 1) / TILE;
-    const int64_t r = blockIdx.x / tiles, v0 = blockIdx.x % tiles * TILE;
-    const int size = (int)(a.vocab - v0 < TILE ? a.vocab - v0 : TILE);
-    for (int i = threadIdx.x; i < TILE; i += THREADS) word[i] = 0u;
-    if (threadIdx.x == 0) repeated = 0;
-    __syncthreads();
+    // All rows' first tiles come first: where frequent tokens have low ids, those
+    // take longest, and the last rows' would be the last to end.
+    uint32_t r = blockIdx.x, tile_no = 0;
+    if (r >= rows) {
+        const uint32_t rest = r - rows;
+        r = rest / (tiles - 1);
+        tile_no = 1 + rest - r * (tiles - 1);
+    }
+    const T* z = (const T*)a.z + r * a.z_stride;
+    // the tile begins where the row's 16-byte units do: v0 < 0 in the first one
+    // of a row that starts inside a unit
+    const int v0 = (int)(tile_no * TILE) - (int)(((uintptr_t)z & 15) / sizeof(T)), vocab = (int)a.vocab;
+    if (v0 >= vocab) return;
+    const uint32_t low = v0 < 0 ? (uint32_t)-v0 : 0u, high = (uint32_t)(vocab - v0 < TILE ? vocab - v0 : TILE);
+    const int tid = threadIdx.x;
+
+    T held[NV][VEC];
+    uint32_t bits[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int at = (n * THREADS + tid) * VEC;
+        load_part(held[n], z + v0 + at, (int)low - at, (int)high - at);
+    }
+    const bool any = a.tokens || a.bias_ids;
+    int64_t b = 0, lo = 0;
+    uint32_t length = 0, written = 0, biases = 0;  // written: the first position that counts
     float rep = 1.0f, freq = 0.0f, pres = 0.0f;
     if (a.tokens) {
-        const int64_t b = clamp64(a.begin[r], 0, a.n_tokens), e = clamp64(a.end[r], b, a.n_tokens);
-        const int64_t p = a.prompt_end ? clamp64(a.prompt_end[r], b, e) : b;
+        b = clamp64(a.begin[r], 0, a.n_tokens);
+        length = (uint32_t)(clamp64(a.end[r], b, a.n_tokens) - b);
+        if (a.prompt_end) written = (uint32_t)(clamp64(a.prompt_end[r], b, b + length) - b);
         if (a.repetition) rep = a.repetition[r];
         if (a.frequency) freq = a.frequency[r];
         if (a.presence) pres = a.presence[r];
-        for (int64_t i = b + threadIdx.x; i < e; i += THREADS) {
-            const int64_t at = (int64_t)a.tokens[i] - v0;
-            if (at >= 0 && at < size) {
-                atomicOr(&word[at], SEEN);
-                if (i >= p) atomicAdd(&word[at], 1u);
-            }
-        }
     }
-    int64_t lo = 0, hi = 0;
     if (a.bias_ids) {
         lo = clamp64(a.bias_offsets[r], 0, a.n_bias);
-        hi = clamp64(a.bias_offsets[r + 1], lo, a.n_bias);
-        for (int64_t i = lo + threadIdx.x; i < hi; i += THREADS) {
-            const int64_t at = (int64_t)a.bias_ids[i] - v0;
-            if (at >= 0 && at < size) {
-                if (atomicOr(&word[at], BIASED) & BIASED) repeated = 1;
-                bias[at] = a.bias_values[i];
-            }
+        biases = (uint32_t)(clamp64(a.bias_offsets[r + 1], lo, a.n_bias) - lo);
+    }
+    if (a.mask) {
+        const int32_t* mask = a.mask + r * a.mask_stride;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {             // the vector's words: two, or one twice
+            const int v = v0 + (n * THREADS + tid) * VEC;
+            const int first = v < 0 ? 0 : (v < vocab ? v : vocab - 1), last = v + VEC <= vocab ? v + VEC - 1 : vocab - 1;
+            const uint32_t b0 = (uint32_t)mask[first >> 5], b1 = (uint32_t)mask[last >> 5];
+            bits[n] = __builtin_amdgcn_alignbit(b1, b0, (uint32_t)first & 31) << (v < 0 ? -v : 0);
         }
     }
-    __syncthreads();
-    const T* z = (const T*)a.z + r * a.z_stride + v0;
+    const int32_t* tokens = a.tokens + b;
+    const int32_t* bias_ids = a.bias_ids + lo;
+    const float* bias_values = a.bias_values + lo;
+
+    if (any) {
+        // the first tokens and the first bias of this thread
+        u32x4 token[AHEAD];
+        auto load_tokens = [&](uint32_t i) {
+#pragma unroll
+            for (int n = 0; n < AHEAD; ++n)
+                if (i + n * THREADS * 4 + 4 <= length) token[n] = *reinterpret_cast<const u32x4*>(tokens + i + n * THREADS * 4);
+        };
+        load_tokens(tid * 4);
+        int32_t bias_id = -1;
+        float bias_value = 0.0f;
+        if (tid < biases) {
+            bias_id = bias_ids[tid];
+            bias_value = bias_values[tid];
+        }
+        // its own part of the tile, from registers
+#pragma unroll
+        for (int n = 0; n < NV; ++n) store_vec(tile + (n * THREADS + tid) * VEC, held[n]);
+        // A count of 16 bits holds a list of 65535; a longer one is taken in two
+        // halves of the tile, with counts of 32 bits.
+        const bool wide = length - written > 65535u;
+        for (uint32_t from = low, to; from < high; from = to) {
+            to = wide && from < TILE / 2 && high > TILE / 2 ? TILE / 2 : high;
+#pragma unroll
+            for (int n = tid; n < TILE / 8; n += THREADS) reinterpret_cast<uint4*>(count)[n] = uint4{0u, 0u, 0u, 0u};
+            for (int n = tid; n < TILE / 32; n += THREADS) seen[n] = biased[n] = 0u;
+            if (tid == 0) repeated = 0;
+            lds_barrier();
+            // position of a token in this part of the tile, or one past it
+            // (vocab < 2^30: no wrap reaches back into the tile)
+            auto place = [&](int32_t token) {
+                const uint32_t at = (uint32_t)token - (uint32_t)v0;
+                return at >= from && at < to ? at : (uint32_t)TILE;
+            };
+            auto count_of = [&](uint32_t at) {
+                return wide ? count[at & (TILE / 2 - 1)] : count[at >> 1] >> (16 * (at & 1)) & 0xffffu;
+            };
+            auto meet = [&](uint32_t i, int32_t token) {
+                const uint32_t at = place(token), bit = 1u << (at & 31);
+                if (at == TILE) return;
+                atomicOr(&seen[at >> 5], bit);
+                if (i >= written) {
+                    if (wide) atomicAdd(&count[at & (TILE / 2 - 1)], 1u);
+                    else atomicAdd(&count[at >> 1], 1u << (16 * (at & 1)));
+                }
+            };
+            for (uint32_t i = tid * 4; i < length; i += THREADS * 4 * AHEAD) {
+                if (i != tid * 4 || from != low) load_tokens(i);
+#pragma unroll
+                for (int n = 0; n < AHEAD; ++n) {
+                    const uint32_t at = i + n * THREADS * 4;
+                    if (at + 4 <= length) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) meet(at + j, (int32_t)token[n][j]);
+                    } else {
+                        for (uint32_t j = at; j < length; ++j) meet(j, tokens[j]);
+                    }
+                }
+            }
+            for (uint32_t i = tid; i < biases; i += THREADS) {
+                const uint32_t at = place(i == tid ? bias_id : bias_ids[i]), bit = 1u << (at & 31);
+                if (at < TILE && (atomicOr(&biased[at >> 5], bit) & bit)) repeated = 1;
+            }
+            lds_barrier();
+            auto penalised = [&](uint32_t at) {
+                const uint32_t n = count_of(at);
+                float v = to_f32(tile[at]);
+                v = v > 0.0f ? v / rep : v * rep;
+                return n ? v - ((float)n * freq + pres) : v;
+            };
+            // the seen tokens without a bias, then the biased ones: no token twice
+            constexpr int FIELD = TILE / THREADS;  // bits of a thread; most threads have none or one set
+            const uint32_t first = tid * FIELD;
+            uint32_t left = (seen[first >> 5] & ~biased[first >> 5]) >> (first & 31) & ((2u << (FIELD - 1)) - 1);
+            while (left) {
+                const uint32_t at = first + __builtin_ctz(left);
+                left &= left - 1;
+                from_f32(tile[at], penalised(at));
+            }
+            if (biases) {
+                const bool again = repeated;
+                if (again) lds_barrier();          // the bits are cleared below
+                for (uint32_t i = tid; i < biases; i += THREADS) {
+                    const int32_t token = i == tid ? bias_id : bias_ids[i];
+                    const uint32_t at = place(token), bit = 1u << (at & 31);
+                    if (at == TILE) continue;
+                    if (again && !(atomicAnd(&biased[at >> 5], ~bit) & bit)) continue;   // one thread a token
+                    float v = seen[at >> 5] & bit ? penalised(at) : to_f32(tile[at]);
+                    if (!again) {
+                        v += i == tid ? bias_value : bias_values[i];
+                    } else {                       // all of the token's, in the list's order
+                        for (uint32_t j = 0; j < biases; ++j)
+                            if (bias_ids[j] == token) v += bias_values[j];
+                    }
+                    from_f32(tile[at], v);
+                }
+            }
+            lds_barrier();
+        }
+#pragma unroll
+        for (int n = 0; n < NV; ++n) load_vec(held[n], tile + (n * THREADS + tid) * VEC);
+    }
+
     T* out = (T*)a.out + r * a.out_stride + v0;
-    for (int i = threadIdx.x; i < size; i += THREADS) {
-        float v = to_f32(z[i]);
-        const uint32_t w = word[i];
-        if (w & SEEN) v = v > 0.0f ? v / rep : v * rep;
-        if (w & COUNT) v = v - ((float)(w & COUNT) * freq + pres);
-        if (w & BIASED) {
-            if (!repeated) {
-                v += bias[i];
-            } else {                               // every bias of the token, in the list's order
-                for (int64_t j = lo; j < hi; ++j)
-                    if (a.bias_ids[j] == v0 + i) v += a.bias_values[j];
-            }
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int at = (n * THREADS + tid) * VEC;
+        if (a.mask) keep_bits(held[n], bits[n]);
+        if (at >= (int)low && at + VEC <= (int)high) {
+            store_vec(out + at, held[n]);
+        } else {                                   // the row's ends
+#pragma unroll
+            for (int j = 0; j < VEC; ++j)
+                if (at + j >= (int)low && at + j < (int)high) out[at + j] = held[n][j];
         }
-        if (a.mask && !((a.mask[r * a.mask_stride + ((v0 + i) >> 5)] >> ((v0 + i) & 31)) & 1)) v = -__builtin_inff();
-        from_f32(out[i], v);
     }
+}
+
+template <typename T, int THREADS, int TILE>
+int launch_form(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
+    const int64_t tiles = (a.vocab + 16 / (int64_t)sizeof(T) - 1 + TILE - 1) / TILE;     // with a shifted first tile
+    if (rows > 0x7fffffff / tiles) return MOEQ8_EUNSUPPORTED;
+    hipLaunchKernelGGL((k_logits<T, THREADS, TILE>), dim3((uint32_t)(rows * tiles)), dim3(THREADS), 0, stream, a, (uint32_t)rows,
+                       (uint32_t)tiles);
+    return check_launch();
 }
 
 template <typename T>
 int launch_logits(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
-    const int64_t tiles = (a.vocab + TILE - 1) / TILE;
-    if (rows > 0x7fffffff / tiles) return MOEQ8_EUNSUPPORTED;
-    hipLaunchKernelGGL(k_logits<T>, dim3((uint32_t)(rows * tiles)), dim3(THREADS), 0, stream, a);
-    return check_launch();
+    // Many tiles: small blocks, 8 on a CU, hide each other's waits (256 x 131072
+    // bf16 with 2048 tokens a row: 37 us; in blocks of 512 55).  Few: what counts
+    // is how soon one block is done, so a thread takes one vector, and blocks of
+    // long lists are larger (5 x 131072 f32 with 8192 tokens a row: 256 threads
+    // 12.7, 512 7.5, 1024 7.0 us; 91 x 21061 with 688: 10.7, 8.5, 10.4).
+    constexpr int VEC = 16 / sizeof(T);
+    if (a.vocab / 4096 * rows > 2048) return launch_form<T, 256, 4096>(a, rows, stream);
+    if (a.n_tokens / rows < 1024) return launch_form<T, 512, 512 * VEC>(a, rows, stream);
+    return launch_form<T, 1024, 1024 * VEC>(a, rows, stream);
 }
 
 }  // namespace
@@ -133,7 +300,7 @@ extern "C" int logits_process(const void* logits, int64_t logits_row_stride, int
         return MOEQ8_EINVAL;
     if (!bias_ids != !bias_values || !bias_ids != !bias_offsets) return MOEQ8_EINVAL;
     if (mask && mask_row_stride < (vocab + 31) / 32) return MOEQ8_EINVAL;
-    if (vocab > 0x7fffffff || n_tokens >= (1 << 30)) return MOEQ8_EUNSUPPORTED;
+    if (vocab >= (1 << 30) || n_tokens >= (1 << 30) || n_bias >= (1 << 30)) return MOEQ8_EUNSUPPORTED;
     const int es = dtype_bytes(dtype);
     if (((uintptr_t)logits | (uintptr_t)out) & (uintptr_t)(es - 1)) return MOEQ8_EALIGN;
     if (((uintptr_t)tokens | (uintptr_t)repetition | (uintptr_t)frequency | (uintptr_t)presence | (uintptr_t)bias_ids |

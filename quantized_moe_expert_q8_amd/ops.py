@@ -788,30 +788,35 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _matrix(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
-    """Checks a device matrix [rows, cols] of rows whose elements lie together;
-    returns its row stride."""
+def _refuse(t, name: str, dtype, dev: int, shape: tuple):
     if not isinstance(t, torch.Tensor) or t.get_device() != dev:
         raise ValueError(f"{name} must be a device tensor, on the same device as the others")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name} must be [{rows}, {cols}], got {tuple(t.shape)}")
-    stride, inner = t.stride()
-    if inner != 1 and cols > 1:
-        raise ValueError(f"{name} must have unit inner stride")
-    return stride if rows > 1 else cols
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must have unit inner stride")
+
+
+# The checks below run on every call of a decode step, whose kernels take a few
+# microseconds: one condition where all is well, the reason found afterwards.
+
+def _matrix(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
+    """Checks a device matrix [rows, cols] of rows whose elements lie together;
+    returns its row stride."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
+        stride, inner = t.stride()
+        if inner == 1 or cols <= 1:
+            return stride if rows > 1 else cols
+    _refuse(t, name, dtype, dev, (rows, cols))
 
 
 def _vector(t: torch.Tensor, name: str, dtype, dev: int, n: int) -> int:
     """Checks a contiguous device vector of n elements; returns its address."""
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a device tensor, on the same device as the others")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be contiguous [{n}], got {tuple(t.shape)}")
-    return t.data_ptr()
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == (n,)
+            and (n <= 1 or t.stride(0) == 1)):
+        return t.data_ptr()
+    _refuse(t, name, dtype, dev, (n,))
 
 
 def _on(t: torch.Tensor, name: str) -> int:
@@ -819,11 +824,17 @@ def _on(t: torch.Tensor, name: str) -> int:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be 2-D, got {list(t.shape)}")
     return t.get_device()
 
 
+# the current stream's handle without a Stream object, where torch has it (1 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current_stream(dev: int) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(dev)
     return torch.cuda.current_stream(dev).cuda_stream
 
 
