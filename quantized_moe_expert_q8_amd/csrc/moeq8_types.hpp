@@ -38,14 +38,18 @@ __device__ __forceinline__ void load_vec(T (&v)[N], const T* p) {
     for (int i = 0; i < N; ++i) v[i] = t.e[i];
 }
 
-template <typename T, int N>
+// LATER: nontemporal, for what is not read again soon.
+template <bool LATER = false, typename T, int N>
 __device__ __forceinline__ void store_vec(T* p, const T (&v)[N]) {
     static_assert(sizeof(T) * N % 16 == 0, "whole 16-byte vectors");
     union { u32x4b u[sizeof(T) * N / 16]; T e[N]; } t;
 #pragma unroll
     for (int i = 0; i < N; ++i) t.e[i] = v[i];
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) * N / 16); ++i) reinterpret_cast<u32x4b*>(p)[i] = t.u[i];
+    for (int i = 0; i < (int)(sizeof(T) * N / 16); ++i) {
+        if constexpr (LATER) __builtin_nontemporal_store(t.u[i], reinterpret_cast<u32x4b*>(p) + i);
+        else reinterpret_cast<u32x4b*>(p)[i] = t.u[i];
+    }
 }
 
 }  // namespace moeq8

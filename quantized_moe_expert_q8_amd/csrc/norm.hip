@@ -10,7 +10,9 @@
 // y / d, and with a sum in 32 bits its order would move codes that lie next to
 // a half.  One pass over the data: a thread keeps its 8-value vectors of s in
 // registers between the two row reductions, so x and the residual are read
-// once.  What bounds it is the memory traffic, for few rows the launch.
+// once, and the weights are loaded with them.  What bounds it is the memory
+// traffic: 8192 x 8192 in bf16 with a residual takes 93 us, 5.1 TB/s, the rate
+// of a large copy.  For few rows it is the launch: 4 us for one of 4096.
 #include "moeq8_types.hpp"
 #include "moeq8_host.hpp"
 
@@ -78,26 +80,36 @@ __device__ __forceinline__ uint2 codes8(const float (&y)[VEC], float d, int& sum
     return o;
 }
 
+// Vector of n valid values at p, the others zero.
 template <typename T>
-__device__ __forceinline__ void load8(float (&v)[VEC], const T* p, int n) {
-    T t[VEC];
+__device__ __forceinline__ void load_raw(T (&v)[VEC], const T* p, int n) {
     if (n >= VEC) {
-        load_vec(t, p);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = to_f32(t[i]);
+        load_vec(v, p);
     } else {
+        T zero;
+        from_f32(zero, 0.0f);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+        for (int i = 0; i < VEC; ++i) v[i] = i < n ? p[i] : zero;
     }
 }
 
+template <typename T>
+__device__ __forceinline__ void load8(float (&v)[VEC], const T* p, int n) {
+    T t[VEC];
+    load_raw(t, p, n);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = to_f32(t[i]);
+}
+
+// The residual, which the next block reads: nontemporal (8192 x 8192 in bf16
+// 96 and 100 us, 1024 x 4096 10.3 and 12.3).
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&v)[VEC], int n) {
     T t[VEC];
 #pragma unroll
     for (int i = 0; i < VEC; ++i) from_f32(t[i], v[i]);
     if (n >= VEC) {
-        store_vec(p, t);
+        store_vec<true>(p, t);
     } else {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
@@ -157,14 +169,15 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, const float (&y)[
 // TPR threads hold a row, NV vectors each (vector i of a thread is vector
 // i * TPR + thread of the row, so a wave's loads are contiguous).
 template <typename T, bool NORM, int TPR, int NV>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_q8(NormArgs a) {
+__global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
     __shared__ double lds_sum[TPR / 64];
     __shared__ float lds_max[TPR / 64];
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr int RPB = TPR == 64 ? 4 : 1;
     const int t = threadIdx.x & (TPR - 1);
     const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
     if (r >= a.rows) return;                       // whole waves; with barriers a block is one row
     float v[NV][VEC];
+    T wt[NORM ? NV : 1][VEC];
     double sq = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -172,6 +185,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_q8(NormArgs a) {
         const int64_t left = a.k - at * VEC;
         const int n = left < VEC ? (left < 0 ? 0 : (int)left) : VEC;
         load_sum<T>(v[i], a, r, n > 0 ? at : 0, n);
+        if constexpr (NORM) load_raw(wt[i], (const T*)a.w + (n > 0 ? at * VEC : 0), n);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -190,13 +204,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_q8(NormArgs a) {
         const float inv = inv_rms(sq, a.k, a.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int64_t at = (int64_t)i * TPR + t;
-            const int64_t left = a.k - at * VEC;
-            const int n = left < VEC ? (left < 0 ? 0 : (int)left) : VEC;
-            float w[VEC];
-            load8(w, (const T*)a.w + (n > 0 ? at * VEC : 0), n);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) v[i][j] = (v[i][j] * inv) * w[j];
+            for (int j = 0; j < VEC; ++j) v[i][j] = (v[i][j] * inv) * to_f32(wt[i][j]);
         }
     }
     float d = 0.0f;
@@ -278,19 +287,24 @@ __global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {
 
 template <typename T, bool NORM, int TPR, int NV>
 int launch(const NormArgs& a, hipStream_t stream) {
-    constexpr int RPB = TPR < 256 ? 256 / TPR : 1;
+    constexpr int RPB = TPR == 64 ? 4 : 1;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
     if (blocks > 0x7fffffff) return MOEQ8_EUNSUPPORTED;
-    hipLaunchKernelGGL((k_norm_q8<T, NORM, TPR, NV>), dim3((uint32_t)blocks), dim3(TPR < 256 ? 256 : TPR), 0, stream, a);
+    hipLaunchKernelGGL((k_norm_q8<T, NORM, TPR, NV>), dim3((uint32_t)blocks), dim3(RPB * TPR), 0, stream, a);
     return check_launch();
 }
 
 template <typename T, bool NORM>
 int launch_rows(const NormArgs& a, hipStream_t stream) {
+    // The fewest vectors a thread that still fill a row's threads: vectors past
+    // the row's end cost as much as others (16384 x 1024 bf16 in 128 and 256
+    // threads: 29 and 42 us).  Few rows of up to 4096 take twice the threads
+    // (one row 4.2 and 4.8 us, 16384 rows 99 and 91).
     if (a.k <= 512) return launch<T, NORM, 64, 1>(a, stream);
+    if (a.k <= 1024) return launch<T, NORM, 128, 1>(a, stream);
     if (a.k <= 2048) return launch<T, NORM, 256, 1>(a, stream);
-    if (a.k <= 4096) return launch<T, NORM, 256, 2>(a, stream);
-    if (a.k <= 8192) return launch<T, NORM, 256, 4>(a, stream);
+    if (a.k <= 4096) return a.rows > 1024 ? launch<T, NORM, 256, 2>(a, stream) : launch<T, NORM, 512, 1>(a, stream);
+    if (a.k <= 8192) return launch<T, NORM, 512, 2>(a, stream);
     if (a.k <= 16384) return launch<T, NORM, 1024, 2>(a, stream);
     if (a.k <= 32768) return launch<T, NORM, 1024, 4>(a, stream);
     if (a.rows > 0x7fffffff) return MOEQ8_EUNSUPPORTED;

@@ -154,10 +154,10 @@ def test_norm_strides_and_in_place(k, dtype):
         check_norm(x, w, res, TYPES[dtype], "both", pad=2, lead=1, inplace=where)
 
 
-@pytest.mark.parametrize("rows", [129, 1000])
-def test_norm_many_rows(rows):
-    say(f"norm rows {rows}")
-    x, w, res = norm_inputs(rows, 288, rows, residual=True)
+@pytest.mark.parametrize("rows,k", [(129, 288), (1000, 288), (1024, 2112), (1025, 2112), (1100, 4096)])
+def test_norm_many_rows(rows, k):
+    say(f"norm rows {rows}x{k}")
+    x, w, res = norm_inputs(rows, k, rows, residual=True)
     check_norm(x, w, res, torch.bfloat16, "both")
 
 
