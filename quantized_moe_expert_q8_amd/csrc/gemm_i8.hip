@@ -538,7 +538,8 @@ int launch_tile(const GemmArgs& g, bool dma, hipStream_t stream) {
 // above, with the reads of a whole stage one stage ahead of its products.
 //
 // 333 x 2047 x 4096 in tiles of 64: 12 us (waves that split the tile: 14 us).
-// What bounds it is the 80 GB/s at which a CU fetches its tile's rows.
+// What bounds it is the fetch of a tile's rows by its CU: 64 bytes a clock
+// (147 GB/s) from L2, about 80 GB/s where they come from memory.
 //
 // The swizzle: with rows of 256 bytes (W = 8) slot t of row r holds piece t ^
 // (r & 15), with 128 bytes (W = 4) piece t ^ ((r >> 1) & 7); both spread the
@@ -579,10 +580,16 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_split(GemmArgs g) {
             off[u] -= at > k - 16 ? at - (k - 16) : 0;
         }
     };
+    // The blocks of an XCD begin at different stages of k (where none is cut), so
+    // that they do not all ask the same memory channels at a time: 20 x 16384 x
+    // 4096 15.4 and 17.6 us, 128 x 4096 x 4096 9.6 and 9.1.
+    const int turn = DMA && k % KB == 0 ? (int)(blockIdx.x / 8) % steps : 0;
     i32x4 held[DMA ? 1 : L];
     auto load_stage = [&](int s, int buf) {
         if (s == steps - 1) clamp_offsets();
-        const int64_t at = (int64_t)(s < steps ? s : steps - 1) * KB;
+        int q = (s < steps ? s : steps - 1) + turn;
+        if (q >= steps) q -= steps;
+        const int64_t at = (int64_t)q * KB;
 #pragma unroll
         for (int u = 0; u < L; ++u) {
             const int8_t* base = (u < FU ? base_a : base_b) + at;
@@ -694,16 +701,17 @@ int launch_split(const GemmArgs& g, bool dma, hipStream_t stream) {
     return check_launch();
 }
 
-// Time of a product in tiles of bm x bn, in us, without the launch and the
-// first loads: the largest of what a CU can fetch (80 GB/s), what all of them
-// can (16 TB/s, most of it from L2) and what the matrix cores do at the clock
-// they hold (60% of peak), and the ends of its tiles.
-double tile_cost(const GemmArgs& g, int bm, int bn, double end) {
+// Time of a product in tiles of bm x bn, in us: the start of a block and, for
+// each tile of a CU, its end; between them the largest of what a CU can fetch
+// (80 GB/s), what all of them can (16 TB/s, most of it from L2) and what the
+// matrix cores do at the clock they hold (60% of peak).  The constants are
+// fitted to the times given in launch_gemm.
+double tile_cost(const GemmArgs& g, int bm, int bn, double start, double end) {
     const double tiles = (double)((g.m + bm - 1) / bm) * (double)((g.n + bn - 1) / bn), k = (double)g.k;
     const double rounds = (double)((int64_t)((tiles + 255) / 256));
     const double fetch = (bm + bn) * k, one = rounds * fetch / 80e3, all = tiles * fetch / 16e6;
     const double mul = rounds * bm * bn * k / 5.85e6;
-    return std::max(std::max(one, all), mul) + rounds * end;
+    return start + std::max(std::max(one, all), mul) + rounds * end;
 }
 
 template <typename T>
@@ -716,10 +724,11 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
         // the instruction, so small ones cost most a product; large ones leave
         // CUs idle.  Measured (us, the tiles in this order): 64 x 4096 x 4096
         // 7.3 8.5 10.7 17.2 41; 333 x 2047 x 4096 13.6 15.1 11.9 18.3 44; 1024 x
-        // 4096 x 4096 56 54 38 23 44; 3000 x 5000 x 512 86 93 70 18 18; 4096 x
-        // 4096 x 1024 - - - 29 24.
-        const double cost[5] = {tile_cost(g, 32, 32, 0.2), tile_cost(g, 32, 64, 0.3), tile_cost(g, 64, 64, 0.6),
-                                tile_cost(g, 128, 128, 1.3), tile_cost(g, 256, 256, 6.5)};
+        // 4096 x 4096 56 54 38 23 44; 600 x 2000 x 1024 11 13 12 8 -; 3000 x 5000 x
+        // 512 86 93 70 18 18; 4096 x 4096 x 1024 - - - 29 24.
+        const double cost[5] = {tile_cost(g, 32, 32, 3.4, 0.2), tile_cost(g, 32, 64, 2.2, 1.6),
+                                tile_cost(g, 64, 64, 2.6, 2.0), tile_cost(g, 128, 128, 3.0, 1.3),
+                                tile_cost(g, 256, 256, 4.0, 6.5)};
         switch (std::min_element(cost, cost + 5) - cost) {
             case 0: return launch_split<T, 8, 1, 1, 4>(g, dma, stream);
             case 1: return launch_split<T, 8, 1, 2, 4>(g, dma, stream);
