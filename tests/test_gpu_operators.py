@@ -555,3 +555,64 @@ def test_graph_replays_and_streams_equal_eager():
             torch.cuda.synchronize()
             for name, t in out.items():
                 assert torch.equal(t, want[name]), (i, how, name)
+
+
+def test_verify_step_uses_them_together():
+    """The step's end: the norm's outputs, the router's scores and the tail
+    exactly as their numpy forms give them, the experts' output to the bar of
+    the whole chain, and the same in a graph."""
+    import oracle
+    import workloads
+    from quantized_moe_expert_q8_amd import moe_layer as ml, verify_step as vs
+    say("verify step")
+    c, n_exp, hidden, inter, topk, vocab, seed = 5, 16, 512, 256, 4, 1003, 3
+    g = np.random.default_rng(seed)
+    f32 = lambda *s: g.standard_normal(s).astype(np.float32)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(DEV)
+    mats = [np.stack([workloads.synth_q8_0_matrix(seed, 0, e, m, r, k) for e in range(n_exp)])
+            for m, r, k in ((0, inter, hidden), (1, inter, hidden), (2, hidden, inter))]
+    raw = [dev(m.view(np.uint8).reshape(-1)) for m in mats]
+    norm, final, wr, wv, bias = (1 + 0.1 * f32(hidden)), (1 + 0.1 * f32(hidden)), f32(n_exp, hidden), f32(vocab, hidden), \
+        workloads.router_bias(seed, n_exp)
+    w = vs.VerifyWeights(dev(norm), vs.quantize_dense(dev(wr)), dev(bias),
+                         ml.RoutedExperts(*raw, n_exp, hidden, inter), dev(final), vs.quantize_dense(dev(wv)))
+    ws = vs.VerifyWorkspace(c, w, topk, DEV)
+    _, kw, _, mask = logits_inputs(c, vocab, 60, seed)
+    rules = {n: dev(v).to(torch.int32 if n == "tokens" else torch.float32 if n in ("repetition", "frequency", "presence")
+                          else torch.int64) for n, v in kw.items()}
+    rules["mask"] = dev(mask)
+    x, res = f32(c, hidden), f32(c, hidden)
+    xd, rd = dev(x), dev(res)
+    z = vs.forward(xd, rd, w, ws, rules=rules)
+    torch.cuda.synchronize()
+
+    s, y = ref.rms_norm_steps(x, norm, 1e-6, res)
+    q, d = ref.quantize_rows_steps(y)
+    rq, rs = ref.quantize_rows_steps(wr)
+    assert np.array_equal(w.router.codes.cpu().numpy(), rq) and np.array_equal(w.router.scale.cpu().numpy(), rs)
+    scores = ref.gemm_i8_steps(q, d, rq, rs)
+    assert np.array_equal(ws.router.cpu().numpy(), scores)
+    layer = oracle.moe_layer(y, scores, bias, None, lambda e: tuple(m[e] for m in mats), topk)
+    assert np.array_equal(ws.ids.cpu().numpy(), layer["ids"])
+    assert ws.xq.cpu().numpy().tobytes() == layer["xq"].tobytes()
+    out = ws.out.cpu().numpy()
+    # a code of q8_1(h) that rounds the other way moves an output by up to a step of its block
+    assert np.abs(out - layer["out"]).max() <= 2e-3 * max(1.0, np.abs(layer["out"]).max())
+    s2, y2 = ref.rms_norm_steps(out, final, 1e-6, s)
+    assert np.array_equal(ws.residual.cpu().numpy(), s2)
+    q2, d2 = ref.quantize_rows_steps(y2)
+    tail = ref.logits_rules(ref.gemm_i8_steps(q2, d2, *ref.quantize_rows_steps(wv)), np.float32, mask=mask, **kw)
+    assert np.array_equal(z.cpu().numpy(), tail)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        vs.forward(xd, rd, w, ws, rules=rules)
+    for i in range(3):
+        xd.copy_(torch.randn(c, hidden, device=DEV))
+        want = vs.forward(xd, rd, w, ws, rules=rules).clone()
+        ws.logits.zero_()
+        graph.replay()
+        assert torch.equal(ws.logits, want)
+    with pytest.raises(ValueError):
+        vs.forward(xd, rd, vs.VerifyWeights(w.norm, w.router, None, ml.RoutedExperts(*raw, n_exp, hidden, inter, packed=True),
+                                            w.final_norm, w.head), ws)
