@@ -4,9 +4,10 @@ library is missing or does not load, every call raises."""
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 c_i32, c_i64, c_u32, c_u64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64
 c_vp, c_fp, c_size = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t
@@ -106,6 +107,18 @@ def lib():
             fn.argtypes = args
         _LIB = so
     return _LIB
+
+
+def load_binding():
+    """The compiled torch side of the operators around the expert layer."""
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"the torch binding is not built ({BINDING_PATH} missing): run __graft_entry__.build() "
+                           "or python -m quantized_moe_expert_q8_amd.build")
+    import torch  # noqa: F401  (its libraries, which the binding's symbols are in)
+    spec = importlib.util.spec_from_file_location(f"{__package__}._binding", BINDING_PATH)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
 def call(name: str, *args) -> int:

@@ -13,7 +13,7 @@ from typing import NamedTuple
 
 import torch
 
-from ._lib import call, lib
+from ._lib import MoeQ8Error, call, lib, load_binding
 
 QK = 32
 Q8_0_BLOCK_BYTES = 34
@@ -777,65 +777,35 @@ def moe_combine(y: torch.Tensor, ids: torch.Tensor, weights: torch.Tensor,
 # around the expert layer: norm, int8 products, logits
 # ---------------------------------------------------------------------------
 
-_DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}       # enum moeq8_dtype
-NORM_FMTS = ("i8", "q8_1", "both")
+# The torch side of these calls is compiled (csrc/binding.cpp): their kernels
+# take a few microseconds, less than checks in Python would.
+_BINDING = None
 
 
-def _dtype_code(t: torch.Tensor, name: str) -> int:
-    code = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if code is None:
-        raise TypeError(f"{name} must be a float32, float16 or bfloat16 tensor")
-    return code
+def _raise(name: str, status: int):
+    raise MoeQ8Error(name, status)
 
 
-def _refuse(t, name: str, dtype, dev: int, shape: tuple):
-    if not isinstance(t, torch.Tensor) or t.get_device() != dev:
-        raise ValueError(f"{name} must be a device tensor, on the same device as the others")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-    raise ValueError(f"{name} must have unit inner stride")
+def _binding():
+    global _BINDING
+    if _BINDING is None:
+        m = load_binding()
+        address = lambda name: ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
+        m.bind(address("rms_norm_q8"), address("i8_quantize_rows"), address("gemm_i8"), address("logits_process"),
+               _raise, NormQ8)
+        _BINDING = m
+    return _BINDING
 
-
-# The checks below run on every call of a decode step, whose kernels take a few
-# microseconds: one condition where all is well, the reason found afterwards.
 
 def _matrix(t: torch.Tensor, name: str, dtype, dev: int, rows: int, cols: int) -> int:
     """Checks a device matrix [rows, cols] of rows whose elements lie together;
     returns its row stride."""
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == (rows, cols):
-        stride, inner = t.stride()
-        if inner == 1 or cols <= 1:
-            return stride if rows > 1 else cols
-    _refuse(t, name, dtype, dev, (rows, cols))
+    return _binding().matrix(t, name, dtype, dev, rows, cols)
 
 
 def _vector(t: torch.Tensor, name: str, dtype, dev: int, n: int) -> int:
     """Checks a contiguous device vector of n elements; returns its address."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev and t.shape == (n,)
-            and (n <= 1 or t.stride(0) == 1)):
-        return t.data_ptr()
-    _refuse(t, name, dtype, dev, (n,))
-
-
-def _on(t: torch.Tensor, name: str) -> int:
-    """Device index of a 2-D device tensor."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D, got {list(t.shape)}")
-    return t.get_device()
-
-
-# the current stream's handle without a Stream object, where torch has it (1 us a call)
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _current_stream(dev: int) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(dev)
-    return torch.cuda.current_stream(dev).cuda_stream
+    return _binding().vector(t, name, dtype, dev, n)
 
 
 class NormQ8(NamedTuple):
@@ -853,66 +823,14 @@ def rms_norm_q8(x: torch.Tensor, w: torch.Tensor, *, eps: float = 1e-6, residual
     w [k], to int8 rows with a scale each (fmt "i8"), to q8_1 rows ("q8_1", k a
     multiple of 32) or to both.  Given outputs are written, missing ones made;
     residual_out may be x or residual (updated in place)."""
-    dev = _on(x, "x")
-    code = _dtype_code(x, "x")
-    if fmt not in NORM_FMTS:
-        raise ValueError(f"fmt must be one of {NORM_FMTS}, got {fmt!r}")
-    rows, k = x.shape
-    dt = x.dtype
-    xs = _matrix(x, "x", dt, dev, rows, k)
-    wp = _vector(w, "w", dt, dev, k)
-    rs = ros = qs = 0
-    if residual is not None:
-        rs = _matrix(residual, "residual", dt, dev, rows, k)
-        if residual_out is None:
-            residual_out = torch.empty((rows, k), dtype=dt, device=x.device)
-        ros = _matrix(residual_out, "residual_out", dt, dev, rows, k)
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    if fmt != "q8_1":
-        if q is None:
-            q = torch.empty((rows, k), dtype=torch.int8, device=x.device)
-        if scale is None:
-            scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-        qs = _matrix(q, "q", torch.int8, dev, rows, k)
-        _vector(scale, "scale", torch.float32, dev, rows)
-    else:
-        q = scale = None
-    if fmt != "i8":
-        if k % QK:
-            raise ValueError(f"q8_1 rows need k to be a multiple of {QK}, got {k}")
-        nb = k // QK * Q8_1_BLOCK_BYTES
-        if xq is None:
-            xq = torch.empty((rows, nb), dtype=torch.uint8, device=x.device)
-        if _matrix(xq, "xq", torch.uint8, dev, rows, nb) != nb:
-            raise ValueError("xq rows must be contiguous")
-    else:
-        xq = None
-    if rows:
-        call("rms_norm_q8", x.data_ptr(), xs, None if residual is None else residual.data_ptr(), rs,
-             None if residual_out is None else residual_out.data_ptr(), ros, wp, code, rows, k, eps,
-             None if q is None else q.data_ptr(), qs, None if scale is None else scale.data_ptr(),
-             None if xq is None else xq.data_ptr(), _current_stream(dev))
-    return NormQ8(q, scale, xq, residual_out)
+    return _binding().rms_norm_q8(x, w, eps, residual, residual_out, fmt, q, scale, xq)
 
 
 def i8_quantize_rows(x: torch.Tensor, q: torch.Tensor | None = None,
                      scale: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """x [rows, k] (fp32, fp16 or bf16) -> int8 rows [rows, k] and their fp32
     scales [rows]: scale = max|x| / 127, codes rounded, halves away from zero."""
-    dev = _on(x, "x")
-    code = _dtype_code(x, "x")
-    rows, k = x.shape
-    xs = _matrix(x, "x", x.dtype, dev, rows, k)
-    if q is None:
-        q = torch.empty((rows, k), dtype=torch.int8, device=x.device)
-    if scale is None:
-        scale = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    qs = _matrix(q, "q", torch.int8, dev, rows, k)
-    sp = _vector(scale, "scale", torch.float32, dev, rows)
-    if rows:
-        call("i8_quantize_rows", x.data_ptr(), code, rows, k, xs, q.data_ptr(), qs, sp, _current_stream(dev))
-    return q, scale
+    return _binding().i8_quantize_rows(x, q, scale)
 
 
 def gemm_i8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor, *,
@@ -922,22 +840,7 @@ def gemm_i8(a: torch.Tensor, sa: torch.Tensor, b: torch.Tensor, sb: torch.Tensor
     with a scale each (rms_norm_q8, i8_quantize_rows) and int8 weights b [n, k]
     with a scale per channel.  The sums are exact.  out's dtype (out_dtype if
     out is made here) is float32, float16 or bfloat16."""
-    dev = _on(a, "a")
-    _on(b, "b")
-    (m, k), n = a.shape, b.shape[0]
-    as_ = _matrix(a, "a", torch.int8, dev, m, k)
-    bs = _matrix(b, "b", torch.int8, dev, n, k)
-    sap = _vector(sa, "sa", torch.float32, dev, m)
-    sbp = _vector(sb, "sb", torch.float32, dev, n)
-    bp = None if bias is None else _vector(bias, "bias", torch.float32, dev, n)
-    if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=a.device)
-    code = _dtype_code(out, "out")
-    os_ = _matrix(out, "out", out.dtype, dev, m, n)
-    if m and n:
-        call("gemm_i8", a.data_ptr(), as_, sap, b.data_ptr(), bs, sbp, bp, m, n, k, code, out.data_ptr(), os_,
-             _current_stream(dev))
-    return out
+    return _binding().gemm_i8(a, sa, b, sb, bias, out, out_dtype)
 
 
 def logits_process(logits: torch.Tensor, *, tokens: torch.Tensor | None = None, begin: torch.Tensor | None = None,
@@ -957,53 +860,8 @@ def logits_process(logits: torch.Tensor, *, tokens: torch.Tensor | None = None, 
     and bias_values.  mask int32 [rows, ceil(vocab / 32)]: bit v % 32 of word
     v // 32 allows token v.  begin, end, prompt_end and bias_offsets are int64,
     the penalties fp32."""
-    dev = _on(logits, "logits")
-    code = _dtype_code(logits, "logits")
-    rows, vocab = logits.shape
-    zs = _matrix(logits, "logits", logits.dtype, dev, rows, vocab)
-    if out is None:
-        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    os_ = _matrix(out, "out", logits.dtype, dev, rows, vocab)
-    tp = bp = ep = pp = rp = fp = sp = ip = vp = op = mp = None
-    nt = nb = ms = 0
-    if tokens is not None:
-        if begin is None or end is None:
-            raise ValueError("tokens need begin and end")
-        nt = tokens.numel()
-        tp = _vector(tokens, "tokens", torch.int32, dev, nt)
-        bp = _vector(begin, "begin", torch.int64, dev, rows)
-        ep = _vector(end, "end", torch.int64, dev, rows)
-        if prompt_end is not None:
-            pp = _vector(prompt_end, "prompt_end", torch.int64, dev, rows)
-        if repetition is not None:
-            rp = _vector(repetition, "repetition", torch.float32, dev, rows)
-        if frequency is not None:
-            fp = _vector(frequency, "frequency", torch.float32, dev, rows)
-        if presence is not None:
-            sp = _vector(presence, "presence", torch.float32, dev, rows)
-        if nt == 0:                                # an empty list has no address
-            tp = bp = ep = pp = rp = fp = sp = None
-    elif not (begin is None and end is None and prompt_end is None and repetition is None and frequency is None
-              and presence is None):
-        raise ValueError("penalties need tokens")
-    if bias_ids is not None:
-        if bias_values is None or bias_offsets is None:
-            raise ValueError("bias_ids, bias_values and bias_offsets go together")
-        nb = bias_ids.numel()
-        ip = _vector(bias_ids, "bias_ids", torch.int32, dev, nb)
-        vp = _vector(bias_values, "bias_values", torch.float32, dev, nb)
-        op = _vector(bias_offsets, "bias_offsets", torch.int64, dev, rows + 1)
-        if nb == 0:
-            ip = vp = op = None
-    elif not (bias_values is None and bias_offsets is None):
-        raise ValueError("bias_ids, bias_values and bias_offsets go together")
-    if mask is not None:
-        ms = _matrix(mask, "mask", torch.int32, dev, rows, (vocab + 31) // 32)
-        mp = mask.data_ptr()
-    if rows and vocab:
-        call("logits_process", logits.data_ptr(), zs, code, rows, vocab, tp, nt, bp, ep, pp, rp, fp, sp, ip, vp, nb,
-             op, mp, ms, out.data_ptr(), os_, _current_stream(dev))
-    return out
+    return _binding().logits_process(logits, tokens, begin, end, prompt_end, repetition, frequency, presence, bias_ids,
+                                     bias_values, bias_offsets, mask, out)
 
 
 # ---------------------------------------------------------------------------

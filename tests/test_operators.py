@@ -176,3 +176,18 @@ def test_matrix_and_vector_checks():
         ops._vector(t[0], "t", torch.float32, -1, 5)
     with pytest.raises(TypeError):
         ops._vector(t[0], "t", torch.int32, -1, 6)
+
+
+def test_compiled_checks_name_the_argument():
+    t, f = torch.zeros(4, 6), torch.float32
+    for err, words, call in [
+            (ValueError, "t must be a device tensor", lambda: ops._matrix(None, "t", f, -1, 4, 6)),
+            (ValueError, "t must be a device tensor", lambda: ops._vector([1.0], "t", f, -1, 1)),
+            (TypeError, "t must be torch.float16, got torch.float32", lambda: ops._matrix(t, "t", torch.float16, -1, 4, 6)),
+            (ValueError, r"t must be \[4, 7\], got \[4, 6\]", lambda: ops._matrix(t, "t", f, -1, 4, 7)),
+            (ValueError, "t must have unit inner stride", lambda: ops._vector(t[:, 0], "t", f, -1, 4)),
+            (ValueError, "logits must be a device tensor", lambda: ops.logits_process(None)),
+            (ValueError, "a must be a device tensor", lambda: ops.gemm_i8(t.to(torch.int8), t[0], None, t[0])),
+            (TypeError, "not a torch dtype", lambda: ops._vector(t[0], "t", 3, -1, 6))]:
+        with pytest.raises(err, match=words):
+            call()
