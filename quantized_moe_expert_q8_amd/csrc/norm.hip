@@ -13,6 +13,7 @@
 // once, and the weights are loaded with them.  What bounds it is the memory
 // traffic: 8192 x 8192 in bf16 with a residual takes 93 us, 5.1 TB/s, the rate
 // of a large copy.  For few rows it is the launch: 4 us for one of 4096.
+#include "moeq8_lds.hpp"
 #include "moeq8_types.hpp"
 #include "moeq8_host.hpp"
 
@@ -33,16 +34,44 @@ struct NormArgs {
 
 constexpr int VEC = 8;                            // values a thread takes at a time: a quarter of a block
 
-// Larger of two magnitudes, NaN if either is.
-__device__ __forceinline__ float max_or_nan(float a, float b) {
-    return (a != a || b != b) ? __builtin_nanf("") : fmaxf(a, b);
+// Bits of |v|: as unsigned numbers they are in the order of the magnitudes, a
+// NaN above all, so a maximum of them keeps a NaN.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+template <int CTRL, typename V>
+__device__ __forceinline__ V moved(V v) {          // v of the lane that the DPP control names
+    if constexpr (sizeof(V) == 8) {
+        const uint2 u = __builtin_bit_cast(uint2, v);
+        return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.x, CTRL, 0xf, 0xf, false),
+                                           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.y, CTRL, 0xf, 0xf, false)});
+    } else {
+        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+    }
+}
+constexpr int XOR1 = 0xB1, XOR2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140;
+
+template <typename V>
+__device__ __forceinline__ V of_lane(V v, int lane) {
+    if constexpr (sizeof(V) == 8) {
+        const uint2 u = __builtin_bit_cast(uint2, v);
+        return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_readlane((int)u.x, lane),
+                                           (uint32_t)__builtin_amdgcn_readlane((int)u.y, lane)});
+    } else {
+        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+    }
 }
 
+// Over the lanes of a full wave, in registers: the 16 lanes of a row by DPP,
+// then the four rows.  (Through LDS, as __shfl_xor goes, the two reductions of
+// one row of 4096 took a seventh of its time.)
 template <typename V, typename F>
 __device__ __forceinline__ V wave_reduce(V v, F op) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v = op(v, __shfl_xor(v, m));
-    return v;
+    v = op(v, moved<XOR1>(v));
+    v = op(v, moved<XOR2>(v));
+    v = op(v, moved<HALF_MIRROR>(v));
+    v = op(v, moved<MIRROR>(v));
+    return op(op(of_lane(v, 0), of_lane(v, 16)), op(of_lane(v, 32), of_lane(v, 48)));
 }
 
 // Over the TPR threads of a row, in a fixed order; every thread gets the value.
@@ -52,7 +81,7 @@ __device__ __forceinline__ V row_reduce(V v, V* lds, F op) {
     if constexpr (TPR > 64) {
         constexpr int W = TPR / 64;
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-        __syncthreads();
+        lds_barrier();
         v = lds[0];
 #pragma unroll
         for (int i = 1; i < W; ++i) v = op(v, lds[i]);
@@ -61,22 +90,40 @@ __device__ __forceinline__ V row_reduce(V v, V* lds, F op) {
 }
 
 // Codes of 8 values of scale d, packed; their sum.  d = 0 and a d that is not
-// finite give zeros (the scale says which).  The codes stay within 127: below
-// the normal range d is so coarse that a quotient may round past it.
+// finite give zeros (the scale says which).
+//
+// The code of y is roundf of the correctly rounded quotient y / d.  y * rcp(d)
+// differs from it by less than 2.3e-5 (v_rcp_f32 within an ulp, the quotient
+// rounded by half of one, both times 127), so where it lies more than 2^-14
+// from every half both round to the same integer; a vector with another value,
+// about one wave's in 16, takes the division.  Adding 1.5 * 2^23 rounds to an
+// integer whose low byte is the code.
 __device__ __forceinline__ uint2 codes8(const float (&y)[VEC], float d, int& sum) {
     uint2 o = {0u, 0u};
     sum = 0;
-    if (d > 0.0f && d < __builtin_inff()) {
-        const float rd = q8_code_rcp(d);
+    if (!(d > 0.0f && d < __builtin_inff())) return o;
+    constexpr float ROUND = 12582912.0f;
+    const float rd = __builtin_amdgcn_rcpf(d);
+    uint32_t u[VEC];
+    float off = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        const float r = __builtin_fmaf(y[i], rd, ROUND);
+        off = fmaxf(off, fabsf(__builtin_fmaf(y[i], rd, ROUND - r)));
+        u[i] = __float_as_uint(r);
+    }
+    // below the normal range the reciprocal is not what the above takes it for
+    if (__builtin_expect(off >= 0.5f - 0x1p-14f || d < 0x1p-126f, 0)) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            int c = q8_code(y[i], d, rd);
-            c = c > 127 ? 127 : (c < -127 ? -127 : c);
-            sum += c;
-            const uint32_t b = ((uint32_t)c & 0xffu) << (8 * (i & 3));
-            if (i < 4) o.x |= b; else o.y |= b;
+            // d is so coarse there that a quotient may round past 127
+            const int c = (int)roundf(y[i] / d);
+            u[i] = (uint32_t)(c > 127 ? 127 : (c < -127 ? -127 : c));
         }
     }
+    o.x = __builtin_amdgcn_perm(u[1], u[0], 0x0c0c0400u) | __builtin_amdgcn_perm(u[3], u[2], 0x04000c0cu);
+    o.y = __builtin_amdgcn_perm(u[5], u[4], 0x0c0c0400u) | __builtin_amdgcn_perm(u[7], u[6], 0x04000c0cu);
+    sum = __builtin_amdgcn_sdot4((int)o.x, 0x01010101, __builtin_amdgcn_sdot4((int)o.y, 0x01010101, 0, false), false);
     return o;
 }
 
@@ -89,7 +136,12 @@ __device__ __forceinline__ void load_raw(T (&v)[VEC], const T* p, int n) {
         T zero;
         from_f32(zero, 0.0f);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = i < n ? p[i] : zero;
+        for (int i = 0; i < VEC; ++i) v[i] = zero;
+        if (n <= 0) return;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = p[i < n ? i : 0];       // no load waits for another
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[i] = i < n ? v[i] : zero;
     }
 }
 
@@ -149,20 +201,19 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, const float (&y)[
         }
     }
     if (a.xq) {                                    // k % 32 == 0: the 4 lanes of a block are all here
-        float m = 0.0f;
+        uint32_t m = 0u;
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) m = max_or_nan(m, fabsf(y[j]));
-        m = max_or_nan(m, __shfl_xor(m, 1));
-        m = max_or_nan(m, __shfl_xor(m, 2));
-        const float db = m / 127.0f;
+        for (int j = 0; j < VEC; ++j) m = larger(m, magnitude(y[j]));
+        m = larger(m, moved<XOR1>(m));
+        m = larger(m, moved<XOR2>(m));
+        const float db = __uint_as_float(m) / 127.0f;
         const uint2 c = codes8(y, db, sum);
-        sum += __shfl_xor(sum, 1);
-        sum += __shfl_xor(sum, 2);
+        sum += moved<XOR1>(sum);
+        sum += moved<XOR2>(sum);
         uint32_t* o = reinterpret_cast<uint32_t*>(a.xq + (r * (a.k / QK) + i / 4) * Q81_BYTES);
         if ((i & 3) == 0)
             o[0] = float_to_half_bits(db) | (float_to_half_bits(materialize_f32(db * (float)sum)) << 16);
-        o[1 + 2 * (i & 3)] = c.x;
-        o[2 + 2 * (i & 3)] = c.y;
+        *reinterpret_cast<u32x2b*>(o + 1 + 2 * (i & 3)) = u32x2b{c.x, c.y};
     }
 }
 
@@ -171,7 +222,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, const float (&y)[
 template <typename T, bool NORM, int TPR, int NV>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
     __shared__ double lds_sum[TPR / 64];
-    __shared__ float lds_max[TPR / 64];
+    __shared__ uint32_t lds_max[TPR / 64];
     constexpr int RPB = TPR == 64 ? 4 : 1;
     const int t = threadIdx.x & (TPR - 1);
     const int64_t r = (int64_t)blockIdx.x * RPB + threadIdx.x / TPR;
@@ -198,7 +249,6 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
             for (int j = 0; j < VEC; ++j) sq += (double)v[i][j] * (double)v[i][j];
         }
     }
-    float m = 0.0f;
     if constexpr (NORM) {
         sq = row_reduce<TPR>(sq, lds_sum, [](double p, double q) { return p + q; });
         const float inv = inv_rms(sq, a.k, a.eps);
@@ -210,13 +260,14 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
     }
     float d = 0.0f;
     if (a.q) {
+        uint32_t m = 0u;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) m = max_or_nan(m, fabsf(v[i][j]));
+            for (int j = 0; j < VEC; ++j) m = larger(m, magnitude(v[i][j]));
         }
-        m = row_reduce<TPR>(m, lds_max, [](float p, float q) { return max_or_nan(p, q); });
-        d = m / 127.0f;
+        m = row_reduce<TPR>(m, lds_max, larger);
+        d = __uint_as_float(m) / 127.0f;
         if (t == 0) a.scale[r] = d;
     }
 #pragma unroll
@@ -234,7 +285,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
 template <typename T, bool NORM>
 __global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {
     __shared__ double lds_sum[16];
-    __shared__ float lds_max[16];
+    __shared__ uint32_t lds_max[16];
     const int64_t r = blockIdx.x;
     const int64_t nvec = (a.k + VEC - 1) / VEC;
     float inv = 1.0f;
@@ -261,16 +312,16 @@ __global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {
     };
     float d = 0.0f;
     if (a.q) {
-        float m = 0.0f;
+        uint32_t m = 0u;
         for (int64_t at = threadIdx.x; at < nvec; at += 1024) {
             float v[VEC];
             const int n = (int)(a.k - at * VEC < VEC ? a.k - at * VEC : VEC);
             row_y(v, at, n);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) m = max_or_nan(m, fabsf(v[j]));
+            for (int j = 0; j < VEC; ++j) m = larger(m, magnitude(v[j]));
         }
-        m = row_reduce<1024>(m, lds_max, [](float p, float q) { return max_or_nan(p, q); });
-        d = m / 127.0f;
+        m = row_reduce<1024>(m, lds_max, larger);
+        d = __uint_as_float(m) / 127.0f;
         if (threadIdx.x == 0) a.scale[r] = d;
     }
     for (int64_t at = threadIdx.x; at < nvec; at += 1024) {
