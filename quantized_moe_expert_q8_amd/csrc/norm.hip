@@ -11,8 +11,10 @@
 // a half.  One pass over the data: a thread keeps its 8-value vectors of s in
 // registers between the two row reductions, so x and the residual are read
 // once, and the weights are loaded with them.  What bounds it is the memory
-// traffic: 8192 x 8192 in bf16 with a residual takes 93 us, 5.1 TB/s, the rate
-// of a large copy.  For few rows it is the launch: 4 us for one of 4096.
+// traffic: 8192 x 8192 in bf16 with a residual takes 87 us, 5.4 TB/s, the rate
+// of a large copy; without a residual and with both formats the arithmetic of
+// the codes comes near it (16000 x 4096 72 us, 3.8 TB/s).  For few rows it is
+// the launch: 3.1 us for one of 4096.
 #include "moeq8_lds.hpp"
 #include "moeq8_types.hpp"
 #include "moeq8_host.hpp"
@@ -347,15 +349,21 @@ int launch(const NormArgs& a, hipStream_t stream) {
 
 template <typename T, bool NORM>
 int launch_rows(const NormArgs& a, hipStream_t stream) {
-    // The fewest vectors a thread that still fill a row's threads: vectors past
-    // the row's end cost as much as others (16384 x 1024 bf16 in 128 and 256
-    // threads: 29 and 42 us).  Few rows of up to 4096 take twice the threads
-    // (one row 4.2 and 4.8 us, 16384 rows 99 and 91).
+    // Few rows: the time is that of one row, so a thread takes as few vectors as
+    // 1024 threads allow (64 x 8192 bf16 in 512 x 2 and 1024 x 1: 4.9 and 4.5 us).
+    // Many: what counts is the work of a CU, in which vectors past a row's end
+    // cost as much as others, and smaller blocks wait less at their barriers
+    // (4000 x 8192 in the same two: 47.4 and 49.3 us; 600 x 10304 in 512 x 3 and
+    // 1024 x 2: 13.1 and 15.1; 16000 x 1504 in 128 x 2 and 256 x 1: 33.8 and 36.8,
+    // but 600 rows of them 5.5 and 4.8).
+    const bool many = a.rows > 512;
     if (a.k <= 512) return launch<T, NORM, 64, 1>(a, stream);
     if (a.k <= 1024) return launch<T, NORM, 128, 1>(a, stream);
-    if (a.k <= 2048) return launch<T, NORM, 256, 1>(a, stream);
-    if (a.k <= 4096) return a.rows > 1024 ? launch<T, NORM, 256, 2>(a, stream) : launch<T, NORM, 512, 1>(a, stream);
-    if (a.k <= 8192) return launch<T, NORM, 512, 2>(a, stream);
+    if (a.k <= 2048) return a.rows > 2048 ? launch<T, NORM, 128, 2>(a, stream) : launch<T, NORM, 256, 1>(a, stream);
+    if (a.k <= 4096) return many ? launch<T, NORM, 256, 2>(a, stream) : launch<T, NORM, 512, 1>(a, stream);
+    if (a.k <= 6144 && many) return launch<T, NORM, 256, 3>(a, stream);
+    if (a.k <= 8192) return many ? launch<T, NORM, 512, 2>(a, stream) : launch<T, NORM, 1024, 1>(a, stream);
+    if (a.k <= 12288 && many) return launch<T, NORM, 512, 3>(a, stream);
     if (a.k <= 16384) return launch<T, NORM, 1024, 2>(a, stream);
     if (a.k <= 32768) return launch<T, NORM, 1024, 4>(a, stream);
     if (a.rows > 0x7fffffff) return MOEQ8_EUNSUPPORTED;

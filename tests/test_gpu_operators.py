@@ -161,6 +161,15 @@ def test_norm_many_rows(rows, k):
     check_norm(x, w, res, torch.bfloat16, "both")
 
 
+@pytest.mark.parametrize("rows,k,fmt", [(512, 5024, "both"), (513, 5024, "both"), (600, 6141, "i8"), (513, 6176, "both"),
+                                        (520, 10272, "both"), (514, 12289, "i8"), (2048, 1056, "both"),
+                                        (2049, 1056, "both"), (2050, 2047, "i8")])
+def test_norm_forms_of_many_rows(rows, k, fmt):
+    say(f"norm form {rows}x{k} {fmt}")
+    x, w, res = norm_inputs(rows, k, rows + k, residual=True)
+    check_norm(x, w, res, torch.float16, fmt)
+
+
 def test_norm_extreme_values():
     """Zero rows, subnormal rows, rows of the largest values, a huge eps, and
     rows that are not finite beside rows that are."""
