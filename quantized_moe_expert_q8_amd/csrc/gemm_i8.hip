@@ -15,6 +15,7 @@ namespace moeq8 {
 namespace {
 
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x4_by4 __attribute__((ext_vector_type(4), aligned(4), may_alias));
 
 struct GemmArgs {
     const int8_t* a; int64_t a_stride;
@@ -40,32 +41,44 @@ __device__ __forceinline__ i32x4 load_piece(const int8_t* row, int64_t k0, int64
     return t.v;
 }
 
-// Four consecutive channels j .. j + 3 of token i.
-template <typename T>
-__device__ __forceinline__ void store_quad(const GemmArgs& g, int64_t i, int64_t j, i32x4 acc) {
-    if (i >= g.m) return;
-    const float sa = g.sa[i];
-    T* o = (T*)g.out + i * g.out_stride + j;
-    if (j + 4 <= g.n) {
-        union { T e[4]; u32x4b q; u32x2b d; } t;
+// Scales and biases of four consecutive channels j .. j + 3, loaded ahead of
+// their use: a load at the end of a kernel is a trip to memory that nothing
+// hides (333 x 2047 x 4096 with a bias: 12.5 us, loaded ahead 10.5).
+struct Channels {
+    float sb[4], bias[4];
+    __device__ __forceinline__ void load(const GemmArgs& g, int64_t j) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float v = ((float)acc[e] * sa) * g.sb[j + e];
-            if (g.bias) v += g.bias[j + e];
-            from_f32(t.e[e], v);
+            const int64_t c = j + e < g.n ? j + e : g.n - 1;
+            sb[e] = g.sb[c];
+            bias[e] = g.bias ? g.bias[c] : 0.0f;
         }
+    }
+};
+
+// Four consecutive channels j .. j + 3 of token i.
+template <typename T>
+__device__ __forceinline__ void store_quad(const GemmArgs& g, int64_t i, int64_t j, i32x4 acc, float sa, const Channels& c) {
+    if (i >= g.m) return;
+    T* o = (T*)g.out + i * g.out_stride + j;
+    union { T e[4]; u32x4b q; u32x2b d; } t;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float v = ((float)acc[e] * sa) * c.sb[e];
+        if (g.bias) v += c.bias[e];
+        from_f32(t.e[e], v);
+    }
+    if (j + 4 <= g.n) {
         if constexpr (sizeof(T) == 4) *reinterpret_cast<u32x4b*>(o) = t.q;
         else *reinterpret_cast<u32x2b*>(o) = t.d;
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (j + e >= g.n) break;
-            float v = ((float)acc[e] * sa) * g.sb[j + e];
-            if (g.bias) v += g.bias[j + e];
-            from_f32(o[e], v);
-        }
+        for (int e = 0; e < 4; ++e)
+            if (j + e < g.n) o[e] = t.e[e];
     }
 }
+
+__device__ __forceinline__ float token_scale(const GemmArgs& g, int64_t i) { return g.sa[i < g.m ? i : g.m - 1]; }
 
 // Rows of fewer than 16 values, and rows too far apart for the kernels below:
 // a tile of 64 tokens x 64 channels, 64 values of k at a time through LDS.
@@ -106,8 +119,12 @@ __global__ __launch_bounds__(256) void k_gemm_i8(GemmArgs g) {
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            store_quad<T>(g, i0 + wi + 16 * s + lane % 16, j0 + wj + 16 * u + lane / 16 * 4, acc[s][u]);
+        for (int u = 0; u < 2; ++u) {
+            const int64_t i = i0 + wi + 16 * s + lane % 16, j = j0 + wj + 16 * u + lane / 16 * 4;
+            Channels c;
+            c.load(g, j);
+            store_quad<T>(g, i, j, acc[s][u], token_scale(g, i), c);
+        }
 }
 
 // Bytes of the 16-byte piece p of a row of k >= 16 bytes: loaded from byte
@@ -129,6 +146,28 @@ __device__ __forceinline__ i32x4 drop_head(i32x4 v, int64_t p, int64_t k) {
     return v;
 }
 
+// 16 bytes at an address that is no multiple of 4, as the 4 dwords it begins in
+// and the one it ends in, each of which holds one of its bytes and so lies in
+// the row's allocation.  Loaded as they lie, from lanes whose neighbours read
+// other rows, such vectors cost many times an aligned one: 14 x 71 x 3305 8.8
+// and 6.1 us, 1 x 19623 x 3710 38 and 26.  (Where the lanes of a row lie
+// together, as in the tiles below, they cost less than these two loads.)
+struct OddPiece {
+    i32x4 v;
+    int32_t last;
+    __device__ __forceinline__ void load(const int8_t* p) {
+        const uintptr_t at = (uintptr_t)p;
+        v = *reinterpret_cast<const i32x4_by4*>(at & ~(uintptr_t)3);
+        last = *reinterpret_cast<const int32_t*>((at + 15) & ~(uintptr_t)3);
+    }
+    __device__ __forceinline__ i32x4 piece(uint32_t shift) const {     // shift: the address modulo 4 in its low two bits
+        return i32x4{(int)__builtin_amdgcn_alignbyte((uint32_t)v[1], (uint32_t)v[0], shift),
+                     (int)__builtin_amdgcn_alignbyte((uint32_t)v[2], (uint32_t)v[1], shift),
+                     (int)__builtin_amdgcn_alignbyte((uint32_t)v[3], (uint32_t)v[2], shift),
+                     (int)__builtin_amdgcn_alignbyte((uint32_t)last, (uint32_t)v[3], shift)};
+    }
+};
+
 // At most 16 tokens: the weights are read once from memory and are what the
 // time goes to.  The W waves of a block form groups of KW; a group takes TP
 // tiles of 16 channels at a time and its waves split k, each keeping its part
@@ -142,7 +181,7 @@ __device__ __forceinline__ i32x4 drop_head(i32x4 v, int64_t p, int64_t k) {
 // 5 x 131072 x 4096: 95 us, 5.7 TB/s (64 x 64 tiles: 132 us); 1 x 4096 x 4096:
 // 5.8 us in a graph (29 us), where the launch and one trip to memory are most
 // of it.
-template <typename T, int W, int KW, int NS, int TP>
+template <typename T, int W, int KW, int NS, int TP, bool ODD>
 __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, int chunks) {
     constexpr int ROW = 20;                        // 16 sums and padding against bank conflicts
     constexpr int G = W / KW, PER = (TP * 256 + KW * 64 - 1) / (KW * 64);      // groups, outputs of a thread
@@ -150,7 +189,10 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
     const int lane = threadIdx.x & 63, wave = (threadIdx.x >> 6) % KW, group = (threadIdx.x >> 6) / KW;
     const int r = lane & 15, quarter = lane >> 4;
     const int64_t rounds = (g.n + 16 * G * TP - 1) / (16 * G * TP), all_steps = (g.k + 63) / 64;
+    static_assert(TP * NS <= 16, "two bits of shift a piece");
     i32x4 act[NS], w[TP][NS];
+    int32_t w_last[ODD ? TP : 1][NS];              // with ODD: the rest of OddPiece, and all pieces' shifts
+    uint32_t w_shift = 0;
     auto first_step = [&](int c) { return ((int64_t)c * KW + wave) * steps; };
     auto own_steps = [&](int c) {                  // steps of the wave that lie inside the row
         const int64_t left = all_steps - first_step(c);
@@ -164,21 +206,40 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
             act[i] = i32x4{0, 0, 0, 0};
             if (i < own) {
                 const int64_t p = (first_step(c) + i) * 4 + quarter;
-                act[i] = drop_head((i32x4) * reinterpret_cast<const u32x4b*>(base + piece_at(p, g.k)), p, g.k);
+                const int8_t* at = base + piece_at(p, g.k);
+                if constexpr (ODD) {
+                    OddPiece o;
+                    o.load(at);
+                    act[i] = o.piece((uint32_t)(uintptr_t)at);
+                } else {
+                    act[i] = *reinterpret_cast<const i32x4_by4*>(at);
+                }
+                act[i] = drop_head(act[i], p, g.k);
             }
         }
     };
     auto channel = [&](int64_t round, int u) { return ((round * G + group) * TP + u) * 16; };
     auto load_w = [&](int64_t round, int c) {
         const int own = own_steps(c);
+        w_shift = 0;
 #pragma unroll
         for (int u = 0; u < TP; ++u) {
             const int64_t j = channel(round, u) + r;
             const int8_t* base = g.b + (j < g.n ? j : g.n - 1) * g.b_stride;
 #pragma unroll
             for (int i = 0; i < NS; ++i)
-                if (i < own)
-                    w[u][i] = (i32x4) * reinterpret_cast<const u32x4b*>(base + piece_at((first_step(c) + i) * 4 + quarter, g.k));
+                if (i < own) {
+                    const int8_t* at = base + piece_at((first_step(c) + i) * 4 + quarter, g.k);
+                    if constexpr (ODD) {
+                        OddPiece o;
+                        o.load(at);
+                        w[u][i] = o.v;
+                        w_last[u][i] = o.last;
+                        w_shift |= ((uint32_t)(uintptr_t)at & 3) << (2 * (u * NS + i));
+                    } else {
+                        w[u][i] = *reinterpret_cast<const i32x4_by4*>(at);
+                    }
+                }
         }
     };
     int64_t round = blockIdx.x;
@@ -186,7 +247,10 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
 #pragma unroll
     for (int u = 0; u < TP; ++u)
 #pragma unroll
-        for (int i = 0; i < NS; ++i) w[u][i] = i32x4{0, 0, 0, 0};
+        for (int i = 0; i < NS; ++i) {
+            w[u][i] = i32x4{0, 0, 0, 0};
+            if constexpr (ODD) w_last[u][i] = 0;
+        }
     load_w(round, 0);
     load_act(0);
     i32x4 acc[TP] = {};
@@ -196,7 +260,12 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
         const bool last = c == chunks - 1;
         const int64_t this_round = round;
         float sa[PER], sb[PER], bias[PER];
-        if (KW > 1 && last) {
+        Channels own[KW == 1 ? TP : 1];
+        if constexpr (KW == 1) {
+            sa[0] = token_scale(g, r);
+#pragma unroll
+            for (int u = 0; u < TP; ++u) own[u].load(g, channel(round, u) + quarter * 4);
+        } else if (last) {
 #pragma unroll
             for (int o = 0; o < PER; ++o) {
                 const int e = first_out + o * KW * 64;
@@ -210,7 +279,11 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
-            for (int u = 0; u < TP; ++u) acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][i], act[i], acc[u], 0, 0, 0);
+            for (int u = 0; u < TP; ++u) {
+                i32x4 x = w[u][i];
+                if constexpr (ODD) x = OddPiece{x, w_last[u][i]}.piece(w_shift >> (2 * (u * NS + i)));
+                acc[u] = __builtin_amdgcn_mfma_i32_16x16x64_i8(x, act[i], acc[u], 0, 0, 0);
+            }
         if (last) { round += gridDim.x; c = 0; } else { ++c; }
         if (round < rounds) {
             load_w(round, c);
@@ -219,7 +292,7 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
         if (last) {
             if constexpr (KW == 1) {
 #pragma unroll
-                for (int u = 0; u < TP; ++u) store_quad<T>(g, r, channel(this_round, u) + quarter * 4, acc[u]);
+                for (int u = 0; u < TP; ++u) store_quad<T>(g, r, channel(this_round, u) + quarter * 4, acc[u], sa[0], own[u]);
             } else {
 #pragma unroll
                 for (int u = 0; u < TP; ++u)
@@ -247,6 +320,13 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
     }
 }
 
+// Whether every piece of every row begins at a multiple of 16 or of 4 bytes.
+uint64_t row_bits(const GemmArgs& g) {
+    return (uintptr_t)g.a | (uintptr_t)g.b | (uint64_t)g.a_stride | (uint64_t)g.b_stride | (uint64_t)g.k;
+}
+bool by_vectors(const GemmArgs& g) { return (row_bits(g) & 15) == 0; }
+bool by_dwords(const GemmArgs& g) { return (row_bits(g) & 3) == 0; }
+
 template <typename T, int W, int KW, int NS, int TP>
 int launch_few_form(const GemmArgs& g, int chunks, hipStream_t stream) {
     // 16 waves a CU, the blocks with the same number of rounds (or one less)
@@ -254,7 +334,10 @@ int launch_few_form(const GemmArgs& g, int chunks, hipStream_t stream) {
     const int64_t rounds = (g.n + CHANNELS - 1) / CHANNELS, each = (rounds + MOST - 1) / MOST;
     const int64_t blocks = (rounds + each - 1) / each, all = (g.k + 63) / 64;
     const int steps = (int)((all + (int64_t)chunks * KW - 1) / ((int64_t)chunks * KW));
-    hipLaunchKernelGGL((k_gemm_i8_few<T, W, KW, NS, TP>), dim3((uint32_t)blocks), dim3(W * 64), 0, stream, g, steps, chunks);
+    if (by_dwords(g))
+        hipLaunchKernelGGL((k_gemm_i8_few<T, W, KW, NS, TP, false>), dim3((uint32_t)blocks), dim3(W * 64), 0, stream, g, steps, chunks);
+    else
+        hipLaunchKernelGGL((k_gemm_i8_few<T, W, KW, NS, TP, true>), dim3((uint32_t)blocks), dim3(W * 64), 0, stream, g, steps, chunks);
     return check_launch();
 }
 
@@ -409,12 +492,11 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_i8_tile(GemmArgs g) {
         for (int u = 0; u < FU; ++u) fa[t & 1][u] = drop_head(fa[t & 1][u], (int64_t)(steps - 1) * 8 + 2 * t + half, k);
     };
 
-    for (int x = threadIdx.x; x < BM; x += WAVES * 64) lds_sa[x] = g.sa[i0 + x < g.m ? i0 + x : g.m - 1];
-    for (int x = threadIdx.x; x < BN; x += WAVES * 64) {
-        const int64_t j = j0 + x < g.n ? j0 + x : g.n - 1;
-        lds_sb[x] = g.sb[j];
-        if (g.bias) lds_bias[x] = g.bias[j];
-    }
+    // the scales, on their way to LDS for the end, are not waited for here
+    static_assert(BM <= WAVES * 64 && BN <= WAVES * 64, "one scale a thread");
+    const int x = threadIdx.x;
+    const int64_t scale_j = j0 + x < g.n ? j0 + x : g.n - 1;
+    const float own_sa = token_scale(g, i0 + x), own_sb = g.sb[scale_j], own_bias = g.bias ? g.bias[scale_j] : 0.0f;
     // Stages past the last are the last one again, into buffers that no one
     // reads any more: a form of the step without loads would make the compiler
     // move the accumulators through memory.
@@ -461,6 +543,8 @@ __global__ __launch_bounds__(WM * WN * 64) void k_gemm_i8_tile(GemmArgs g) {
     drop_tail(3);
     step(integral_constant<int, 3>{}, no{}, no{}, buf, 0, 0);
     wait_vm<0>();                                  // no load may reach LDS after the block has left it
+    if (x < BM) lds_sa[x] = own_sa;
+    if (x < BN) lds_sb[x] = own_sb, lds_bias[x] = own_bias;
 
     // A lane holds token fr of each 32 x 32 tile and channels 8 q + 4 half .. +
     // 3.  The wave turns 32 tokens at a time round through its own LDS, so that
@@ -529,7 +613,7 @@ int launch_tile(const GemmArgs& g, bool dma, hipStream_t stream) {
     return check_launch();
 }
 
-// Small tiles, of FU x FV tiles of 32 x 32: the W waves of a block split k, not
+// Small tiles, of FU x FV tiles of 32 x 32: the 8 waves of a block split k, not
 // the tile.  A stage is 32 values of k for each wave; every wave multiplies its
 // part of it for the whole tile, so its products are FU x FV independent sums
 // and a fragment is read from LDS once, where waves that split the tile would
@@ -537,27 +621,26 @@ int launch_tile(const GemmArgs& g, bool dma, hipStream_t stream) {
 // waves' sums are added through LDS at the end.  Stages go round ST buffers as
 // above, with the reads of a whole stage one stage ahead of its products.
 //
-// 333 x 2047 x 4096 in tiles of 64: 12 us (waves that split the tile: 14 us).
+// 333 x 2047 x 4096 in tiles of 64: 10.5 us (waves that split the tile: 14 us).
 // What bounds it is the fetch of a tile's rows by its CU: 64 bytes a clock
 // (147 GB/s) from L2, about 80 GB/s where they come from memory.
 //
-// The swizzle: with rows of 256 bytes (W = 8) slot t of row r holds piece t ^
-// (r & 15), with 128 bytes (W = 4) piece t ^ ((r >> 1) & 7); both spread the
-// lanes that LDS serves together over all banks.
-template <typename T, int W, int FU, int FV, int ST, bool DMA>
-__global__ __launch_bounds__(W * 64) void k_gemm_i8_split(GemmArgs g) {
-    constexpr int BM = FU * 32, BN = FV * 32, KB = W * 32, STAGE = (BM + BN) * KB, SUMS = W * BM * BN * 4;
+// The swizzle: slot t of row r (256 bytes) holds piece t ^ (r & 15), which
+// spreads the lanes that LDS serves together over all banks.
+template <typename T, int FU, int FV, int ST, bool DMA>
+__global__ __launch_bounds__(512) void k_gemm_i8_split(GemmArgs g) {
+    constexpr int W = 8, BM = FU * 32, BN = FV * 32, KB = W * 32, STAGE = (BM + BN) * KB, SUMS = W * BM * BN * 4;
     constexpr int LDS = ST * STAGE > SUMS ? ST * STAGE : SUMS;
     constexpr int L = FU + FV;                     // loads of 1 KB a wave and stage, and fragments
     constexpr int LR = 1024 / KB, SLOTS = KB / 16; // rows a load, 16-byte slots a row
-    static_assert((W == 4 || W == 8) && (DMA || ST == 2), "");
+    static_assert(DMA || ST == 2, "");
     __shared__ __attribute__((aligned(1024))) int8_t ring[LDS];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     int64_t ti, tj;
     tile_of(blockIdx.x, (uint32_t)((g.m + BM - 1) / BM), (uint32_t)((g.n + BN - 1) / BN), ti, tj);
     const int64_t i0 = ti * BM, j0 = tj * BN;
     const int k = (int)g.k, steps = (k + KB - 1) / KB;
-    auto mix = [&](int r) { return W == 8 ? r & 15 : (r >> 1) & 7; };
+    auto mix = [&](int r) { return r & 15; };
 
     // load u of the wave: rows of a for u < FU, of b for the others
     auto first_row = [&](int u) { return u < FU ? (wave * FU + u) * LR : (wave * FV + u - FU) * LR; };
@@ -622,6 +705,15 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_split(GemmArgs g) {
                 acc[u][v] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[at][v], fa[at][u], acc[u][v], 0, 0, 0);
     };
 
+    // a thread's outputs: quads of the same four channels, of every TOKENS-th token
+    constexpr int QUADS = BN / 4, TOKENS = W * 64 / QUADS, OUTS = BM > TOKENS ? BM / TOKENS : 1;
+    const int out_i = threadIdx.x / QUADS, out_q = threadIdx.x % QUADS;
+    Channels channels;
+    channels.load(g, j0 + out_q * 4);
+    float sa[OUTS];
+#pragma unroll
+    for (int o = 0; o < OUTS; ++o) sa[o] = token_scale(g, i0 + out_i + o * TOKENS);
+
     constexpr int AHEAD = DMA ? ST : 3;
     if constexpr (DMA) {
 #pragma unroll
@@ -670,7 +762,6 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_split(GemmArgs g) {
 
     // [wave][token][channel]: quad of channels x of token i at x ^ (i & (BN / 4 - 1))
     int32_t* sums = reinterpret_cast<int32_t*>(ring);
-    constexpr int QUADS = BN / 4;
     auto quad_at = [&](int w, int i, int x) { return ((w * BM + i) * QUADS + (x ^ (i & (QUADS - 1)))) * 4; };
 #pragma unroll
     for (int u = 0; u < FU; ++u)
@@ -681,23 +772,25 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_split(GemmArgs g) {
                 *reinterpret_cast<i32x4*>(sums + quad_at(wave, 32 * u + fr, 8 * v + 2 * q + half)) =
                     i32x4{acc[u][v][4 * q], acc[u][v][4 * q + 1], acc[u][v][4 * q + 2], acc[u][v][4 * q + 3]};
     lds_barrier();
-    for (int x = threadIdx.x; x < BM * QUADS; x += W * 64) {
-        const int i = x / QUADS, qd = x % QUADS;
-        i32x4 sum = *reinterpret_cast<const i32x4*>(sums + quad_at(0, i, qd));
 #pragma unroll
-        for (int w = 1; w < W; ++w) sum += *reinterpret_cast<const i32x4*>(sums + quad_at(w, i, qd));
-        store_quad<T>(g, i0 + i, j0 + qd * 4, sum);
+    for (int o = 0; o < OUTS; ++o) {
+        const int i = out_i + o * TOKENS;
+        if (i >= BM) break;
+        i32x4 sum = *reinterpret_cast<const i32x4*>(sums + quad_at(0, i, out_q));
+#pragma unroll
+        for (int w = 1; w < W; ++w) sum += *reinterpret_cast<const i32x4*>(sums + quad_at(w, i, out_q));
+        store_quad<T>(g, i0 + i, j0 + out_q * 4, sum, sa[o], channels);
     }
 }
 
-template <typename T, int W, int FU, int FV, int ST>
+template <typename T, int FU, int FV, int ST>
 int launch_split(const GemmArgs& g, bool dma, hipStream_t stream) {
     const int64_t blocks = ((g.m + FU * 32 - 1) / (FU * 32)) * ((g.n + FV * 32 - 1) / (FV * 32));
     if (blocks > 0x0fffffff) return MOEQ8_EUNSUPPORTED;
     if (dma)
-        hipLaunchKernelGGL((k_gemm_i8_split<T, W, FU, FV, ST, true>), dim3((uint32_t)blocks), dim3(W * 64), 0, stream, g);
+        hipLaunchKernelGGL((k_gemm_i8_split<T, FU, FV, ST, true>), dim3((uint32_t)blocks), dim3(512), 0, stream, g);
     else
-        hipLaunchKernelGGL((k_gemm_i8_split<T, W, FU, FV, 2, false>), dim3((uint32_t)blocks), dim3(W * 64), 0, stream, g);
+        hipLaunchKernelGGL((k_gemm_i8_split<T, FU, FV, 2, false>), dim3((uint32_t)blocks), dim3(512), 0, stream, g);
     return check_launch();
 }
 
@@ -719,7 +812,7 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
     constexpr int64_t MAX_STRIDE = 1 << 23;        // a tile's rows within 31-bit offsets
     if (g.k >= 16 && g.m <= 16) return launch_few<T>(g, stream);
     if (g.k >= 16 && g.a_stride < MAX_STRIDE && g.b_stride < MAX_STRIDE) {
-        const bool dma = (((uintptr_t)g.a | (uintptr_t)g.b | (uint64_t)g.a_stride | (uint64_t)g.b_stride | (uint64_t)g.k) & 15) == 0;
+        const bool dma = by_vectors(g);
         // The tile with the least time.  A CU fetches tiles at 80 GB/s whatever
         // the instruction, so small ones cost most a product; large ones leave
         // CUs idle.  Measured (us, the tiles in this order): 64 x 4096 x 4096
@@ -730,9 +823,9 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
                                 tile_cost(g, 64, 64, 2.6, 2.0), tile_cost(g, 128, 128, 3.0, 1.3),
                                 tile_cost(g, 256, 256, 4.0, 6.5)};
         switch (std::min_element(cost, cost + 5) - cost) {
-            case 0: return launch_split<T, 8, 1, 1, 4>(g, dma, stream);
-            case 1: return launch_split<T, 8, 1, 2, 4>(g, dma, stream);
-            case 2: return launch_split<T, 8, 2, 2, 4>(g, dma, stream);
+            case 0: return launch_split<T, 1, 1, 4>(g, dma, stream);
+            case 1: return launch_split<T, 1, 2, 4>(g, dma, stream);
+            case 2: return launch_split<T, 2, 2, 4>(g, dma, stream);
             case 3:
                 // up to one tile a CU four stages, above it two blocks a CU of two
                 // stages: 1024 x 4096 x 4096 23 and 26 us, 2048 x 4096 x 4096 45 and 42

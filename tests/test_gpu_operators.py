@@ -301,6 +301,15 @@ def test_gemm_strides(m, pads, leads):
     check_gemm(m, 75, 200, torch.float32, False, pads, leads)
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 70, 17), (5, 33000, 255), (16, 33001, 197), (3, 17000, 449), (2, 300, 1001),
+                                   (7, 100, 2046), (14, 71, 3305), (16, 222, 4097), (4, 40, 16399)])
+@pytest.mark.parametrize("leads", [(0, 0), (1, 2), (3, 5)])
+def test_gemm_few_tokens_off_dwords(m, n, k, leads):
+    """Rows that begin and end at every byte of a dword."""
+    say(f"gemm off dwords {m}x{n}x{k} {leads}")
+    check_gemm(m, n, k, torch.float16, m % 2 == 0, (0, leads[1] - leads[0], 0), (*leads, 0))
+
+
 @pytest.mark.parametrize("m", [1, 20, 70, 260])
 def test_gemm_extreme_codes(m):
     """All -128 (the largest sums), at k past 65536 and at the longest."""
