@@ -271,13 +271,16 @@ int launch_form(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
 
 template <typename T>
 int launch_logits(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
-    // Many tiles: small blocks, 8 on a CU, hide each other's waits (256 x 131072
-    // bf16 with 2048 tokens a row: 37 us; in blocks of 512 55).  Few: what counts
-    // is how soon one block is done, so a thread takes one vector, and blocks of
-    // long lists are larger (5 x 131072 f32 with 8192 tokens a row: 256 threads
-    // 12.7, 512 7.5, 1024 7.0 us; 91 x 21061 with 688: 10.7, 8.5, 10.4).
+    // More blocks of 512 threads than run at a time, 4 a CU: a thread takes two
+    // vectors (220 x 19809 bf16 8.0 and 9.9 us, 16 x 131072 f32 8.9 and 9.6, but
+    // 91 x 21061 f32, 1001 blocks, 8.2 and 7.7; 256 x 131072 bf16 with 2048 tokens
+    // a row 39 us).  Fewer: what counts is how soon one block is done, so a thread
+    // takes one vector, and blocks of long lists are larger (5 x 131072 f32 with
+    // 8192 tokens a row: 256 threads 9.1, 512 7.2, 1024 6.3 us; 32 x 32000 bf16
+    // with 1000: 5.6, 5.4, 5.7).
     constexpr int VEC = 16 / sizeof(T);
-    if (a.vocab / 4096 * rows > 2048) return launch_form<T, 256, 4096>(a, rows, stream);
+    const int64_t tiles = (a.vocab + 512 * VEC - 1) / (512 * VEC);
+    if (rows > 1024 / tiles) return launch_form<T, 512, 1024 * VEC>(a, rows, stream);
     if (a.n_tokens / rows < 1024) return launch_form<T, 512, 512 * VEC>(a, rows, stream);
     return launch_form<T, 1024, 1024 * VEC>(a, rows, stream);
 }
