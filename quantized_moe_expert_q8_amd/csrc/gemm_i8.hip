@@ -796,15 +796,30 @@ int launch_split(const GemmArgs& g, bool dma, hipStream_t stream) {
 
 // Time of a product in tiles of bm x bn, in us: the start of a block and, for
 // each tile of a CU, its end; between them the largest of what a CU can fetch
-// (80 GB/s), what all of them can (16 TB/s, most of it from L2) and what the
-// matrix cores do at the clock they hold (60% of peak).  The constants are
-// fitted to the times given in launch_gemm.
+// (74 GB/s), what all of them can (15 TB/s, most of it from L2) and what the
+// matrix cores do at the clock they hold (two thirds of peak).  The constants
+// are fitted to the times of the five tiles on 83 products of 17 to 8192 tokens,
+// 64 to 16384 channels and k = 128 to 8192: the tile chosen takes 0.02% longer
+// than the best one on average (0.6% for rows off 16 bytes).
 double tile_cost(const GemmArgs& g, int bm, int bn, double start, double end) {
     const double tiles = (double)((g.m + bm - 1) / bm) * (double)((g.n + bn - 1) / bn), k = (double)g.k;
     const double rounds = (double)((int64_t)((tiles + 255) / 256));
-    const double fetch = (bm + bn) * k, one = rounds * fetch / 80e3, all = tiles * fetch / 16e6;
-    const double mul = rounds * bm * bn * k / 5.85e6;
+    const double fetch = (bm + bn) * k, one = rounds * fetch / 74e3, all = tiles * fetch / 14.8e6;
+    const double mul = rounds * bm * bn * k / 6.6e6;
     return start + std::max(std::max(one, all), mul) + rounds * end;
+}
+
+// Tiles of 128 x 128 in WM x 8 / WM waves.  Up to one tile a CU three stages,
+// above it two blocks a CU of two stages: 1024 x 4096 x 4096 22 and 25 us, 2048 x
+// 4096 x 4096 44 and 40.  (Four stages were no faster: 800 x 3873 x 3488 20.6 and
+// 20.1.)  With outputs of 16 bits a wave's part is 32 x 64, whose rows in out are
+// whole lines: the same product 20.6 us, in parts of 64 x 32 21.4.  (In tiles of
+// 256 the higher parts are better: 8192 x 8192 x 4096 272-280 us sustained, in
+// parts of 64 x 128 284-290.)
+template <typename T, int WM>
+int launch_middle(const GemmArgs& g, bool dma, hipStream_t stream) {
+    if (((g.m + 127) / 128) * ((g.n + 127) / 128) <= 256) return launch_tile<T, WM, 8 / WM, 4 / WM, WM / 2, 3>(g, dma, stream);
+    return launch_tile<T, WM, 8 / WM, 4 / WM, WM / 2, 2>(g, dma, stream);
 }
 
 template <typename T>
@@ -815,23 +830,20 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
         const bool dma = by_vectors(g);
         // The tile with the least time.  A CU fetches tiles at 80 GB/s whatever
         // the instruction, so small ones cost most a product; large ones leave
-        // CUs idle.  Measured (us, the tiles in this order): 64 x 4096 x 4096
-        // 7.3 8.5 10.7 17.2 41; 333 x 2047 x 4096 13.6 15.1 11.9 18.3 44; 1024 x
-        // 4096 x 4096 56 54 38 23 44; 600 x 2000 x 1024 11 13 12 8 -; 3000 x 5000 x
-        // 512 86 93 70 18 18; 4096 x 4096 x 1024 - - - 29 24.
-        const double cost[5] = {tile_cost(g, 32, 32, 3.4, 0.2), tile_cost(g, 32, 64, 2.2, 1.6),
-                                tile_cost(g, 64, 64, 2.6, 2.0), tile_cost(g, 128, 128, 3.0, 1.3),
-                                tile_cost(g, 256, 256, 4.0, 6.5)};
+        // CUs idle.  Measured (us, the tiles in this order): 333 x 2047 x 4096
+        // 13.5 14.5 10.7 17.4 44; 1024 x 4096 x 4096 57 52 37 22 42; 1327 x 249 x
+        // 896 5.5 5.0 6.2 7.3 17; 836 x 7175 x 1024 46 46 35 13 19.
+        const double cost[5] = {tile_cost(g, 32, 32, 2.2, 0.86), tile_cost(g, 32, 64, 1.1, 2.3),
+                                tile_cost(g, 64, 64, 2.3, 2.1), tile_cost(g, 128, 128, 2.0, 2.0),
+                                tile_cost(g, 256, 256, 2.7, 8.6)};
         switch (std::min_element(cost, cost + 5) - cost) {
             case 0: return launch_split<T, 1, 1, 4>(g, dma, stream);
             case 1: return launch_split<T, 1, 2, 4>(g, dma, stream);
             case 2: return launch_split<T, 2, 2, 4>(g, dma, stream);
             case 3:
-                // up to one tile a CU four stages, above it two blocks a CU of two
-                // stages: 1024 x 4096 x 4096 23 and 26 us, 2048 x 4096 x 4096 45 and 42
-                if (((g.m + 127) / 128) * ((g.n + 127) / 128) <= 256) return launch_tile<T, 2, 4, 2, 1, 4>(g, dma, stream);
-                return launch_tile<T, 2, 4, 2, 1, 2>(g, dma, stream);
-            default: return launch_tile<T, 2, 4, 4, 2, 2>(g, dma, stream);
+                return launch_middle<T, sizeof(T) == 2 ? 4 : 2>(g, dma, stream);
+            default:
+                return launch_tile<T, 2, 4, 4, 2, 2>(g, dma, stream);
         }
     }
     const int64_t blocks = ((g.m + 63) / 64) * ((g.n + 63) / 64);
