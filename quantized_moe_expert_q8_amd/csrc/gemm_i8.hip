@@ -795,17 +795,17 @@ int launch_split(const GemmArgs& g, bool dma, hipStream_t stream) {
 }
 
 // Time of a product in tiles of bm x bn, in us: the start of a block and, for
-// each tile of a CU, its end; between them the largest of what a CU can fetch
-// (74 GB/s), what all of them can (15 TB/s, most of it from L2) and what the
-// matrix cores do at the clock they hold (two thirds of peak).  The constants
-// are fitted to the times of the five tiles on 83 products of 17 to 8192 tokens,
-// 64 to 16384 channels and k = 128 to 8192: the tile chosen takes 0.02% longer
-// than the best one on average (0.6% for rows off 16 bytes).
-double tile_cost(const GemmArgs& g, int bm, int bn, double start, double end) {
+// each tile of a CU, its end; between them the largest of what a CU takes in
+// (rate, in GB/s), what all of them can (18 TB/s, most of it from L2) and what
+// the matrix cores do at the clock they hold (two thirds of peak).  The
+// constants are fitted to the times of the six tiles on 66 products of 17 to
+// 8192 tokens, 64 to 16384 channels and k = 128 to 8192, where the tile chosen
+// was the best one in each (within 1% on average for rows off 16 bytes).
+double tile_cost(const GemmArgs& g, int bm, int bn, double rate, double start, double end) {
     const double tiles = (double)((g.m + bm - 1) / bm) * (double)((g.n + bn - 1) / bn), k = (double)g.k;
     const double rounds = (double)((int64_t)((tiles + 255) / 256));
-    const double fetch = (bm + bn) * k, one = rounds * fetch / 74e3, all = tiles * fetch / 14.8e6;
-    const double mul = rounds * bm * bn * k / 6.6e6;
+    const double fetch = (bm + bn) * k, one = rounds * fetch / (rate * 1e3), all = tiles * fetch / 17.8e6;
+    const double mul = rounds * bm * bn * k / 6.77e6;
     return start + std::max(std::max(one, all), mul) + rounds * end;
 }
 
@@ -828,21 +828,27 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
     if (g.k >= 16 && g.m <= 16) return launch_few<T>(g, stream);
     if (g.k >= 16 && g.a_stride < MAX_STRIDE && g.b_stride < MAX_STRIDE) {
         const bool dma = by_vectors(g);
-        // The tile with the least time.  A CU fetches tiles at 80 GB/s whatever
-        // the instruction, so small ones cost most a product; large ones leave
-        // CUs idle.  Measured (us, the tiles in this order): 333 x 2047 x 4096
-        // 13.5 14.5 10.7 17.4 44; 1024 x 4096 x 4096 57 52 37 22 42; 1327 x 249 x
-        // 896 5.5 5.0 6.2 7.3 17; 836 x 7175 x 1024 46 46 35 13 19.
-        const double cost[5] = {tile_cost(g, 32, 32, 2.2, 0.86), tile_cost(g, 32, 64, 1.1, 2.3),
-                                tile_cost(g, 64, 64, 2.3, 2.1), tile_cost(g, 128, 128, 2.0, 2.0),
-                                tile_cost(g, 256, 256, 2.7, 8.6)};
-        switch (std::min_element(cost, cost + 5) - cost) {
+        // The tile with the least time.  A CU takes in its rows at a rate that hardly
+        // depends on the tile, so small ones cost most a product; large ones leave
+        // CUs idle.  Measured (us, the tiles in this order): 333 x 2047 x 4096 13.6
+        // 15.0 10.4 13.7 17.9 44; 1007 x 1217 x 7168 33 31 29 22 29 71; 1024 x 4096 x
+        // 4096 56 52 37 26 23 42; 481 x 2434 x 960 11.6 12.6 11.4 7.0 8.3 19.2.
+        const double cost[6] = {tile_cost(g, 32, 32, 87, 2.3, 0.88), tile_cost(g, 32, 64, 87, 1.4, 2.6),
+                                tile_cost(g, 64, 64, 87, 1.9, 2.5), tile_cost(g, 64, 128, 87, 1.8, 1.9),
+                                tile_cost(g, 128, 128, 61, 2.25, 1.8), tile_cost(g, 256, 256, 87, 1.7, 7.7)};
+        switch (std::min_element(cost, cost + 6) - cost) {
             case 0: return launch_split<T, 1, 1, 4>(g, dma, stream);
             case 1: return launch_split<T, 1, 2, 4>(g, dma, stream);
             case 2: return launch_split<T, 2, 2, 4>(g, dma, stream);
-            case 3:
-                return launch_middle<T, sizeof(T) == 2 ? 4 : 2>(g, dma, stream);
+            case 3: return launch_tile<T, 2, 4, 1, 1, 3>(g, dma, stream);
+            case 4: return launch_middle<T, sizeof(T) == 2 ? 4 : 2>(g, dma, stream);
             default:
+                // 16 waves end a tile sooner, 8 read fewer fragments a product: 1029 x
+                // 12114 x 2240 39.3 and 42.4 us, 5626 x 5808 x 3840 131 and 128.  (The end
+                // of 16 with outputs of 32 bits has no room in the ring.)
+                if constexpr (sizeof(T) == 2) {
+                    if (g.k <= 2560) return launch_tile<T, 4, 4, 2, 2, 2>(g, dma, stream);
+                }
                 return launch_tile<T, 2, 4, 4, 2, 2>(g, dma, stream);
         }
     }

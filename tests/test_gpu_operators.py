@@ -292,6 +292,16 @@ def test_gemm_tiles(m, n, k, dtype):
     check_gemm(m, n, k, TYPES[dtype], k % 2 == 0)
 
 
+@pytest.mark.parametrize("m,n,k,dtype", [
+    # 32 x 64, 64 x 64, 64 x 128 and 256 x 256 (16 and 8 waves), on aligned rows and on others
+    (100, 3000, 2048, "bf16"), (90, 3100, 2037, "f32"), (300, 2000, 1040, "f16"), (300, 2000, 1029, "f32"),
+    (290, 2100, 1040, "f32"), (700, 1500, 2048, "bf16"), (600, 2000, 1029, "f16"), (700, 1500, 1040, "f32"),
+    (3900, 4000, 1312, "f16"), (3900, 4000, 1297, "bf16"), (4090, 4080, 2624, "bf16"), (4090, 4080, 2601, "f16")])
+def test_gemm_more_tiles(m, n, k, dtype):
+    say(f"gemm more tiles {m}x{n}x{k} {dtype}")
+    check_gemm(m, n, k, TYPES[dtype], k % 2 == 0)
+
+
 @pytest.mark.parametrize("m", [1, 6, 16, 40, 130, 300])
 @pytest.mark.parametrize("pads,leads", [((16, 32, 8), (16, 16, 8)), ((1, 0, 0), (0, 0, 0)), ((0, 3, 1), (1, 2, 1)),
                                         ((4, 4, 2), (4, 8, 4))])
