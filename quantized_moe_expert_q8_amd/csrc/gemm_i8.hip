@@ -178,8 +178,8 @@ struct OddPiece {
 // wave takes `steps` steps of 64 values (NS at most) a chunk; rows longer than
 // KW waves x NS steps are taken in chunks, with the tokens' part loaded for each.
 //
-// 5 x 131072 x 4096: 95 us, 5.7 TB/s (64 x 64 tiles: 132 us); 1 x 4096 x 4096:
-// 5.8 us in a graph (29 us), where the launch and one trip to memory are most
+// 5 x 131072 x 4096: 90 us, 6.0 TB/s (64 x 64 tiles: 132 us); 1 x 4096 x 4096:
+// 5.2 us in a graph (29 us), where the launch and one trip to memory are most
 // of it.
 template <typename T, int W, int KW, int NS, int TP, bool ODD>
 __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, int chunks) {
@@ -218,7 +218,15 @@ __global__ __launch_bounds__(W * 64) void k_gemm_i8_few(GemmArgs g, int steps, i
             }
         }
     };
-    auto channel = [&](int64_t round, int u) { return ((round * G + group) * TP + u) * 16; };
+    // Of each 256 rounds, blocks of one XCD (every 8th) take 32 that follow each
+    // other, so that the parts of a line of out meet in one L2 (where a round is
+    // less than a line: 5 x 131072 x 4096 f32 90 and 95.5 us, 8 tokens bf16 94 and
+    // 103; with 8 of each 64 1% slower).
+    const int64_t whole = G * TP < 4 ? rounds / 256 * 256 : 0;
+    auto channel = [&](int64_t round, int u) {
+        if (round < whole) round = (round & ~(int64_t)255) + (round & 7) * 32 + (round >> 3 & 31);
+        return ((round * G + group) * TP + u) * 16;
+    };
     auto load_w = [&](int64_t round, int c) {
         const int own = own_steps(c);
         w_shift = 0;
@@ -347,7 +355,14 @@ int launch_few(const GemmArgs& g, hipStream_t stream) {
     // Each wave takes as few steps in a row as 8 waves allow; past 8 steps a wave
     // the registers of 16 waves a CU are full, so such rows get 16 waves.
     if (all > 64) return launch_few_form<T, 16, 16, 8, 1>(g, (int)((all + 127) / 128), stream);
-    if (all > 32) return launch_few_form<T, 8, 8, 8, 1>(g, 1, stream);
+    // More tiles than CUs: 16 waves too, which split a tile's rows finer (5 x 9000 x
+    // 4096 13.6 and 11.5 us, 14 x 20000 x 2048 11.6 and 10.0; 1 x 4096 x 4096 5.35 and
+    // 5.6; 5 x 100000 x 1088, whose 17 steps leave waves idle, 23 and 28).
+    if (all > 32) {
+        if (g.n > 4096) return launch_few_form<T, 16, 16, 4, 1>(g, 1, stream);
+        return launch_few_form<T, 8, 8, 8, 1>(g, 1, stream);
+    }
+    if (all > 24 && g.n > 4096) return launch_few_form<T, 16, 16, 2, 1>(g, 1, stream);
     if (all > 16) return launch_few_form<T, 8, 8, 4, 1>(g, 1, stream);
     if (all > 8) return launch_few_form<T, 8, 8, 2, 1>(g, 1, stream);
     // Short rows leave a wave a load or two a tile, too few to keep memory busy

@@ -320,6 +320,13 @@ def test_gemm_few_tokens_off_dwords(m, n, k, leads):
     check_gemm(m, n, k, torch.float16, m % 2 == 0, (0, leads[1] - leads[0], 0), (*leads, 0))
 
 
+@pytest.mark.parametrize("m,n,k", [(5, 4096, 4096), (5, 4100, 4096), (16, 9000, 2240), (3, 8200, 3001), (7, 4097, 1600),
+                                   (16, 10000, 2048), (2, 5000, 1667), (1, 4099, 1537), (9, 5000, 1536)])
+def test_gemm_few_tokens_many_channels(m, n, k):
+    say(f"gemm few tokens {m}x{n}x{k}")
+    check_gemm(m, n, k, torch.bfloat16, m % 2 == 0)
+
+
 @pytest.mark.parametrize("m", [1, 20, 70, 260])
 def test_gemm_extreme_codes(m):
     """All -128 (the largest sums), at k past 65536 and at the longest."""
