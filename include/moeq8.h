@@ -573,7 +573,8 @@ int i8_quantize_rows(const void* x, int32_t dtype, int64_t n_rows, int64_t k, in
  *   bias fp32 [n] or NULL
  *   out  out_dtype [m][out_row_stride]
  * The sum is exact in int32; k <= MOEQ8_MAX_I8_K.  A row's result depends on
- * its own row of a alone, not on m.  All 256 codes are allowed. */
+ * its own row of a alone, not on m.  All 256 codes are allowed.  Rows that are
+ * not on a dword may be read in the whole dwords that they touch. */
 int gemm_i8(const int8_t* a, int64_t a_row_stride, const float* sa, const int8_t* b, int64_t b_row_stride,
             const float* sb, const float* bias, int64_t m, int64_t n, int64_t k, int32_t out_dtype,
             void* out, int64_t out_row_stride, void* stream);

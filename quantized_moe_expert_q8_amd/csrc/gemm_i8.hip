@@ -412,10 +412,10 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 // With DMA the loads go straight into LDS, which needs 16-byte aligned rows;
 // otherwise they pass through registers, at any alignment, and ST is 2.
 //
-// 8192 x 8192 x 4096 in tiles of 256: 235 us, 2340 TOP/s, the rate the card
-// holds in int8 products of this size (its clock falls under this load); the
-// same with rows of 4097 bytes 315 us.  The ends of the tiles, about 7 us
-// each, are what keeps short rows below that: 8192 x 8192 x 1024 81 us.
+// 8192 x 8192 x 4096 in tiles of 256: 235 to 253 us by the card, 2200 to 2340
+// TOP/s, the rate it holds in int8 products of this size (its clock falls under
+// this load); the same with rows of 4097 bytes 315 us.  The ends of the tiles,
+// about 7 us each, are what keeps short rows below that: 8192 x 8192 x 1024 87 us.
 template <typename T, int WM, int WN, int FU, int FV, int ST, bool DMA>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_i8_tile(GemmArgs g) {
     constexpr int BM = WM * FU * 32, BN = WN * FV * 32, WAVES = WM * WN, STAGE = (BM + BN) * 128;
