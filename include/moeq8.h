@@ -544,7 +544,8 @@ enum moeq8_dtype {
 
 /* RMS norm with the residual's addition and 8-bit outputs:
  *   s = fp32(x) + fp32(residual)                       (s = x without a residual)
- *   y = (s * inv) * w,  inv = fp32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits
+ *   y = (s * inv) * w,  inv = fp32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits,
+ *                       inv at most the largest finite value
  *   residual_out = dtype(s)
  *   scale, q     int8 rows:  scale = max|y| / 127 over the row, q = roundf(y / scale)
  *                on the fp32 quotient (halves away from zero), within +-127
@@ -552,9 +553,10 @@ enum moeq8_dtype {
  *   x, residual, residual_out  dtype [n_rows][...]; w dtype [k]
  * q and scale go together, as do residual and residual_out; q, xq or both are
  * wanted; xq needs k % 32 == 0.  residual_out may be x or residual itself (the
- * same rows).  A row or block of zeros has the scale 0 and zero codes.  A NaN
- * or an infinity in a row makes its scale NaN and its codes 0 (in xq: for
- * every block of the row); a finite row whose sum passes fp32 counts as such. */
+ * same rows).  A row or block of zeros has the scale 0 and zero codes (with
+ * eps = 0 too).  A NaN or an infinity in a row makes its scale NaN and its
+ * codes 0 (in xq: for every block of the row); a finite row whose sum passes
+ * fp32 counts as such. */
 int rms_norm_q8(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
                 void* residual_out, int64_t residual_out_row_stride, const void* w, int32_t dtype,
                 int64_t n_rows, int64_t k, double eps, int8_t* q, int64_t q_row_stride, float* scale,

@@ -59,14 +59,15 @@ def rms_norm_steps(x, w, eps, residual=None):
     with np.errstate(all="ignore"):
         s = np.asarray(x, F32) if residual is None else (np.asarray(x, F32) + np.asarray(residual, F32)).astype(F32)
         mean = np.sum(s.astype(np.float64) ** 2, axis=1, keepdims=True) / s.shape[1]
-        inv = (1.0 / np.sqrt(mean + eps)).astype(F32)
+        inv = np.minimum((1.0 / np.sqrt(mean + eps)).astype(F32), np.finfo(F32).max)      # NaN stays
         return s, ((s * inv).astype(F32) * np.asarray(w, F32)).astype(F32)
 
 
 def rms_norm_def(x, w, eps, residual=None):
-    """(s, y) in 64 bits."""
+    """(s, y) in 64 bits; y 0 for zero rows."""
     s = np.asarray(x, np.float64) + (0.0 if residual is None else np.asarray(residual, np.float64))
-    return s, s / np.sqrt(np.mean(s * s, axis=1, keepdims=True) + eps) * np.asarray(w, np.float64)
+    root = np.sqrt(np.mean(s * s, axis=1, keepdims=True) + eps)
+    return s, np.divide(s, root, out=np.zeros_like(s), where=root != 0) * np.asarray(w, np.float64)
 
 
 def gemm_i8_sums(a, b):

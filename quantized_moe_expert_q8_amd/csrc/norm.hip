@@ -2,7 +2,8 @@
 // rows without the norm.
 //
 //   s = f32(x) + f32(residual)          residual_out = T(s)
-//   y = (s * inv) * w                   inv = f32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits
+//   y = (s * inv) * w                   inv = f32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits;
+//                                       at most the largest finite value
 //   i8 rows:   d = max|y| / 127 over the row, codes roundf(y / d) on the fp32 quotient
 //   q8_1 rows: the block rule of q8_1_quantize_rows on y
 //
@@ -183,8 +184,11 @@ __device__ __forceinline__ void load_sum(float (&v)[VEC], const NormArgs& a, int
     }
 }
 
+// At most the largest finite value: with no eps to speak of, a row of zeros would
+// else be 0 * inf, and the padding of every row below the normal range too.
 __device__ __forceinline__ float inv_rms(double sum, int64_t k, double eps) {
-    return (float)(1.0 / sqrt(sum / (double)k + eps));
+    const float inv = (float)(1.0 / sqrt(sum / (double)k + eps));
+    return inv > __FLT_MAX__ ? __FLT_MAX__ : inv;
 }
 
 // Outputs of one vector: y, with d the row's scale when i8 rows are wanted.
