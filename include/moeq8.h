@@ -545,7 +545,7 @@ enum moeq8_dtype {
 /* RMS norm with the residual's addition and 8-bit outputs:
  *   s = fp32(x) + fp32(residual)                       (s = x without a residual)
  *   y = (s * inv) * w,  inv = fp32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits,
- *                       inv at most the largest finite value
+ *                       inv at most the largest finite value, NaN where an s is not finite
  *   residual_out = dtype(s)
  *   scale, q     int8 rows:  scale = max|y| / 127 over the row, q = roundf(y / scale)
  *                on the fp32 quotient (halves away from zero), within +-127

@@ -59,7 +59,8 @@ def rms_norm_steps(x, w, eps, residual=None):
     with np.errstate(all="ignore"):
         s = np.asarray(x, F32) if residual is None else (np.asarray(x, F32) + np.asarray(residual, F32)).astype(F32)
         mean = np.sum(s.astype(np.float64) ** 2, axis=1, keepdims=True) / s.shape[1]
-        inv = np.minimum((1.0 / np.sqrt(mean + eps)).astype(F32), np.finfo(F32).max)      # NaN stays
+        inv = np.minimum((1.0 / np.sqrt(mean + eps)).astype(F32), np.finfo(F32).max)
+        inv = np.where(np.isfinite(mean), inv, F32(np.nan))
         return s, ((s * inv).astype(F32) * np.asarray(w, F32)).astype(F32)
 
 

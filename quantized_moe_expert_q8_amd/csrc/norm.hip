@@ -3,7 +3,7 @@
 //
 //   s = f32(x) + f32(residual)          residual_out = T(s)
 //   y = (s * inv) * w                   inv = f32(1 / sqrt(mean(s^2) + eps)), the mean in 64 bits;
-//                                       at most the largest finite value
+//                                       at most the largest finite value, NaN where s is not finite
 //   i8 rows:   d = max|y| / 127 over the row, codes roundf(y / d) on the fp32 quotient
 //   q8_1 rows: the block rule of q8_1_quantize_rows on y
 //
@@ -185,9 +185,12 @@ __device__ __forceinline__ void load_sum(float (&v)[VEC], const NormArgs& a, int
 }
 
 // At most the largest finite value: with no eps to speak of, a row of zeros would
-// else be 0 * inf, and the padding of every row below the normal range too.
+// else be 0 * inf, and the padding of every row below the normal range too.  NaN
+// where the row holds an infinity (fp32 squares cannot pass 64 bits otherwise):
+// its reciprocal root is 0, which would make the row's other blocks valid zeros.
 __device__ __forceinline__ float inv_rms(double sum, int64_t k, double eps) {
     const float inv = (float)(1.0 / sqrt(sum / (double)k + eps));
+    if (!(sum < __builtin_inf())) return __builtin_nanf("");
     return inv > __FLT_MAX__ ? __FLT_MAX__ : inv;
 }
 

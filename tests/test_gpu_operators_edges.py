@@ -55,3 +55,30 @@ def test_norm_rows_below_the_normal_range_without_eps():
         q, d = ref.quantize_rows_steps(y)
         assert bool(torch.isfinite(got.scale).all())
         assert np.array_equal(got.scale.cpu().numpy(), d) and np.array_equal(got.q.cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,k", [(7, 64), (7, 1504), (7, 4128), (600, 4128), (7, 33024)])
+def test_norm_not_finite_in_every_block(rows, k, dtype):
+    """An infinity or a NaN anywhere in a row shows in all its scales and
+    blocks, and in no other row's."""
+    say(f"norm not finite {rows}x{k} {dtype}")
+    t = TYPES[dtype]
+    x, w, res = norm_inputs(rows, k, k, residual=True)
+    xt, wt, rt = (typed(a, t)[0].to(DEV) for a in (x, w, res))
+    want = moeq8.rms_norm_q8(xt, wt, residual=rt, fmt="both")
+    bad = {1: np.inf, 2: -np.inf, 4: np.nan}
+    for r, v in bad.items():
+        xt[r, (r * 37) % k] = v
+    rt[5, k - 1] = np.inf
+    got = moeq8.rms_norm_q8(xt, wt, residual=rt, fmt="both")
+    d, s, q = q81_fields(got.xq, rows)
+    wd, ws, wq = q81_fields(want.xq, rows)
+    scale = got.scale.cpu().numpy()
+    for r in range(rows):
+        if r in (1, 2, 4, 5):
+            assert np.isnan(scale[r]) and not got.q[r].any()
+            assert np.isnan(d[r]).all() and np.isnan(s[r]).all() and not q[r].any()
+        else:
+            assert scale[r] == float(want.scale[r]) and torch.equal(got.q[r], want.q[r])
+            assert np.array_equal(d[r], wd[r]) and np.array_equal(s[r], ws[r]) and np.array_equal(q[r], wq[r])
