@@ -556,7 +556,8 @@ enum moeq8_dtype {
  * same rows).  A row or block of zeros has the scale 0 and zero codes (with
  * eps = 0 too).  A NaN or an infinity in a row makes its scale NaN and its
  * codes 0 (in xq: for every block of the row); a finite row whose sum passes
- * fp32 counts as such. */
+ * fp32 counts as such.  A row's results depend on its own values alone, not on
+ * n_rows. */
 int rms_norm_q8(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
                 void* residual_out, int64_t residual_out_row_stride, const void* w, int32_t dtype,
                 int64_t n_rows, int64_t k, double eps, int8_t* q, int64_t q_row_stride, float* scale,

@@ -43,53 +43,89 @@ __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(
 __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
 template <int CTRL, typename V>
-__device__ __forceinline__ V moved(V v) {          // v of the lane that the DPP control names
+__device__ __forceinline__ V moved(V v) {          // v of the lane that the DPP control names, an active one
     if constexpr (sizeof(V) == 8) {
         const uint2 u = __builtin_bit_cast(uint2, v);
-        return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.x, CTRL, 0xf, 0xf, false),
-                                           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.y, CTRL, 0xf, 0xf, false)});
+        return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_mov_dpp((int)u.x, CTRL, 0xf, 0xf, false),
+                                           (uint32_t)__builtin_amdgcn_mov_dpp((int)u.y, CTRL, 0xf, 0xf, false)});
     } else {
-        return __builtin_bit_cast(V, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+        return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
     }
 }
 constexpr int XOR1 = 0xB1, XOR2 = 0x4E, HALF_MIRROR = 0x141, MIRROR = 0x140;
 
-template <typename V>
-__device__ __forceinline__ V of_lane(V v, int lane) {
-    if constexpr (sizeof(V) == 8) {
-        const uint2 u = __builtin_bit_cast(uint2, v);
-        return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_readlane((int)u.x, lane),
-                                           (uint32_t)__builtin_amdgcn_readlane((int)u.y, lane)});
-    } else {
-        return __builtin_bit_cast(V, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
-    }
-}
-
-// Over the lanes of a full wave, in registers: the 16 lanes of a row by DPP,
-// then the four rows.  (Through LDS, as __shfl_xor goes, the two reductions of
-// one row of 4096 took a seventh of its time.)
-template <typename V, typename F>
-__device__ __forceinline__ V wave_reduce(V v, F op) {
-    v = op(v, moved<XOR1>(v));
-    v = op(v, moved<XOR2>(v));
-    v = op(v, moved<HALF_MIRROR>(v));
-    v = op(v, moved<MIRROR>(v));
-    return op(op(of_lane(v, 0), of_lane(v, 16)), op(of_lane(v, 32), of_lane(v, 48)));
-}
-
-// Over the TPR threads of a row, in a fixed order; every thread gets the value.
-template <int TPR, typename V, typename F>
-__device__ __forceinline__ V row_reduce(V v, V* lds, F op) {
-    v = wave_reduce(v, op);
+// Largest over the TPR threads of a row; every thread gets it.  Over a full wave
+// in registers: the 16 lanes of a row by DPP, then the four rows.  (Through LDS,
+// as __shfl_xor goes, the reductions of one row of 4096 took a seventh of its
+// time.)
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* lds) {
+    v = larger(v, moved<XOR1>(v));
+    v = larger(v, moved<XOR2>(v));
+    v = larger(v, moved<HALF_MIRROR>(v));
+    v = larger(v, moved<MIRROR>(v));
+    auto of_row = [&](int r) { return (uint32_t)__builtin_amdgcn_readlane((int)v, 16 * r); };
+    v = larger(larger(of_row(0), of_row(1)), larger(of_row(2), of_row(3)));
     if constexpr (TPR > 64) {
-        constexpr int W = TPR / 64;
         if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
         lds_barrier();
         v = lds[0];
 #pragma unroll
-        for (int i = 1; i < W; ++i) v = op(v, lds[i]);
+        for (int i = 1; i < TPR / 64; ++i) v = larger(v, lds[i]);
     }
     return v;
+}
+
+// Lower halves of a wave's a and b beside the upper ones: {a.lo, b.lo} + {a.hi,
+// b.hi}; or rows of 16 lanes: {a0, b0, a2, b2} + {a1, b1, a3, b3}.
+template <bool HALVES>
+__device__ __forceinline__ double added_crosswise(double a, double b) {
+    auto swap = [](uint32_t x, uint32_t y) {
+        if constexpr (HALVES) return __builtin_amdgcn_permlane32_swap(x, y, false, false);
+        else return __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    };
+    const uint2 x = __builtin_bit_cast(uint2, a), y = __builtin_bit_cast(uint2, b);
+    const auto lo = swap(x.x, y.x), hi = swap(x.y, y.y);
+    return __builtin_bit_cast(double, uint2{lo[0], hi[0]}) + __builtin_bit_cast(double, uint2{lo[1], hi[1]});
+}
+
+// Sum over LANES lanes (a power of two), in every group of as many.
+template <int LANES>
+__device__ __forceinline__ double lanes_sum(double v) {
+    if constexpr (LANES >= 2) v += moved<XOR1>(v);
+    if constexpr (LANES >= 4) v += moved<XOR2>(v);
+    if constexpr (LANES >= 8) v += moved<HALF_MIRROR>(v);
+    if constexpr (LANES >= 16) v += moved<MIRROR>(v);
+    if constexpr (LANES >= 32) v = added_crosswise<false>(v, v);
+    if constexpr (LANES >= 64) v = added_crosswise<true>(v, v);
+    return v;
+}
+
+// Sum over a row, of which thread t of TPR has the sums of its vectors i * TPR +
+// t; every thread gets it.  The order is that of spans of 64 vectors, each
+// summed over its lanes, and of a tree over the spans: the same for every TPR,
+// since the form goes by the number of rows too and a row's outputs are not to
+// depend on it.  (With a thread's NV sums added first, a row among 2049 could
+// differ from the same row alone.)  The NV spans of a wave go through one tree,
+// in its halves or rows of lanes: with a tree each, 3000 x 16384 in fp16 took
+// 77 us and not 58, 16000 x 4096 in bf16 to q8_1 rows 61 and not 58.5.
+template <int TPR, int NV>
+__device__ __forceinline__ double row_sum(const double (&v)[NV], double* lds) {
+    static_assert(NV <= 4 && (TPR > 64 || NV == 1), "a row of lanes a span");
+    double u = added_crosswise<true>(v[0], v[NV > 1 ? 1 : 0]);
+    if constexpr (NV > 2) u = added_crosswise<false>(u, added_crosswise<true>(v[2], NV > 3 ? v[NV - 1] : 0.0));
+    else u = added_crosswise<false>(u, u);
+    u = lanes_sum<16>(u);
+    if constexpr (TPR > 64) {
+        constexpr int W = TPR / 64, SPANS = NV * W, SLOTS = SPANS <= 2 ? 2 : SPANS <= 4 ? 4 : SPANS <= 8 ? 8 : SPANS <= 16 ? 16
+                                                               : SPANS <= 32 ? 32 : 64;
+        const int lane = threadIdx.x & 63, i = (lane >> 4 & 1) << 1 | lane >> 5;       // the span that this row of lanes has
+        if ((lane & 15) == 0 && i < NV) lds[i * W + (threadIdx.x >> 6)] = u;
+        lds_barrier();
+        const int slot = lane & (SLOTS - 1);
+        u = lanes_sum<SLOTS>(SLOTS == SPANS || slot < SPANS ? lds[slot] : 0.0);
+    }
+    return u;
 }
 
 // Codes of 8 values of scale d, packed; their sum.  d = 0 and a d that is not
@@ -190,8 +226,7 @@ __device__ __forceinline__ void load_sum(float (&v)[VEC], const NormArgs& a, int
 // its reciprocal root is 0, which would make the row's other blocks valid zeros.
 __device__ __forceinline__ float inv_rms(double sum, int64_t k, double eps) {
     const float inv = (float)(1.0 / sqrt(sum / (double)k + eps));
-    if (!(sum < __builtin_inf())) return __builtin_nanf("");
-    return inv > __FLT_MAX__ ? __FLT_MAX__ : inv;
+    return fminf(inv, __FLT_MAX__) + (float)(sum - sum);        // 0, or NaN
 }
 
 // Outputs of one vector: y, with d the row's scale when i8 rows are wanted.
@@ -230,7 +265,7 @@ __device__ __forceinline__ void store_codes(const NormArgs& a, const float (&y)[
 // i * TPR + thread of the row, so a wave's loads are contiguous).
 template <typename T, bool NORM, int TPR, int NV>
 __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
-    __shared__ double lds_sum[TPR / 64];
+    __shared__ double lds_sum[NV * TPR / 64];
     __shared__ uint32_t lds_max[TPR / 64];
     constexpr int RPB = TPR == 64 ? 4 : 1;
     const int t = threadIdx.x & (TPR - 1);
@@ -238,7 +273,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
     if (r >= a.rows) return;                       // whole waves; with barriers a block is one row
     float v[NV][VEC];
     T wt[NORM ? NV : 1][VEC];
-    double sq = 0.0;
+    double sq[NV] = {};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int64_t at = (int64_t)i * TPR + t;
@@ -255,12 +290,11 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
         if (a.res) store8((T*)a.res_out + r * a.res_out_stride + at * VEC, v[i], n);
         if constexpr (NORM) {
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sq += (double)v[i][j] * (double)v[i][j];
+            for (int j = 0; j < VEC; ++j) sq[i] += (double)v[i][j] * (double)v[i][j];
         }
     }
     if constexpr (NORM) {
-        sq = row_reduce<TPR>(sq, lds_sum, [](double p, double q) { return p + q; });
-        const float inv = inv_rms(sq, a.k, a.eps);
+        const float inv = inv_rms(row_sum<TPR>(sq, lds_sum), a.k, a.eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -275,7 +309,7 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) m = larger(m, magnitude(v[i][j]));
         }
-        m = row_reduce<TPR>(m, lds_max, larger);
+        m = row_max<TPR>(m, lds_max);
         d = __uint_as_float(m) / 127.0f;
         if (t == 0) a.scale[r] = d;
     }
@@ -299,16 +333,15 @@ __global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {
     const int64_t nvec = (a.k + VEC - 1) / VEC;
     float inv = 1.0f;
     if constexpr (NORM) {
-        double sq = 0.0;
+        double sq[1] = {};
         for (int64_t at = threadIdx.x; at < nvec; at += 1024) {
             float v[VEC];
             const int n = (int)(a.k - at * VEC < VEC ? a.k - at * VEC : VEC);
             load_sum<T>(v, a, r, at, n);
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) sq += (double)v[j] * (double)v[j];
+            for (int j = 0; j < VEC; ++j) sq[0] += (double)v[j] * (double)v[j];
         }
-        sq = row_reduce<1024>(sq, lds_sum, [](double p, double q) { return p + q; });
-        inv = inv_rms(sq, a.k, a.eps);
+        inv = inv_rms(row_sum<1024>(sq, lds_sum), a.k, a.eps);
     }
     auto row_y = [&](float (&v)[VEC], int64_t at, int n) {
         load_sum<T>(v, a, r, at, n);
@@ -329,7 +362,7 @@ __global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {
 #pragma unroll
             for (int j = 0; j < VEC; ++j) m = larger(m, magnitude(v[j]));
         }
-        m = row_reduce<1024>(m, lds_max, larger);
+        m = row_max<1024>(m, lds_max);
         d = __uint_as_float(m) / 127.0f;
         if (threadIdx.x == 0) a.scale[r] = d;
     }

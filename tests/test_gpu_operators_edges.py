@@ -82,3 +82,47 @@ def test_norm_not_finite_in_every_block(rows, k, dtype):
         else:
             assert scale[r] == float(want.scale[r]) and torch.equal(got.q[r], want.q[r])
             assert np.array_equal(d[r], wd[r]) and np.array_equal(s[r], ws[r]) and np.array_equal(q[r], wq[r])
+
+
+def near_a_rounding(k, far):
+    """A row of k values whose sum of squares lies so near the border between
+    two fp32 reciprocals of its root that the order of the sum decides: three
+    values that make up the border and eight at `far`, whose squares are each
+    below half a step of that sum but not together."""
+    g = np.random.default_rng(k)
+    while True:
+        inv = np.float32(0.5 + g.random())
+        border = (float(inv) + float(np.nextafter(inv, np.float32(2)))) / 2
+        want = k / border**2
+        row = np.zeros(k, np.float32)
+        total = 0.0
+        for i in range(3):
+            row[i] = np.float32(np.sqrt(max(want - total, 0)) * (1 - 2.0**-24))
+            total += float(row[i]) ** 2
+        small = np.float32(np.sqrt(np.spacing(total) * 0.49))
+        one = total
+        for _ in range(8):
+            one += float(small) ** 2                       # one at a time: nothing
+        both = total + 8 * float(small) ** 2               # together: four steps
+        f = [np.float32(1 / np.sqrt(v / k)) for v in (one, both)]
+        y = [np.float32(row[0] * v) / np.float32(127) for v in f]
+        if one == total and y[0] != y[1]:
+            row[far:far + 8] = small
+            return row
+
+
+@pytest.mark.parametrize("k,far", [(2048, 1024), (4096, 2048), (6144, 2048), (8192, 4096), (12288, 4096)])
+def test_norm_rows_do_not_depend_on_their_number(k, far):
+    """Every form of the kernel sums a row's squares in the same order: a row
+    has the same outputs alone, among a few and among thousands."""
+    say(f"norm batch invariance {k}")
+    row = np.stack([near_a_rounding(k, far)] + [norm_inputs(1, k, s, residual=False)[0][0] for s in range(15)])
+    w = torch.ones(k, device=DEV)
+    x = torch.from_numpy(row.astype(np.float32)).to(DEV)
+    one = moeq8.rms_norm_q8(x, w, eps=0.0, fmt="both")
+    for rows in (513, 2049):
+        many = moeq8.rms_norm_q8(x.repeat(rows // 16 + 1, 1)[:rows], w, eps=0.0, fmt="both")
+        for a, b in ((many.scale, one.scale), (many.q, one.q), (many.xq, one.xq)):
+            a, b = a.view(torch.int32 if a.dtype == torch.float32 else a.dtype), \
+                b.view(torch.int32 if b.dtype == torch.float32 else b.dtype)
+            assert torch.equal(a[:16], b) and torch.equal(a[-(rows % 16) - 16:][:16], b)
