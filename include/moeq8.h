@@ -533,7 +533,8 @@ int q4_pack64_rows(const void* src, int64_t n_rows, int64_t k, int64_t src_row_s
  * elements, row strides in elements (>= the row's length); any row length is
  * accepted where none is named.  Arithmetic is fp32 unless stated; a value is
  * rounded to its output type once, to the nearest even.  Outputs must not
- * overlap inputs, except where a call says so.  Values that are not finite
+ * overlap inputs, except where a call says so (rows that take turns in one
+ * buffer, at one stride, do not overlap).  Values that are not finite
  * have the results given at each call.
  * ------------------------------------------------------------------------- */
 enum moeq8_dtype {

@@ -311,10 +311,7 @@ extern "C" int logits_process(const void* logits, int64_t logits_row_stride, int
         return MOEQ8_EALIGN;
     if (((uintptr_t)begin | (uintptr_t)end | (uintptr_t)prompt_end | (uintptr_t)bias_offsets) & 7u) return MOEQ8_EALIGN;
     if (n_rows == 0 || vocab == 0) return MOEQ8_OK;
-    if (!(logits == out && logits_row_stride == out_row_stride) &&
-        ranges_overlap(logits, ((n_rows - 1) * logits_row_stride + vocab) * es, out,
-                       ((n_rows - 1) * out_row_stride + vocab) * es))
-        return MOEQ8_EINVAL;
+    if (rows_clash(logits, logits_row_stride * es, out, out_row_stride * es, n_rows, vocab * es)) return MOEQ8_EINVAL;
     const LogitsArgs a{logits, logits_row_stride, out, out_row_stride, vocab, tokens, n_tokens, begin, end, prompt_end,
                        repetition, frequency, presence, bias_ids, bias_values, n_bias, bias_offsets,
                        mask, mask_row_stride};

@@ -26,4 +26,15 @@ inline bool ranges_overlap(const void* p, int64_t p_bytes, const void* q, int64_
     return a < b + q_bytes && b < a + p_bytes;
 }
 
+// Whether rows of `bytes` bytes at p and at o overlap otherwise than by being the
+// same rows, where each element is read before it is written.  Rows of one
+// stride may take turns in a buffer.
+inline bool rows_clash(const void* p, int64_t p_stride, const void* o, int64_t o_stride, int64_t rows, int64_t bytes) {
+    if (p == o && (p_stride == o_stride || rows == 1)) return false;
+    if (!ranges_overlap(p, (rows - 1) * p_stride + bytes, o, (rows - 1) * o_stride + bytes)) return false;
+    if (p_stride != o_stride) return true;
+    const int64_t apart = ((const uint8_t*)o - (const uint8_t*)p) % p_stride, behind = apart < 0 ? apart + p_stride : apart;
+    return behind < bytes || p_stride - behind < bytes;
+}
+
 }  // namespace moeq8

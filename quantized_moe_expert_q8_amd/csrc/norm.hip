@@ -420,13 +420,6 @@ int launch_dtype(int32_t dtype, const NormArgs& a, void* stream) {
     }
 }
 
-// Whether two row ranges overlap otherwise than by being the same rows (each
-// thread reads its own elements before it writes them, so in place is fine).
-bool clash(const void* p, int64_t p_stride, const void* o, int64_t o_stride, int64_t rows, int64_t k, int es) {
-    if (p == o && p_stride == o_stride) return false;
-    return ranges_overlap(p, ((rows - 1) * p_stride + k) * es, o, ((rows - 1) * o_stride + k) * es);
-}
-
 }  // namespace
 }  // namespace moeq8
 
@@ -445,8 +438,8 @@ extern "C" int rms_norm_q8(const void* x, int64_t x_row_stride, const void* resi
         return MOEQ8_EALIGN;
     if (((uintptr_t)scale | (uintptr_t)xq) & 3u) return MOEQ8_EALIGN;
     if (n_rows == 0) return MOEQ8_OK;
-    if (residual && (clash(x, x_row_stride, residual_out, residual_out_row_stride, n_rows, k, es) ||
-                     clash(residual, residual_row_stride, residual_out, residual_out_row_stride, n_rows, k, es)))
+    if (residual && (rows_clash(x, x_row_stride * es, residual_out, residual_out_row_stride * es, n_rows, k * es) ||
+                     rows_clash(residual, residual_row_stride * es, residual_out, residual_out_row_stride * es, n_rows, k * es)))
         return MOEQ8_EINVAL;
     NormArgs a{x, x_row_stride, residual, residual_row_stride, residual_out, residual_out_row_stride, w,
                n_rows, k, eps, q, q_row_stride, scale, (uint8_t*)xq};

@@ -126,3 +126,30 @@ def test_norm_rows_do_not_depend_on_their_number(k, far):
             a, b = a.view(torch.int32 if a.dtype == torch.float32 else a.dtype), \
                 b.view(torch.int32 if b.dtype == torch.float32 else b.dtype)
             assert torch.equal(a[:16], b) and torch.equal(a[-(rows % 16) - 16:][:16], b)
+
+
+# ---- rows of two tensors in one buffer ----------------------------------------------
+
+def test_rows_beside_each_other_in_one_buffer():
+    """Inputs and outputs whose rows take turns in one buffer do not overlap."""
+    say("rows beside each other")
+    rows, k = 5, 96
+    buf = torch.randn(rows, 2 * k + 4, device=DEV)
+    x, beside = buf[:, :k], buf[:, k + 4:]
+    w, res = torch.ones(k, device=DEV), torch.randn(rows, k, device=DEV)
+    want = moeq8.rms_norm_q8(x.clone(), w, residual=res)
+    got = moeq8.rms_norm_q8(x, w, residual=res, residual_out=beside)
+    assert torch.equal(beside, want.residual) and torch.equal(got.q, want.q) and torch.equal(x + res, beside)
+    want = moeq8.rms_norm_q8(res, w, residual=x.clone())
+    got = moeq8.rms_norm_q8(res, w, residual=x, residual_out=beside)
+    assert torch.equal(beside, want.residual) and torch.equal(got.q, want.q)
+    bias = dict(bias_ids=torch.tensor([1] * rows, dtype=torch.int32, device=DEV), bias_values=torch.ones(rows, device=DEV),
+                bias_offsets=torch.arange(rows + 1, device=DEV))
+    want = moeq8.logits_process(x.clone(), **bias)
+    assert torch.equal(moeq8.logits_process(x, out=beside, **bias), want) and torch.equal(beside, want)
+    for o in (buf[:, 1:k + 1], buf[:, k - 1:2 * k - 1]):
+        with pytest.raises(moeq8.MoeQ8Error):
+            moeq8.logits_process(x, out=o)
+        with pytest.raises(moeq8.MoeQ8Error):
+            moeq8.rms_norm_q8(x, w, residual=res, residual_out=o)
+    torch.cuda.synchronize()

@@ -5,7 +5,12 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
+import quantized_moe_expert_q8_amd as moeq8  # noqa: E402
 from oracle import operators_ref as ref  # noqa: E402
+
+# fake, never-dereferenced addresses: skipped where a GPU could take a launch
+P, Q, R = 0x10000, 0x10000000, 0x20000000
+cpu_only = pytest.mark.skipif(torch.cuda.is_available(), reason="host-validation calls use fake pointers")
 
 
 def test_norm_zero_rows():
@@ -25,3 +30,25 @@ def test_norm_not_finite_in_every_value():
     _, y = ref.rms_norm_steps(x, np.ones(64), 1e-6)
     d, _, q = ref.q8_1_steps(y)
     assert np.isfinite(d[0]).all() and np.isnan(d[1:]).all() and not q[1:].any()
+
+
+@cpu_only
+def test_rows_that_take_turns_in_a_buffer_are_no_overlap():
+    """Accepted by the host (the launch then fails without a GPU), beside rows
+    that do overlap."""
+    norm, logits = moeq8.lib().rms_norm_q8, moeq8.lib().logits_process
+
+    def residual(res, rs, out, os, rows=3):
+        return norm(P, 200, res, rs, out, os, Q, 0, rows, 64, 1e-6, R, 64, R, None, None)
+
+    def rules(out, stride, rows=3):
+        return logits(P, 200, 0, rows, 64, None, 0, None, None, None, None, None, None, None, None, 0, None, None, 0,
+                      out, stride, None)
+
+    for off in (64, 100, 136, -64, -136, 264, -264):                # elements, rows 200 apart
+        assert residual(Q, 64, P + 4 * off, 200) == rules(P + 4 * off, 200) == -4
+        assert residual(P + 4 * off, 200, P + 4 * off, 200) == -4
+    for off in (1, 63, 137, 199, 200, -1, -63, -200, 263):
+        assert residual(Q, 64, P + 4 * off, 200) == rules(P + 4 * off, 200) == -1
+    assert residual(Q, 64, P + 400, 100) == rules(P + 400, 100) == -1               # at another stride
+    assert residual(P, 300, P, 500, rows=1) == rules(P, 500, rows=1) == -4          # one row is the same row
