@@ -43,6 +43,7 @@ struct LogitsArgs {
 };
 
 constexpr int AHEAD = 4;                           // loads of 4 tokens a thread has in flight
+typedef uint16_t half_t __attribute__((may_alias));
 
 __device__ __forceinline__ int64_t clamp64(int64_t v, int64_t lo, int64_t hi) {
     return v < lo ? lo : (v > hi ? hi : v);
@@ -87,8 +88,8 @@ __global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a, uint32_t rows,
     static_assert(NV * VEC * THREADS == TILE, "whole vectors");
     __shared__ __attribute__((aligned(16))) T tile[TILE];
     __shared__ __attribute__((aligned(16))) uint32_t count[TILE / 2];   // written tokens: 16 bits each, or 32 of half a tile
-    __shared__ uint32_t seen[TILE / 32], biased[TILE / 32];         // a bit each token
-    __shared__ int repeated;                       // a token has more than one bias
+    __shared__ uint32_t seen[TILE / 32], biased[TILE / 32], again[TILE / 32];   // a bit each token; again: more than one bias
+    __shared__ int repeated;                       // any bit of again
     // All rows' first tiles come first: where frequent tokens have low ids, those
     // take longest, and the last rows' would be the last to end.
     uint32_t r = blockIdx.x, tile_no = 0;
@@ -163,11 +164,68 @@ __global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a, uint32_t rows,
         // A count of 16 bits holds a list of 65535; a longer one is taken in two
         // halves of the tile, with counts of 32 bits.
         const bool wide = length - written > 65535u;
+        // The tokens with more than one bias.  A token's are added in the list's
+        // order, so one wave has all of a token's (those of every WAVES-th word of
+        // the bits) and goes through the list.  That is read once, however many
+        // repeat: 50000 biases on 131072 fp32 logits take 53 us where all differ, 157
+        // where one or all come twice (with a search of the list for each such
+        // token 270000).  Between two additions the value is kept in fp32: for 16-bit
+        // elements its low half is where the token's count was.
+        auto add_repeated = [&](auto place, auto penalised) {
+            constexpr int WAVES = THREADS / 64, WORDS = TILE / 32 / WAVES, LOADS = 2;
+            static_assert(WORDS <= 64, "a word a lane");
+            uint32_t id = tid;
+            asm volatile("" : "+v"(id));           // or what is made of it takes registers from the start, and waves from the CU
+            const uint32_t wave = __builtin_amdgcn_readfirstlane(id >> 6), lane = id & 63;
+            auto low_half = [&](uint32_t at) -> half_t& {
+                return reinterpret_cast<half_t*>(count)[wide ? 2 * (at & (TILE / 2 - 1)) : at];
+            };
+            auto value = [&](uint32_t at) {
+                if constexpr (sizeof(T) == 4) return tile[at];
+                else return __uint_as_float((uint32_t)tile[at].bits << 16 | low_half(at));
+            };
+            auto hold = [&](uint32_t at, float v) {
+                if constexpr (sizeof(T) == 4) {
+                    tile[at] = v;
+                } else {
+                    tile[at].bits = (uint16_t)(__float_as_uint(v) >> 16);
+                    low_half(at) = (uint16_t)__float_as_uint(v);
+                }
+            };
+            auto each = [&](auto f) {              // this lane's tokens
+                const uint32_t word = wave + lane * WAVES;
+                for (uint32_t left = lane < WORDS ? again[word] : 0u; left; left &= left - 1) f(word * 32 + __builtin_ctz(left));
+            };
+            each([&](uint32_t at) { hold(at, seen[at >> 5] >> (at & 31) & 1 ? penalised(at) : to_f32(tile[at])); });
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // for the wave's other lanes
+            for (uint32_t first = 0; first < biases; first += 64 * LOADS) {
+                uint32_t at[LOADS];
+                float add[LOADS];
+#pragma unroll
+                for (int n = 0; n < LOADS; ++n) {
+                    const uint32_t i = first + n * 64 + lane < biases ? first + n * 64 + lane : biases - 1;
+                    at[n] = (uint32_t)bias_ids[i];
+                    add[n] = bias_values[i];
+                }
+#pragma unroll
+                for (int n = 0; n < LOADS; ++n) {
+                    at[n] = place((int32_t)at[n]);
+                    const bool own = first + n * 64 + lane < biases && at[n] != TILE && (at[n] >> 5) % WAVES == wave &&
+                                     (again[at[n] >> 5] >> (at[n] & 31) & 1);
+                    for (uint64_t left = __ballot(own); left; left &= left - 1) {
+                        const int l = __builtin_ctzll(left);       // all lanes write the same
+                        const uint32_t to = __builtin_amdgcn_readlane((int)at[n], l);
+                        hold(to, value(to) + __uint_as_float(__builtin_amdgcn_readlane(__float_as_int(add[n]), l)));
+                    }
+                }
+            }
+            if constexpr (sizeof(T) == 2) each([&](uint32_t at) { from_f32(tile[at], value(at)); });
+        };
         for (uint32_t from = low, to; from < high; from = to) {
             to = wide && from < TILE / 2 && high > TILE / 2 ? TILE / 2 : high;
 #pragma unroll
             for (int n = tid; n < TILE / 8; n += THREADS) reinterpret_cast<uint4*>(count)[n] = uint4{0u, 0u, 0u, 0u};
-            for (int n = tid; n < TILE / 32; n += THREADS) seen[n] = biased[n] = 0u;
+            for (int n = tid; n < TILE / 32; n += THREADS) seen[n] = biased[n] = again[n] = 0u;
             if (tid == 0) repeated = 0;
             lds_barrier();
             // position of a token in this part of the tile, or one past it
@@ -203,7 +261,10 @@ __global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a, uint32_t rows,
             }
             for (uint32_t i = tid; i < biases; i += THREADS) {
                 const uint32_t at = place(i == tid ? bias_id : bias_ids[i]), bit = 1u << (at & 31);
-                if (at < TILE && (atomicOr(&biased[at >> 5], bit) & bit)) repeated = 1;
+                if (at < TILE && (atomicOr(&biased[at >> 5], bit) & bit)) {
+                    atomicOr(&again[at >> 5], bit);
+                    repeated = 1;
+                }
             }
             lds_barrier();
             auto penalised = [&](uint32_t at) {
@@ -222,22 +283,13 @@ __global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a, uint32_t rows,
                 from_f32(tile[at], penalised(at));
             }
             if (biases) {
-                const bool again = repeated;
-                if (again) lds_barrier();          // the bits are cleared below
                 for (uint32_t i = tid; i < biases; i += THREADS) {
-                    const int32_t token = i == tid ? bias_id : bias_ids[i];
-                    const uint32_t at = place(token), bit = 1u << (at & 31);
-                    if (at == TILE) continue;
-                    if (again && !(atomicAnd(&biased[at >> 5], ~bit) & bit)) continue;   // one thread a token
-                    float v = seen[at >> 5] & bit ? penalised(at) : to_f32(tile[at]);
-                    if (!again) {
-                        v += i == tid ? bias_value : bias_values[i];
-                    } else {                       // all of the token's, in the list's order
-                        for (uint32_t j = 0; j < biases; ++j)
-                            if (bias_ids[j] == token) v += bias_values[j];
-                    }
-                    from_f32(tile[at], v);
+                    const uint32_t at = place(i == tid ? bias_id : bias_ids[i]);
+                    if (at == TILE || again[at >> 5] >> (at & 31) & 1) continue;
+                    const float v = seen[at >> 5] >> (at & 31) & 1 ? penalised(at) : to_f32(tile[at]);
+                    from_f32(tile[at], v + (i == tid ? bias_value : bias_values[i]));
                 }
+                if (__builtin_expect(repeated, 0)) add_repeated(place, penalised);
             }
             lds_barrier();
         }
@@ -321,3 +373,4 @@ extern "C" int logits_process(const void* logits, int64_t logits_row_stride, int
         default: return launch_logits<bf16_t>(a, n_rows, (hipStream_t)stream);
     }
 }
+

@@ -153,3 +153,81 @@ def test_rows_beside_each_other_in_one_buffer():
         with pytest.raises(moeq8.MoeQ8Error):
             moeq8.rms_norm_q8(x, w, residual=res, residual_out=o)
     torch.cuda.synchronize()
+
+
+# ---- logits ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,vocab,lead", [(2, 20011, 3), (2, 4100, 1), (345, 9001, 2)])
+def test_logits_long_counts_over_tiles(rows, vocab, lead, dtype):
+    """More than 65535 written tokens over tiles taken in two halves, tokens
+    and biases (repeated ones too) on both sides of every border."""
+    say(f"logits long counts {rows}x{vocab} {dtype}")
+    g = np.random.default_rng(vocab)
+    edge = np.array([0, 1, 1023, 1024, 2045, 2046, 2047, 2048, 2049, 4093, 4094, 4095, 4096, 4097, 8190, 8192, vocab - 1])
+    edge = edge[edge < vocab]
+    tokens = np.concatenate([np.full(66000, edge[5]), g.choice(edge, 3000), g.integers(0, vocab, 1500)]).astype(np.int32)
+    g.shuffle(tokens)
+    z = (3 * g.standard_normal((rows, vocab))).astype(np.float32)
+    begin, end = np.zeros(rows, np.int64), np.full(rows, 30, np.int64)
+    end[[0, 1]] = [len(tokens), len(tokens) - 7]
+    kw = dict(tokens=tokens, begin=begin, end=end, prompt_end=np.minimum(begin + 5, end),
+              repetition=(1 + 0.3 * g.random(rows)).astype(np.float32),
+              frequency=(0.01 * g.random(rows)).astype(np.float32), presence=(0.5 * g.random(rows)).astype(np.float32))
+    some = lambda: [(int(t), float(np.float32(g.standard_normal()))) for t in g.choice(edge, 40)]
+    bias = [some() if r < 6 else [] for r in range(rows)]
+    mask = g.integers(-2**31, 2**31, (rows, (vocab + 31) // 32)).astype(np.int32)
+    check_logits(z, TYPES[dtype], kw, bias, mask, (1, 2), (lead, 0))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,history,lead", [(2, 300, 0), (1, 3000, 1), (70, 40, 3)])
+def test_logits_many_repeated_biases(rows, history, lead, dtype):
+    """Long lists in which tokens have one bias, two and hundreds; each token's
+    are added in the list's order."""
+    say(f"logits repeated biases {rows} {history} {dtype}")
+    vocab = 30011
+    g = np.random.default_rng(history)
+    z, kw, _, mask = logits_inputs(rows, vocab, history, history)
+    bias = []
+    for r in range(rows):
+        if r >= 3:
+            bias.append([(int(g.integers(0, vocab)), 1.0)] * (r % 3))
+            continue
+        ids = np.concatenate([g.integers(0, vocab, 700), g.integers(0, 64, 900), np.full(300, 4095), np.full(300, 2048),
+                              g.integers(8000, 8400, 600), np.array([-1, -3, vocab, vocab + 2, 2**31 - 1])])
+        g.shuffle(ids)
+        bias.append([(int(t), float(np.float32(v))) for t, v in zip(ids, g.standard_normal(len(ids)) * 3)])
+    check_logits(z, TYPES[dtype], kw, bias, mask, (2, 1), (lead, 0))
+    check_logits(z, TYPES[dtype], {}, bias, None, (2, 1), (lead, 0))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_logits_repeated_biases_cost_no_more_than_the_list(dtype):
+    """A list of 50000 biases with one token twice, and one with all of them
+    twice, take a small multiple of the time of one without repetitions."""
+    say(f"logits repeated biases, time {dtype}")
+    vocab, n = 131072, 50000
+    z = torch.randn(1, vocab, device=DEV).to(TYPES[dtype])
+    ids = torch.randperm(vocab, device=DEV)[:n].int()
+    one, all_twice = ids.clone(), torch.cat([ids[:n // 2], ids[:n // 2]])
+    one[-1] = one[0]
+    values, at = torch.randn(n, device=DEV), torch.tensor([0, n], device=DEV)
+    out = torch.empty_like(z)
+
+    def time(t):
+        best = float("inf")
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            moeq8.logits_process(z, bias_ids=t, bias_values=values, bias_offsets=at, out=out)
+            a.record()
+            for _ in range(5):
+                moeq8.logits_process(z, bias_ids=t, bias_values=values, bias_offsets=at, out=out)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) / 5 * 1e3)
+        return best
+
+    took = {name: time(t) for name, t in (("distinct", ids), ("one twice", one), ("all twice", all_twice))}
+    say(f"{took} us")
+    assert took["one twice"] <= 20 * took["distinct"] and took["all twice"] <= 20 * took["distinct"]
