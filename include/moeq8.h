@@ -530,12 +530,13 @@ int q4_pack64_rows(const void* src, int64_t n_rows, int64_t k, int64_t src_row_s
  * products beside it and the rules on the logits behind it.
  *
  * Rows are fp32, fp16 or bf16 (enum moeq8_dtype) at the alignment of their
- * elements, row strides in elements (>= the row's length); any row length is
- * accepted where none is named.  Arithmetic is fp32 unless stated; a value is
+ * elements, row strides in elements (>= the row's length); any row length
+ * from 1 on is accepted where none is named.  Arithmetic is fp32 unless stated; a value is
  * rounded to its output type once, to the nearest even.  Outputs must not
  * overlap inputs, except where a call says so (rows that take turns in one
  * buffer, at one stride, do not overlap).  Values that are not finite
- * have the results given at each call.
+ * have the results given at each call.  Calls whose grid would pass 2^32
+ * threads (8 million rows of 8192 values) are MOEQ8_EUNSUPPORTED.
  * ------------------------------------------------------------------------- */
 enum moeq8_dtype {
     MOEQ8_F32 = 0,

@@ -618,7 +618,7 @@ template <typename T, int WM, int WN, int FU, int FV, int ST>
 int launch_tile(const GemmArgs& g, bool dma, hipStream_t stream) {
     constexpr int BM = WM * FU * 32, BN = WN * FV * 32;
     const int64_t blocks = ((g.m + BM - 1) / BM) * ((g.n + BN - 1) / BN);
-    if (blocks > 0x0fffffff) return MOEQ8_EUNSUPPORTED;       // 8 * tiles_n within 32 bits
+    if (blocks > most_blocks(WM * WN * 64)) return MOEQ8_EUNSUPPORTED;
     if (dma)
         hipLaunchKernelGGL((k_gemm_i8_tile<T, WM, WN, FU, FV, ST, true>), dim3((uint32_t)blocks), dim3(WM * WN * 64), 0,
                            stream, g);
@@ -801,7 +801,7 @@ __global__ __launch_bounds__(512) void k_gemm_i8_split(GemmArgs g) {
 template <typename T, int FU, int FV, int ST>
 int launch_split(const GemmArgs& g, bool dma, hipStream_t stream) {
     const int64_t blocks = ((g.m + FU * 32 - 1) / (FU * 32)) * ((g.n + FV * 32 - 1) / (FV * 32));
-    if (blocks > 0x0fffffff) return MOEQ8_EUNSUPPORTED;
+    if (blocks > most_blocks(512)) return MOEQ8_EUNSUPPORTED;
     if (dma)
         hipLaunchKernelGGL((k_gemm_i8_split<T, FU, FV, ST, true>), dim3((uint32_t)blocks), dim3(512), 0, stream, g);
     else
@@ -868,7 +868,7 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
         }
     }
     const int64_t blocks = ((g.m + 63) / 64) * ((g.n + 63) / 64);
-    if (blocks > 0x7fffffff) return MOEQ8_EUNSUPPORTED;
+    if (blocks > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
     hipLaunchKernelGGL(k_gemm_i8<T>, dim3((uint32_t)blocks), dim3(256), 0, stream, g);
     return check_launch();
 }

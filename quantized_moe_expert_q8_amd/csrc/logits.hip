@@ -315,7 +315,7 @@ __global__ __launch_bounds__(THREADS) void k_logits(LogitsArgs a, uint32_t rows,
 template <typename T, int THREADS, int TILE>
 int launch_form(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
     const int64_t tiles = (a.vocab + 16 / (int64_t)sizeof(T) - 1 + TILE - 1) / TILE;     // with a shifted first tile
-    if (rows > 0x7fffffff / tiles) return MOEQ8_EUNSUPPORTED;
+    if (rows > most_blocks(THREADS) / tiles) return MOEQ8_EUNSUPPORTED;
     hipLaunchKernelGGL((k_logits<T, THREADS, TILE>), dim3((uint32_t)(rows * tiles)), dim3(THREADS), 0, stream, a, (uint32_t)rows,
                        (uint32_t)tiles);
     return check_launch();

@@ -17,6 +17,9 @@ inline int check_launch() {
     return e == hipSuccess ? MOEQ8_OK : MOEQ8_EHIP;
 }
 
+// Most blocks of a launch: HIP counts a grid's threads in 32 bits.
+inline int64_t most_blocks(int64_t threads) { return 0xffffffffll / threads; }
+
 // Bytes of one element of an enum moeq8_dtype.
 inline int dtype_bytes(int32_t dtype) { return dtype == MOEQ8_F32 ? 4 : 2; }
 

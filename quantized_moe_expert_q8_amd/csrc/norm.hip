@@ -382,7 +382,7 @@ template <typename T, bool NORM, int TPR, int NV>
 int launch(const NormArgs& a, hipStream_t stream) {
     constexpr int RPB = TPR == 64 ? 4 : 1;
     const int64_t blocks = (a.rows + RPB - 1) / RPB;
-    if (blocks > 0x7fffffff) return MOEQ8_EUNSUPPORTED;
+    if (blocks > most_blocks(RPB * TPR)) return MOEQ8_EUNSUPPORTED;
     hipLaunchKernelGGL((k_norm_q8<T, NORM, TPR, NV>), dim3((uint32_t)blocks), dim3(RPB * TPR), 0, stream, a);
     return check_launch();
 }
@@ -406,7 +406,7 @@ int launch_rows(const NormArgs& a, hipStream_t stream) {
     if (a.k <= 12288 && many) return launch<T, NORM, 512, 3>(a, stream);
     if (a.k <= 16384) return launch<T, NORM, 1024, 2>(a, stream);
     if (a.k <= 32768) return launch<T, NORM, 1024, 4>(a, stream);
-    if (a.rows > 0x7fffffff) return MOEQ8_EUNSUPPORTED;
+    if (a.rows > most_blocks(1024)) return MOEQ8_EUNSUPPORTED;
     hipLaunchKernelGGL((k_norm_q8_long<T, NORM>), dim3((uint32_t)a.rows), dim3(1024), 0, stream, a);
     return check_launch();
 }

@@ -52,3 +52,28 @@ def test_rows_that_take_turns_in_a_buffer_are_no_overlap():
         assert residual(Q, 64, P + 4 * off, 200) == rules(P + 4 * off, 200) == -1
     assert residual(Q, 64, P + 400, 100) == rules(P + 400, 100) == -1               # at another stride
     assert residual(P, 300, P, 500, rows=1) == rules(P, 500, rows=1) == -4          # one row is the same row
+
+
+@cpu_only
+def test_grids_past_32_bits_are_refused():
+    """Before a launch (which without a GPU fails with -4)."""
+    rows, norm, gemm, logits = (getattr(moeq8.lib(), n) for n in
+                                ("i8_quantize_rows", "rms_norm_q8", "gemm_i8", "logits_process"))
+    big = 1 << 40
+    for n, k, fits in ((1 << 26, 8, False), ((1 << 26) - 4, 8, True), (1 << 24, 4096, False), ((1 << 23) - 1, 8192, True),
+                       (1 << 22, 40000, False), ((1 << 22) - 1, 40000, True)):
+        assert rows(P, 0, n, k, k, Q + big, k, R + 2 * big, None) == (-4 if fits else -3), (n, k)
+    assert norm(P, 8, None, 0, None, 0, Q, 0, 1 << 26, 8, 0.0, Q + big, 8, R + 2 * big, None, None) == -3
+
+    def rules(n, vocab):
+        return logits(P, vocab, 2, n, vocab, None, 0, None, None, None, None, None, None, None, None, 0, None, None, 0,
+                      Q + big, vocab, None)
+
+    assert rules(1 << 23, 8) == rules(1 << 21, 32000) == -3 and rules((1 << 23) - 1, 8) == -4
+
+    def product(m, n, k):
+        return gemm(P, k, Q + big, R + 2 * big, k, Q + big, None, m, n, k, 2, P + 3 * big, n, None)
+
+    # blocks of 512 threads on 256 x 256, of 256 threads on 64 x 64
+    assert product(1 << 20, 1 << 20, 64) == product(1 << 18, 1 << 18, 8) == -3
+    assert product((1 << 18) - 64, 1 << 18, 8) == -4
