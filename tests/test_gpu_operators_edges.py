@@ -128,6 +128,29 @@ def test_norm_rows_do_not_depend_on_their_number(k, far):
             assert torch.equal(a[:16], b) and torch.equal(a[-(rows % 16) - 16:][:16], b)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,k,fmt", [(2049, 1056, "q8_1"), (2049, 2047, "i8"), (513, 4064, "q8_1"), (513, 4095, "i8"),
+                                        (513, 6112, "both"), (520, 6141, "i8"), (513, 8160, "q8_1"), (513, 8191, "i8"),
+                                        (513, 12256, "both"), (514, 12287, "i8")])
+def test_norm_forms_of_many_rows_by_type(rows, k, fmt, residual, dtype):
+    say(f"norm form {rows}x{k} {fmt} {dtype} residual={residual}")
+    x, w, res = norm_inputs(rows, k, rows + k, residual)
+    check_norm(x, w, res, TYPES[dtype], fmt)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,k", [(2049, 2047), (513, 4095), (520, 6141), (513, 8191), (513, 12287), (1030, 64)])
+def test_rows_forms_of_many_rows(rows, k, dtype):
+    say(f"rows form {rows}x{k} {dtype}")
+    xt, xv = typed(np.random.default_rng(k).standard_normal((rows, k)) * 3, TYPES[dtype])
+    qbuf, q = framed(rows, k, torch.int8, 3, 1)
+    got, scale = moeq8.i8_quantize_rows(put(xt, 1, 2), q=q)
+    qs, d = ref.quantize_rows_steps(xv)
+    assert np.array_equal(scale.cpu().numpy(), d) and np.array_equal(got.cpu().numpy(), qs)
+    assert frame_kept(qbuf, rows, k, 3, 1)
+
+
 # ---- rows of two tensors in one buffer ----------------------------------------------
 
 def test_rows_beside_each_other_in_one_buffer():
@@ -155,7 +178,54 @@ def test_rows_beside_each_other_in_one_buffer():
     torch.cuda.synchronize()
 
 
+# ---- int8 product ---------------------------------------------------------------------
+
+@pytest.mark.parametrize("m,n,k", [
+    # tiles of 32 x 32, 32 x 64, 64 x 64, 64 x 128, 128 x 128 in three stages and in two (many channels for few
+    # tokens, as in a vocabulary head), 256 x 256
+    (20, 40, 144), (100, 2100, 400), (130, 4000, 1040), (100, 2100, 144), (70, 17000, 144), (70, 33000, 144),
+    (17, 40000, 256), (700, 17000, 144)])
+@pytest.mark.parametrize("cut", [0, 7])
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_gemm_every_tile_in_every_type(m, n, k, cut, dtype):
+    """On rows of whole 16 bytes and on others."""
+    say(f"gemm tiles {m}x{n}x{k - cut} {dtype}")
+    check_gemm(m, n, k - cut, TYPES[dtype], m % 20 == 0)
+
+
+@pytest.mark.parametrize("m,n,k,dtype", [(1, 1, 15, "f32"), (16, 70, 8, "bf16"), (17, 70, 3, "f32"), (64, 64, 15, "f16"),
+                                         (130, 200, 7, "bf16"), (300, 129, 12, "f32"), (65, 66, 1, "f16"),
+                                         (257, 1000, 15, "bf16")])
+@pytest.mark.parametrize("bias", [False, True])
+def test_gemm_rows_of_under_sixteen(m, n, k, dtype, bias):
+    say(f"gemm short {m}x{n}x{k} {dtype}")
+    check_gemm(m, n, k, TYPES[dtype], bias)
+    check_gemm(m, n, k, TYPES[dtype], bias, (3, 1, 5), (1, 2, 3))
+
+
+@pytest.mark.parametrize("pads", [((1 << 23) - 200, 0, 0), (0, 1 << 23, 3), ((1 << 23) + 1, (1 << 23) + 5, 0)])
+def test_gemm_rows_far_apart(pads):
+    """Rows 8 MB apart, for tiles (through the plain kernel) and for few tokens."""
+    say(f"gemm far rows {pads}")
+    check_gemm(20, 70, 200, torch.float32, True, pads)
+    check_gemm(5, 40, 331, torch.bfloat16, False, pads)
+
+
 # ---- logits ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("pads,leads", [((0, 0), (0, 0)), ((5, 2), (1, 3))])
+def test_logits_many_rows(dtype, pads, leads):
+    """More blocks than run at a time: two vectors a thread."""
+    say(f"logits many rows {dtype} {pads}")
+    rows, vocab = (60, 40001) if dtype == "f32" else (110, 40001)
+    z, kw, bias, mask = logits_inputs(rows, vocab, 60, 21, biases=6)
+    bias[3] = [(7, 1.5), (4099, -2.0), (7, 0.25), (8191, 3.0), (8192, 1.0), (8191, 1.0)]
+    check_logits(z, TYPES[dtype], kw, bias, mask, pads, leads)
+    check_logits(z, TYPES[dtype], kw, bias, None, pads, leads, inplace=True)
+    check_logits(z, TYPES[dtype], {}, None, mask, pads, leads)
+    check_logits(z, TYPES[dtype], {}, None, None, pads, leads)
+
 
 @pytest.mark.parametrize("dtype", list(TYPES))
 @pytest.mark.parametrize("rows,vocab,lead", [(2, 20011, 3), (2, 4100, 1), (345, 9001, 2)])
