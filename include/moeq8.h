@@ -530,13 +530,13 @@ int q4_pack64_rows(const void* src, int64_t n_rows, int64_t k, int64_t src_row_s
  * products beside it and the rules on the logits behind it.
  *
  * Rows are fp32, fp16 or bf16 (enum moeq8_dtype) at the alignment of their
- * elements, row strides in elements (>= the row's length); any row length
- * from 1 on is accepted where none is named.  Arithmetic is fp32 unless stated; a value is
- * rounded to its output type once, to the nearest even.  Outputs must not
- * overlap inputs, except where a call says so (rows that take turns in one
- * buffer, at one stride, do not overlap).  Values that are not finite
- * have the results given at each call.  Calls whose grid would pass 2^32
- * threads (8 million rows of 8192 values) are MOEQ8_EUNSUPPORTED.
+ * elements, row strides in elements (>= the row's length); any row length from
+ * 1 on is accepted where none is named.  Arithmetic is fp32 unless stated; a
+ * value is rounded to its output type once, to the nearest even.  Outputs must
+ * not overlap inputs, except where a call says so (rows that take turns in one
+ * buffer, at one stride, do not overlap).  Values that are not finite have the
+ * results given at each call.  Calls whose grid would pass 2^32 threads (8
+ * million rows of 8192 values) are MOEQ8_EUNSUPPORTED.
  * ------------------------------------------------------------------------- */
 enum moeq8_dtype {
     MOEQ8_F32 = 0,
@@ -558,8 +558,9 @@ enum moeq8_dtype {
  * same rows).  A row or block of zeros has the scale 0 and zero codes (with
  * eps = 0 too).  A NaN or an infinity in a row makes its scale NaN and its
  * codes 0 (in xq: for every block of the row); a finite row whose sum passes
- * fp32 counts as such.  A row's results depend on its own values alone, not on
- * n_rows. */
+ * fp32 counts as such.  Where w takes a y past fp32, the scale (in xq: its
+ * block's) is infinite and the codes are 0.  A row's results depend on its own
+ * values alone, not on n_rows. */
 int rms_norm_q8(const void* x, int64_t x_row_stride, const void* residual, int64_t residual_row_stride,
                 void* residual_out, int64_t residual_out_row_stride, const void* w, int32_t dtype,
                 int64_t n_rows, int64_t k, double eps, int8_t* q, int64_t q_row_stride, float* scale,

@@ -412,10 +412,11 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 // With DMA the loads go straight into LDS, which needs 16-byte aligned rows;
 // otherwise they pass through registers, at any alignment, and ST is 2.
 //
-// 8192 x 8192 x 4096 in tiles of 256: 235 to 253 us by the card, 2200 to 2340
+// 8192 x 8192 x 4096 in tiles of 256: 240 to 256 us by the card, 2150 to 2290
 // TOP/s, the rate it holds in int8 products of this size (its clock falls under
-// this load); the same with rows of 4097 bytes 315 us.  The ends of the tiles,
-// about 7 us each, are what keeps short rows below that: 8192 x 8192 x 1024 87 us.
+// this load; right after a pause 290 us); the same with rows of 4097 bytes 315 us.
+// The ends of the tiles, about 7 us each, are what keeps short rows below that:
+// 8192 x 8192 x 1024 83 to 87 us, x 256 43 to 47 (its bytes take 27).
 template <typename T, int WM, int WN, int FU, int FV, int ST, bool DMA>
 __global__ __launch_bounds__(WM * WN * 64) void k_gemm_i8_tile(GemmArgs g) {
     constexpr int BM = WM * FU * 32, BN = WN * FV * 32, WAVES = WM * WN, STAGE = (BM + BN) * 128;
@@ -815,7 +816,11 @@ int launch_split(const GemmArgs& g, bool dma, hipStream_t stream) {
 // the matrix cores do at the clock they hold (two thirds of peak).  The
 // constants are fitted to the times of the six tiles on 66 products of 17 to
 // 8192 tokens, 64 to 16384 channels and k = 128 to 8192, where the tile chosen
-// was the best one in each (within 1% on average for rows off 16 bytes).
+// was the best one in each (within 1% on average for rows off 16 bytes).  More
+// channels were not among them, and nothing here stands for the memory that a
+// head of many channels comes from: 17, 32, 64 and 256 x 131072 x 4096 take 120,
+// 120, 124 and 167 us, where the rate of a large copy would allow 104 to 116 (the
+// last 133 by its operations).
 double tile_cost(const GemmArgs& g, int bm, int bn, double rate, double start, double end) {
     const double tiles = (double)((g.m + bm - 1) / bm) * (double)((g.n + bn - 1) / bn), k = (double)g.k;
     const double rounds = (double)((int64_t)((tiles + 255) / 256));
@@ -829,8 +834,8 @@ double tile_cost(const GemmArgs& g, int bm, int bn, double rate, double start, d
 // 4096 x 4096 44 and 40.  (Four stages were no faster: 800 x 3873 x 3488 20.6 and
 // 20.1.)  With outputs of 16 bits a wave's part is 32 x 64, whose rows in out are
 // whole lines: the same product 20.6 us, in parts of 64 x 32 21.4.  (In tiles of
-// 256 the higher parts are better: 8192 x 8192 x 4096 272-280 us sustained, in
-// parts of 64 x 128 284-290.)
+// 256 the higher parts are better: 8192 x 8192 x 4096 without a pause 248 us, in
+// parts of 64 x 128 253.)
 template <typename T, int WM>
 int launch_middle(const GemmArgs& g, bool dma, hipStream_t stream) {
     if (((g.m + 127) / 128) * ((g.n + 127) / 128) <= 256) return launch_tile<T, WM, 8 / WM, 4 / WM, WM / 2, 3>(g, dma, stream);
@@ -859,8 +864,11 @@ int launch_gemm(const GemmArgs& g, hipStream_t stream) {
             case 4: return launch_middle<T, sizeof(T) == 2 ? 4 : 2>(g, dma, stream);
             default:
                 // 16 waves end a tile sooner, 8 read fewer fragments a product: 1029 x
-                // 12114 x 2240 39.3 and 42.4 us, 5626 x 5808 x 3840 131 and 128.  (The end
-                // of 16 with outputs of 32 bits has no room in the ring.)
+                // 12114 x 2240 40.3 and 41.2 us, 5626 x 5808 x 3840 131 and 128.  (The end
+                // of 16 with outputs of 32 bits has no room in the ring.)  On rows off 16
+                // bytes 16 waves have 4 registers too few and keep them in memory, which
+                // costs what they gain: 4090 x 4080 x 2001 49.1 and 47.3 us, x 1297 38.7 and
+                // 38.5, 1029 x 12114 x 2233 50.1 and 50.8.
                 if constexpr (sizeof(T) == 2) {
                     if (g.k <= 2560) return launch_tile<T, 4, 4, 2, 2, 2>(g, dma, stream);
                 }

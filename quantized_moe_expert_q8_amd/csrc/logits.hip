@@ -324,12 +324,15 @@ int launch_form(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
 template <typename T>
 int launch_logits(const LogitsArgs& a, int64_t rows, hipStream_t stream) {
     // More blocks of 512 threads than run at a time, 4 a CU: a thread takes two
-    // vectors (220 x 19809 bf16 8.0 and 9.9 us, 16 x 131072 f32 8.9 and 9.6, but
-    // 91 x 21061 f32, 1001 blocks, 8.2 and 7.7; 256 x 131072 bf16 with 2048 tokens
-    // a row 39 us).  Fewer: what counts is how soon one block is done, so a thread
-    // takes one vector, and blocks of long lists are larger (5 x 131072 f32 with
-    // 8192 tokens a row: 256 threads 9.1, 512 7.2, 1024 6.3 us; 32 x 32000 bf16
-    // with 1000: 5.6, 5.4, 5.7).
+    // vectors (us, with two and with one: 17 x 131072 f32, 1088 blocks, 8.2 and 9.5;
+    // 220 x 19809 bf16 9.8 and 10.9; 256 x 131072 bf16 with 2048 tokens a row 39 and
+    // 55; but 91 x 21061 f32, 1001 blocks, 8.0 and 7.7; 1024 blocks to the block,
+    // 16 x 131072 f32, would still be better with two, 7.8 and 8.5).  Fewer: what
+    // counts is how soon one block is done, so a thread takes one vector, and blocks
+    // of long lists are larger (5 x 131072 f32 with 8192 tokens a row: 512 threads
+    // 7.0, 1024 6.3 us; 32 x 32000 bf16 with 1000: 5.8 and 6.1).  The lists' own
+    // lengths are on the device: rows that share a list count as having a part of it
+    // each (8 x 100000 f32 on one list of 8000 tokens 7.2 us, in larger blocks 6.6).
     constexpr int VEC = 16 / sizeof(T);
     const int64_t tiles = (a.vocab + 512 * VEC - 1) / (512 * VEC);
     if (rows > 1024 / tiles) return launch_form<T, 512, 1024 * VEC>(a, rows, stream);

@@ -12,9 +12,10 @@
 // a half.  One pass over the data: a thread keeps its 8-value vectors of s in
 // registers between the two row reductions, so x and the residual are read
 // once, and the weights are loaded with them.  What bounds it is the memory
-// traffic: 8192 x 8192 in bf16 with a residual takes 87 us, 5.4 TB/s, the rate
-// of a large copy; without a residual and with both formats the arithmetic of
-// the codes comes near it (16000 x 4096 72 us, 3.8 TB/s).  For few rows it is
+// traffic: 8192 x 8192 in bf16 with a residual takes 84 to 86 us, 5.5 TB/s, the
+// rate of a large copy.  Without a residual the arithmetic of the q8_1 codes is
+// more than that (16000 x 4096 to q8_1 rows 59 us, 3.5 TB/s, to both formats 73,
+// 3.7 TB/s; with a residual 86 and 102 us, 5.4 and 5.3 TB/s).  For few rows it is
 // the launch: 3.1 us for one of 4096.
 #include "moeq8_lds.hpp"
 #include "moeq8_types.hpp"
@@ -322,8 +323,9 @@ __global__ __launch_bounds__(TPR == 64 ? 256 : TPR) void k_norm_q8(NormArgs a) {
     }
 }
 
-// Rows longer than the registers of one block hold: three passes over the
-// row.  Each thread comes back to its own vectors, and residual_out is written
+// Rows longer than the registers of one block hold: three passes over the row
+// (53248 values in bf16 with a residual: one row 18 us, 1000 rows 115, 3.2 TB/s;
+// without the norm, in two passes, 6.5 and 43 us, 3.7 TB/s).  Each thread comes back to its own vectors, and residual_out is written
 // in the last pass, so it may be the residual or x itself.
 template <typename T, bool NORM>
 __global__ __launch_bounds__(1024) void k_norm_q8_long(NormArgs a) {

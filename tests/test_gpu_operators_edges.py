@@ -84,6 +84,24 @@ def test_norm_not_finite_in_every_block(rows, k, dtype):
             assert np.array_equal(d[r], wd[r]) and np.array_equal(s[r], ws[r]) and np.array_equal(q[r], wq[r])
 
 
+def test_norm_weights_past_the_largest_value():
+    """An infinite y makes the row's scale and its own block's infinite, and
+    their codes 0; the other blocks stand."""
+    say("norm weights past fp32")
+    x, w, _ = norm_inputs(3, 4128, 5, residual=False)
+    w[70], x[:, 70] = 3e38, [0.0, 30.0, -40.0]
+    (xt, xv), (wt, wv) = (typed(a, torch.float32) for a in (x, w))
+    got = moeq8.rms_norm_q8(xt.to(DEV), wt.to(DEV), fmt="both")
+    _, y = ref.rms_norm_steps(xv, wv, 1e-6)
+    q, d = ref.quantize_rows_steps(y)
+    bd, bs, bq = q81_fields(got.xq, 3)
+    ed, es, eq = ref.q8_1_steps(y)
+    assert np.array_equal(got.scale.cpu().numpy(), d) and np.array_equal(got.q.cpu().numpy(), q)
+    assert np.array_equal(bd, ed) and np.array_equal(bq, eq) and np.array_equal(np.isnan(bs), np.isnan(es))
+    assert np.isinf(d).tolist() == np.isinf(bd[:, 2]).tolist() == [False, True, True]
+    assert not q[1:].any() and not bq[1:, 2].any() and bq[1:, 0].any() and np.isfinite(bd[1:, [0, 1, 3]]).all()
+
+
 def near_a_rounding(k, far):
     """A row of k values whose sum of squares lies so near the border between
     two fp32 reciprocals of its root that the order of the sum decides: three
