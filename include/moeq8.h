@@ -67,6 +67,7 @@ extern "C" {
 #define MOEQ8_EXCHANGE_BLOCK_BYTES 36
 #define MOEQ8_Q4_BLOCK_BYTES 18
 #define MOEQ8_MAX_I8_K 131071      /* values of one gemm_i8 sum: exact in int32 */
+#define MOEQ8_MAX_HEAD_DIM 256     /* values of a row of the key/value cache */
 
 enum moeq8_status {
     MOEQ8_OK = 0,
@@ -609,6 +610,113 @@ int logits_process(const void* logits, int64_t logits_row_stride, int32_t dtype,
                    const float* presence, const int32_t* bias_ids, const float* bias_values, int64_t n_bias,
                    const int64_t* bias_offsets, const int32_t* mask, int64_t mask_row_stride, void* out,
                    int64_t out_row_stride, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * From a step's hidden states to its tokens: a paged cache of keys and values in
+ * int8, the attention that reads it, and the draw of a token.  Element types,
+ * row strides, roundings and the limit of a grid's threads are as above; all
+ * strides are at least the length of what they step over.
+ *
+ * The cache holds pages of page_size positions; the row of a (position, head) is
+ * d int8 codes of one fp32 scale each for the key and the value, by the rule of
+ * i8_quantize_rows.  A slot is page * page_size + place in the page.
+ *   k, v              int8; the row of page p, head h, place t lies at
+ *                     p * page_stride + h * head_stride + t * token_stride bytes
+ *   k_scale, v_scale  fp32, at p * scale_page_stride + h * scale_head_stride + t
+ *                     elements
+ * page_size is a power of two from 16 on, d a multiple of 16 up to
+ * MOEQ8_MAX_HEAD_DIM.  Pointers and byte strides are multiples of 16 bytes,
+ * scale strides of 4 elements (a stride along one page, head or place does not
+ * count).  Slots and pages outside the cache are nowhere an error: what each
+ * call does with them is said there.
+ * ------------------------------------------------------------------------- */
+typedef struct moeq8_kv_cache {
+    int8_t* k;
+    float* k_scale;
+    int8_t* v;
+    float* v_scale;
+    int64_t n_pages, n_heads, page_size, d;
+    int64_t page_stride, head_stride, token_stride;      /* bytes */
+    int64_t scale_page_stride, scale_head_stride;        /* elements */
+} moeq8_kv_cache;
+
+/* Keys and values of n_tokens tokens into their slots:
+ *   k, v   dtype [n_tokens][n_heads][d], at token and head strides in elements
+ *   slots  int64 [n_tokens]; a token whose slot is outside the cache is skipped
+ * A slot that comes twice holds bytes of either token.  The cache must not
+ * overlap k and v.  `cache` is read on the host, during the call. */
+int kv_cache_write_i8(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
+                      int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
+                      const int64_t* slots, const moeq8_kv_cache* cache, void* stream);
+
+/* Rows of the cache as values: out = dtype(fp32(code * scale)), zeros for a slot
+ * outside the cache.  Arguments as above, k_out and v_out the outputs; slots may
+ * come more than once. */
+int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t n_tokens, int32_t dtype,
+                     void* k_out, int64_t k_token_stride, int64_t k_head_stride, void* v_out,
+                     int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/* Attention of a step's columns over the cache:
+ *   out[s][c][a] = sum_i softmax_i(scale * q[s][c][a] . k_i) v_i
+ * over the positions i < visible[s][c] of sequence s, for key head a / (n_q_heads /
+ * n_heads); a column that sees nothing gives zeros.  The scales of k_i and v_i
+ * multiply the finished product and the weight.
+ *   q, out    dtype [n_seqs][n_cols][n_q_heads][d], at strides in elements; out
+ *             must not overlap q or the cache
+ *   pages     int32 [n_seqs][pages_row_stride]: position i lies in page
+ *             pages[s][i / page_size]; n_table entries a sequence.  The positions
+ *             of a page outside the cache are not seen.
+ *   visible   int32 [n_seqs][n_cols], taken within 0 .. min(max_visible, n_table *
+ *             page_size); for causal columns of a sequence of n positions, the
+ *             columns the last ones, visible[s][c] = n - (n_cols - 1 - c)
+ *   max_visible  what the host knows of the longest; work is split by it, so a
+ *             close bound is faster.  The results' roundings depend on it too.
+ *   scale     finite; the inner products' factor (commonly d^-0.5)
+ * n_q_heads is a multiple of n_heads, 1 <= n_cols <= MOEQ8_MAX_COLS, max_visible <
+ * 2^30.  Scores and sums are fp32; fp32 queries and the weights of fp32 and fp16
+ * outputs go through the matrix cores as two fp16 parts (22 bits), bf16 outputs'
+ * weights as one (11 bits).  Codes outside of what is seen do not matter, nor do
+ * their scales; a scale or query that is not finite follows IEEE arithmetic in the
+ * rows that see it and touches no others (infinite sums may come out as NaN).
+ *   workspace  at least paged_attention_workspace_bytes() bytes, 16-byte aligned
+ *             (NULL where that is 0).  It holds nothing between calls; calls that
+ *             may run at the same time need one each.
+ * paged_attention_workspace_bytes: 0 also for arguments that the call refuses. */
+size_t paged_attention_workspace_bytes(int64_t n_seqs, int64_t n_cols, int64_t n_q_heads, int64_t n_heads, int64_t d,
+                                       int64_t max_visible);
+int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q_col_stride, int64_t q_head_stride, int32_t dtype,
+                       int64_t n_seqs, int64_t n_cols, int64_t n_q_heads, const moeq8_kv_cache* cache,
+                       const int32_t* pages, int64_t pages_row_stride, int64_t n_table, const int32_t* visible,
+                       int64_t max_visible, double scale, void* out, int64_t out_seq_stride, int64_t out_col_stride,
+                       int64_t out_head_stride, void* workspace, size_t workspace_bytes, void* stream);
+
+/* A token for each row of logits, from the given number u[r] in [0, 1):
+ *   weights   w_i = exp((z_i - max z) / temperature[r]) in 64 bits; 0 for -inf and
+ *             NaN; where the largest is +inf, 1 for those and 0 for the others;
+ *             temperature 0: the token of the largest logit (the first of equals)
+ *   order     by falling logit, equals by their index
+ *   top-k     the first top_k[r] of the order are kept (<= 0: all)
+ *   top-p     of these, those before which there is less than top_p[r] of their
+ *             mass (>= 1: all); always the first
+ *   min-p     of these, those with w >= min_p[r]; always the first
+ *   draw      in the order of the indexes, the first kept token up to which there
+ *             is more than u[r] of the kept mass
+ *   logits       dtype [n_rows][...]
+ *   temperature, top_p, min_p  fp32 [n_rows], top_k int32 [n_rows]; NULL: 1, 1, 0, 0
+ *   token        int32 [n_rows]: -1 for a row without a token to draw
+ *   logprob      fp32 [n_rows] or NULL: log(w / kept mass) of the token drawn; -inf
+ *                for a row without
+ * A temperature that is negative or NaN counts as 0; a NaN of the others, or of u,
+ * as their NULL or 0.  Weights are held to 2^-63 of the row's largest sum, and sums
+ * are exact, so a result does not depend on the number of rows or on the form taken.
+ * vocab < 2^30.
+ *   workspace  at least logits_sample_workspace_bytes() bytes, 16-byte aligned, as
+ *             above. */
+size_t logits_sample_workspace_bytes(int64_t n_rows, int64_t vocab);
+int logits_sample(const void* logits, int64_t logits_row_stride, int32_t dtype, int64_t n_rows, int64_t vocab,
+                  const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                  const float* min_p, int32_t* token, float* logprob, void* workspace, size_t workspace_bytes,
+                  void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,17 @@ c_i32, c_i64, c_u32, c_u64 = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ct
 c_vp, c_fp, c_size = ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t
 c_f64 = ctypes.c_double
 
+
+
+class KvCache(ctypes.Structure):
+    """struct moeq8_kv_cache"""
+    _fields_ = [("k", c_vp), ("k_scale", c_vp), ("v", c_vp), ("v_scale", c_vp),
+                *((n, c_i64) for n in ("n_pages", "n_heads", "page_size", "d", "page_stride", "head_stride",
+                                       "token_stride", "scale_page_stride", "scale_head_stride"))]
+
+
+c_cache = ctypes.POINTER(KvCache)
+
 # name -> (restype, argtypes); one entry per declaration in include/moeq8.h and
 # include/moeq8_synth.h
 SIGNATURES = {
@@ -68,6 +79,14 @@ SIGNATURES = {
                                c_i64, c_vp]),
     "logits_process": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp,
                                       c_vp, c_vp, c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "kv_cache_write_i8": (ctypes.c_int, [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_i32, c_i64, c_vp, c_cache, c_vp]),
+    "kv_cache_read_i8": (ctypes.c_int, [c_cache, c_vp, c_i64, c_i32, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp]),
+    "paged_attention_workspace_bytes": (c_size, [c_i64, c_i64, c_i64, c_i64, c_i64, c_i64]),
+    "paged_attention_i8": (ctypes.c_int, [c_vp, c_i64, c_i64, c_i64, c_i32, c_i64, c_i64, c_i64, c_cache, c_vp, c_i64,
+                                          c_i64, c_vp, c_i64, c_f64, c_vp, c_i64, c_i64, c_i64, c_vp, c_size, c_vp]),
+    "logits_sample_workspace_bytes": (c_size, [c_i64, c_i64]),
+    "logits_sample": (ctypes.c_int, [c_vp, c_i64, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                     c_size, c_vp]),
     "moeq8_synth_stream_key": (c_u64, [c_u32, c_u32, c_u32, c_u32]),
     "moeq8_synth_q8_0_fill": (ctypes.c_int, [c_vp, c_i64, c_i64, c_i64, c_u32, c_u32, c_u32,
                                              c_u32, c_vp]),

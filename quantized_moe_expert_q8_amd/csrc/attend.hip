@@ -1,0 +1,568 @@
+// Attention of a step's columns over the paged int8 cache.
+//
+//   t_i = scale * (q . kc_i) * kd_i                 codes kc, vc; scales kd, vd
+//   out = (sum_i e^(t_i - m) vd_i vc_i) / (sum_i e^(t_i - m)),  m = max t_i
+//
+// over the positions i that a column sees, in one pass: a running maximum m and
+// sum, and the outputs' sums rescaled where m grows.
+//
+// What it reads is the cache, once: a block takes a span of one sequence's
+// positions for one key head, with all rows (columns times query heads of the key
+// head) that read it; its waves take turns at tiles of 32 positions.  Both
+// products go through v_mfma_f32_16x16x32_f16 with the rows as the 16 columns of
+// the result:
+//
+//   S^T [positions x rows] = K [positions x d] Q^T     lane: one row, 2 x 4 positions
+//   O^T [d x rows]         = V^T [d x positions] P^T   lane: one row, 4 x 4 NC values
+//
+// A lane's scores of the first product are, as they are, its operand of the
+// second: which position a place of the product's inner index stands for is free as
+// long as both operands agree, so the lane's V rows are loaded by that order.
+// Everything of a row (maximum, sum, factors) lies in the lane that has it, and
+// nothing of a tile goes through LDS.  int8 codes are exact in fp16: a code's byte
+// under 0x64 is the fp16 number 1024 + byte.
+//
+// fp16 operands: a row of q is scaled by a power of two to a largest value in
+// [2^13, 2^14), so what its smallest values lose is below 2^-38 of the largest; fp32
+// rows go as two parts (22 bits), and bf16 and fp16 rows are exact in one.  The
+// weights e^(t - m) vd are scaled by a power of two that keeps the largest vd's
+// below 2^14, and go as one part for bf16 outputs (an error of 2^-12 against the
+// output's own 2^-9) and as two for others.
+//
+// Spans: one sequence and key head rarely fill the card, so positions are split
+// over blocks; each writes its rows' sums, maximum and total, and k_join adds them.
+#include "moeq8_cache.hpp"
+#include "moeq8_lds.hpp"
+
+#include <type_traits>
+
+namespace moeq8 {
+namespace {
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+constexpr int TILE = 32, SEGMENT = 1024;          // positions a tile; positions whose pages a wave holds at a time
+constexpr int WAVES = 4;
+constexpr int WEIGHT_BITS = 13;                   // weights stay below 2^14
+
+struct AttendArgs {
+    const void* q; int64_t q_seq, q_col, q_head;
+    void* out; int64_t o_seq, o_col, o_head;
+    Cache c;
+    const int32_t* pages; int64_t pages_row;
+    const int32_t* visible;
+    float* sums;                                  // [seqs][heads][rows][spans][d], then {m, l} [...][spans]
+    float2* stats;
+    uint32_t cols, group, rows, limit;            // rows: cols * group; limit: what visible is taken within
+    uint32_t span, spans, seqs;
+    float factor;                                 // scale * log2(e)
+};
+
+__device__ __forceinline__ uint32_t seen_by(const AttendArgs& a, uint32_t seq, uint32_t col) {
+    const int32_t n = a.visible[(int64_t)seq * a.cols + col];
+    return n < 0 ? 0u : ((uint32_t)n < a.limit ? (uint32_t)n : a.limit);
+}
+__device__ __forceinline__ uint32_t seen_by_any(const AttendArgs& a, uint32_t seq) {
+    uint32_t n = 0;
+    for (uint32_t c = 0; c < a.cols; ++c) {
+        const uint32_t s = seen_by(a, seq, c);
+        n = s > n ? s : n;
+    }
+    return n;
+}
+
+// Over the four lanes that have a row (or a position of the other product): l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ float quad_max(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// The four codes of a dword, their sign bits flipped, as fp16 numbers: two a dword.
+__device__ __forceinline__ half2v halves(uint32_t bytes, uint32_t select) {
+    const uint32_t u = __builtin_amdgcn_perm(0x64646464u, bytes, select);      // 1024 + 128 + code
+    return __builtin_bit_cast(half2v, u) - half2v{(_Float16)1152.0f, (_Float16)1152.0f};
+}
+__device__ __forceinline__ half8 as_half8(half2v a, half2v b, half2v c, half2v d) {
+    return half8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+constexpr uint32_t FLIP = 0x80808080u, LOW = 0x04010400u, HIGH = 0x04030402u;
+
+template <typename T>
+struct Parts {                                    // fp16 parts of a query value and of a weight
+    static constexpr int Q = std::is_same_v<T, float> ? 2 : 1, P = std::is_same_v<T, bf16_t> ? 1 : 2;
+};
+
+template <typename T, int NC, int NT>
+constexpr int query_bytes() { return Parts<T>::Q * NT * NC * 2 * 64 * 16; }
+
+// LDS of a block: the queries' operands; their rows' factors; then, over both, the
+// waves' statistics and one row tile's sums of each wave.
+template <typename T, int NC, int NT>
+constexpr int lds_bytes(int waves) {
+    const int queries = query_bytes<T, NC, NT>() + NT * 16 * 4, join = waves * (NT * 16 * 8 + 64 * 16 * NC * 4);
+    return queries > join ? queries : join;
+}
+
+template <typename T, int NC, int NT, int W>
+__global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
+    constexpr int DV = 4 * NC;                    // values of a V row a lane loads
+    constexpr int QP = Parts<T>::Q, PP = Parts<T>::P;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes<T, NC, NT>(W)];
+    constexpr uint32_t waves = W;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
+
+    // block: the rows' part slowest, then sequence, key head and span
+    uint32_t id = blockIdx.x;
+    const uint32_t split = id % a.spans;
+    id /= a.spans;
+    const uint32_t head = id % a.c.n_heads;
+    id /= a.c.n_heads;
+    const uint32_t seq = id % a.seqs, row0 = id / a.seqs * (16 * NT);
+    const uint32_t length = seen_by_any(a, seq);
+    const uint32_t begin = split * a.span;
+    if (begin >= length && a.spans > 1) return;   // k_join reads spans with a position only
+    const uint32_t end = length - begin < a.span ? length : begin + a.span;      // 0 for a sequence of no position
+
+    // ---- queries: fp16 operands and their rows' factors, in LDS -----------------
+    half8* const query = reinterpret_cast<half8*>(lds);          // [part][tile][chunk][step][lane]
+    float* const factors = reinterpret_cast<float*>(lds + query_bytes<T, NC, NT>());
+    for (uint32_t t = wave; t < NT; t += waves) {
+        const uint32_t row = row0 + 16 * t + n;
+        const bool real = row < a.rows;
+        const uint32_t col = real ? row / a.group : 0u, sub = real ? row - col * a.group : 0u;
+        const T* q = (const T*)a.q + seq * a.q_seq + col * a.q_col + ((int64_t)head * a.group + sub) * a.q_head;
+        float v[NC][16];
+        float m = 0.0f;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            const uint32_t at = 64 * c + 16 * g;
+            T raw[16];
+            load_vec(raw, q + (at < a.c.d ? at : 0u));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[c][i] = real && at < a.c.d ? to_f32(raw[i]) : 0.0f;
+                m = fmaxf(m, fabsf(v[c][i]));
+            }
+        }
+        m = quad_max(m);
+        const int up = m > 0.0f && m < __builtin_inff() ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;
+        if (g == 0) factors[16 * t + n] = ldexpf(a.factor, -up);
+#pragma unroll
+        for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                half8 hi, lo;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float x = ldexpf(v[c][8 * s + i], up);
+                    hi[i] = (_Float16)x;
+                    lo[i] = (_Float16)(x - (float)hi[i]);
+                }
+                half8* o = query + ((t * NC + c) * 2 + s) * 64 + lane;
+                *o = hi;
+                if constexpr (QP == 2) o[NT * NC * 2 * 64] = lo;
+            }
+    }
+    __syncthreads();
+
+    float factor[NT];
+    uint32_t seen[NT], least = ~0u;               // positions that this lane's rows see; the fewest of any row
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const uint32_t row = row0 + 16 * t + n;
+        factor[t] = factors[16 * t + n];
+        seen[t] = row < a.rows ? seen_by(a, seq, row / a.group) : ~0u;
+    }
+    for (uint32_t c = 0; c < a.cols; ++c) {
+        const uint32_t s = seen_by(a, seq, c);
+        least = s < least ? s : least;
+    }
+
+    f32x4 o[NT][DV];
+    float m[NT], l[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        m[t] = -__builtin_inff();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < DV; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    int up = 127 + WEIGHT_BITS;                   // weights are scaled by 2^up, for scales below the normal range
+
+    // a lane's part of a row: 16 values of each 64 of K, DV values of V; a row
+    // shorter than that reads its first values again, against queries of 0 and
+    // into outputs that no one stores
+    const int64_t k_lane = n * a.c.token_stride, v_lane = (uint32_t)(DV * n) < a.c.d ? DV * n : 0;
+    const uint32_t in_page = (1u << a.c.page_shift) - 1u;
+
+    for (uint32_t from = begin; from < end; from += SEGMENT) {
+        const uint32_t to = end - from < SEGMENT ? end : from + SEGMENT;
+        // the page of every 16 positions, one a lane
+        uint32_t page = ~0u;
+        if (from + 16 * lane < to) page = (uint32_t)a.pages[seq * a.pages_row + ((from + 16 * lane) >> a.c.page_shift)];
+        for (uint32_t at = from + TILE * wave; at < to; at += TILE * waves) {
+            u32x4 kq[2][NC];
+            uint32_t vq[8][NC];
+            f32x4 kd[2], vd[2];
+            bool ok[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)page, (int)((at - from) / 16 + h));
+                ok[h] = p < a.c.n_pages;
+                p = ok[h] ? p : 0u;
+                const uint32_t place = (at + 16 * h) & in_page;
+                const int64_t row = p * a.c.page_stride + head * a.c.head_stride + place * a.c.token_stride;
+                const int64_t scale = p * a.c.scale_page_stride + head * a.c.scale_head_stride + place + 4 * g;
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const uint32_t d = 64 * c + 16 * g;
+                    kq[h][c] = *reinterpret_cast<const u32x4*>(a.c.k + row + k_lane + (d < a.c.d ? d : 0u));
+                }
+                kd[h] = *reinterpret_cast<const f32x4*>(a.c.k_scale + scale);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int8_t* v = a.c.v + row + (4 * g + j) * a.c.token_stride + v_lane;
+                    if constexpr (NC == 1) {
+                        vq[4 * h + j][0] = *reinterpret_cast<const uint32_t*>(v);
+                    } else if constexpr (NC == 2) {
+                        const u32x2 u = *reinterpret_cast<const u32x2*>(v);
+                        vq[4 * h + j][0] = u[0];
+                        vq[4 * h + j][1] = u[1];
+                    } else {
+                        const u32x4 u = *reinterpret_cast<const u32x4*>(v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) vq[4 * h + j][i] = u[i];
+                    }
+                }
+                vd[h] = *reinterpret_cast<const f32x4*>(a.c.v_scale + scale);
+            }
+
+            // scores
+            f32x4 s[NT][2];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c = 0; c < NC; ++c)
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    half8 k[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t x = kq[h][c][2 * st] ^ FLIP, y = kq[h][c][2 * st + 1] ^ FLIP;
+                        k[h] = as_half8(halves(x, LOW), halves(x, HIGH), halves(y, LOW), halves(y, HIGH));
+                    }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int p = 0; p < QP; ++p) {
+                            const half8 b = query[(((p * NT + t) * NC + c) * 2 + st) * 64 + lane];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                s[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[h], b, s[t][h], 0, 0, 0);
+                        }
+                }
+
+            // values past the length: 0, whatever their scales hold
+            const bool whole = at + TILE <= least && ok[0] && ok[1];
+            if (!whole) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (!ok[h] || at + 16 * h + 4 * g + r >= length) vd[h][r] = 0.0f;
+            }
+            // the power of two that keeps weights in fp16
+            float most = 0.0f;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(vd[h][r]) < __builtin_inff() ? fabsf(vd[h][r]) : 0.0f);
+            const uint32_t top = __builtin_amdgcn_readfirstlane(__float_as_uint(quad_max(most)));
+            const int want = WEIGHT_BITS + 127 - (int)(top >> 23);       // 2^want * top in [2^13, 2^14); top >= 0
+            if (want < up) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < DV; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) o[t][i][r] = ldexpf(o[t][i][r], want - up);
+                up = want;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) vd[h][r] = ldexpf(vd[h][r], up);
+
+            half8 w[PP][NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                float x[8];
+                float top_t = -__builtin_inff();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = s[t][i / 4][i % 4] * kd[i / 4][i % 4] * factor[t];
+                    if (!whole && !(ok[i / 4] && at + 16 * (i / 4) + 4 * g + i % 4 < seen[t])) x[i] = -__builtin_inff();
+                    top_t = fmaxf(top_t, x[i]);
+                }
+                const float now = fmaxf(m[t], quad_max(top_t)), base = now == -__builtin_inff() ? 0.0f : now;
+                if (__any(now > m[t])) {
+                    const float keep = __builtin_amdgcn_exp2f(m[t] - base);
+                    l[t] *= keep;
+#pragma unroll
+                    for (int i = 0; i < DV; ++i) o[t][i] *= keep;
+                    m[t] = now;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float p = __builtin_amdgcn_exp2f(x[i] - base);
+                    l[t] += p;
+                    float v = p * vd[i / 4][i % 4];
+                    // a position that others see may have a scale that is not finite
+                    if (!whole && x[i] == -__builtin_inff()) v = 0.0f;
+                    const _Float16 hi = (_Float16)v;
+                    w[0][t][i] = hi;
+                    if constexpr (PP == 2) w[1][t][i] = (_Float16)(v - (float)hi);
+                }
+            }
+
+            // outputs
+#pragma unroll
+            for (int d4 = 0; d4 < NC; ++d4) {
+                uint32_t b01[4], b23[4];          // codes 0 and 1, 2 and 3 of two positions each
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t x = vq[2 * j][d4] ^ FLIP, y = vq[2 * j + 1][d4] ^ FLIP;
+                    b01[j] = __builtin_amdgcn_perm(y, x, 0x05010400u);
+                    b23[j] = __builtin_amdgcn_perm(y, x, 0x07030602u);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t(&b)[4] = i < 2 ? b01 : b23;
+                    const uint32_t sel = i & 1 ? HIGH : LOW;
+                    const half8 v = as_half8(halves(b[0], sel), halves(b[1], sel), halves(b[2], sel), halves(b[3], sel));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int p = 0; p < PP; ++p)
+                            o[t][4 * d4 + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[p][t], o[t][4 * d4 + i], 0, 0, 0);
+                }
+            }
+        }
+    }
+
+    // ---- the waves' sums together ------------------------------------------------
+    __syncthreads();                              // the queries are done with
+    float2* const stats = reinterpret_cast<float2*>(lds);        // [wave][row]
+    f32x4* const sums = reinterpret_cast<f32x4*>(stats + waves * NT * 16);     // [wave][DV][lane]
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const float total = quad_sum(l[t]);
+        if (g == 0) stats[(wave * NT + t) * 16 + n] = float2{m[t], total};
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float most = -__builtin_inff(), total = 0.0f;
+        for (uint32_t w = 0; w < waves; ++w) most = fmaxf(most, stats[(w * NT + t) * 16 + n].x);
+        const float base = most == -__builtin_inff() ? 0.0f : most;
+        for (uint32_t w = 0; w < waves; ++w) {
+            const float2 s = stats[(w * NT + t) * 16 + n];
+            total += s.y * __builtin_amdgcn_exp2f(s.x - base);
+        }
+        const float keep = __builtin_amdgcn_exp2f(m[t] - base);
+        // i counts the values of a lane's row in order: DV of each r
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int i = 0; i < DV; i += 4) {
+                f32x4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = ldexpf(o[t][i + j][r] * keep, -up);
+                sums[(wave * DV + (r * DV + i) / 4) * 64 + lane] = v;
+            }
+        __syncthreads();
+        const uint32_t row = row0 + 16 * t + n;
+        if (row < a.rows) {                       // this thread's lane number names the row in every wave
+            const uint32_t col = row / a.group, sub = row - col * a.group;
+            const int64_t place = (((int64_t)seq * a.c.n_heads + head) * a.rows + row) * a.spans + split;
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            for (uint32_t i = wave; i < DV; i += waves) {
+                const uint32_t d = 4 * DV * g + 4 * i;
+                if (d >= a.c.d) break;
+                f32x4 v = sums[i * 64 + lane];
+                for (uint32_t w = 1; w < waves; ++w) v += sums[(w * DV + i) * 64 + lane];
+                if (a.spans == 1) {
+                    T* out = (T*)a.out + seq * a.o_seq + col * a.o_col + ((int64_t)head * a.group + sub) * a.o_head + d;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) from_f32(out[j], v[j] * inv);
+                } else {
+                    *reinterpret_cast<f32x4*>(a.sums + place * a.c.d + d) = v;
+                }
+            }
+            if (a.spans > 1 && wave == 0 && g == 0) a.stats[place] = float2{most, total};
+        }
+        __syncthreads();
+    }
+}
+
+// A row's spans together: 256 threads, each with 4 values of every so many spans.
+template <typename T>
+__global__ __launch_bounds__(256) void k_join(AttendArgs a) {
+    __shared__ f32x4 part[256];
+    const uint32_t row_id = blockIdx.x, row = row_id % a.rows, pair = row_id / a.rows, head = pair % a.c.n_heads,
+                   seq = pair / a.c.n_heads;
+    const uint32_t length = seen_by_any(a, seq), spans = (length + a.span - 1) / a.span;
+    const uint32_t vecs = a.c.d / 4, lanes = 256 / vecs, k = threadIdx.x / vecs, at = threadIdx.x - k * vecs;
+    const float2* stats = a.stats + (int64_t)row_id * a.spans;
+    const f32x4* sums = reinterpret_cast<const f32x4*>(a.sums) + (int64_t)row_id * a.spans * vecs;
+    float m = -__builtin_inff(), l = 0.0f;
+    for (uint32_t s = 0; s < spans; ++s) m = fmaxf(m, stats[s].x);
+    const float base = m == -__builtin_inff() ? 0.0f : m;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t s = 0; s < spans; ++s) l += stats[s].y * __builtin_amdgcn_exp2f(stats[s].x - base);
+    if (k < lanes)
+        for (uint32_t s = k; s < spans; s += lanes) v += sums[(int64_t)s * vecs + at] * __builtin_amdgcn_exp2f(stats[s].x - base);
+    part[threadIdx.x] = v;
+    __syncthreads();
+    if (k == 0) {
+        for (uint32_t i = 1; i < lanes; ++i) v += part[i * vecs + at];
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const uint32_t col = row / a.group, sub = row - col * a.group;
+        T* out = (T*)a.out + seq * a.o_seq + col * a.o_col + ((int64_t)head * a.group + sub) * a.o_head + 4 * at;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) from_f32(out[j], v[j] * inv);
+    }
+}
+
+// How a call's work is split.
+struct Plan {
+    int64_t rows, span, spans, blocks;
+    int chunks, tiles;                            // 64 values of a row, 16 rows
+    size_t sums_bytes, bytes;
+};
+
+Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_t d, int64_t limit) {
+    Plan p;
+    p.rows = cols * (q_heads / heads);
+    p.chunks = d <= 64 ? 1 : d <= 128 ? 2 : 4;
+    const int64_t tiles = (p.rows + 15) / 16, most = p.chunks == 4 ? 2 : 3;
+    p.tiles = (int)std::min(tiles, most);
+    const int64_t pairs = seqs * heads * ((tiles + p.tiles - 1) / p.tiles);
+        // four blocks for each of 256 CUs, spans of at least 256 positions
+    const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, pairs));
+    p.span = std::max<int64_t>(256, ((limit + want - 1) / want + 127) / 128 * 128);
+    p.spans = std::max<int64_t>(1, (limit + p.span - 1) / p.span);
+    p.blocks = pairs * p.spans;
+    p.sums_bytes = p.spans > 1 ? (size_t)(seqs * heads * p.rows * p.spans * d * 4) : 0;
+    p.bytes = p.spans > 1 ? p.sums_bytes + (size_t)(seqs * heads * p.rows * p.spans * 8) : 0;
+    return p;
+}
+
+template <typename T, int NC, int NT>
+int launch_attend(const AttendArgs& a, const Plan& p, hipStream_t stream) {
+    hipLaunchKernelGGL((k_attend<T, NC, NT, WAVES>), dim3((uint32_t)p.blocks), dim3(WAVES * 64), 0, stream, a);
+    return check_launch();
+}
+
+template <typename T>
+int attend(const AttendArgs& a, const Plan& p, hipStream_t stream) {
+    int s;
+    switch (p.chunks * 4 + p.tiles) {
+        case 5: s = launch_attend<T, 1, 1>(a, p, stream); break;
+        case 6: s = launch_attend<T, 1, 2>(a, p, stream); break;
+        case 7: s = launch_attend<T, 1, 3>(a, p, stream); break;
+        case 9: s = launch_attend<T, 2, 1>(a, p, stream); break;
+        case 10: s = launch_attend<T, 2, 2>(a, p, stream); break;
+        case 11: s = launch_attend<T, 2, 3>(a, p, stream); break;
+        case 17: s = launch_attend<T, 4, 1>(a, p, stream); break;
+        default: s = launch_attend<T, 4, 2>(a, p, stream); break;
+    }
+    if (s != MOEQ8_OK || p.spans == 1) return s;
+    hipLaunchKernelGGL((k_join<T>), dim3((uint32_t)((int64_t)a.seqs * a.c.n_heads * a.rows)), dim3(256), 0, stream, a);
+    return check_launch();
+}
+
+// What both entry points refuse of the sizes.
+int check_sizes(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_t d, int64_t limit) {
+    if (seqs < 0 || cols < 1 || cols > MOEQ8_MAX_COLS || heads < 1 || q_heads < heads || q_heads % heads || d < 1 || limit < 0)
+        return MOEQ8_EINVAL;
+    if (d % 16 || d > MOEQ8_MAX_HEAD_DIM || limit >= (1 << 30) || q_heads >= (1 << 20) || seqs >= (1 << 24))
+        return MOEQ8_EUNSUPPORTED;
+    if (seqs && heads > (1 << 26) / seqs) return MOEQ8_EUNSUPPORTED;
+    return MOEQ8_OK;
+}
+
+}  // namespace
+}  // namespace moeq8
+
+extern "C" size_t paged_attention_workspace_bytes(int64_t n_seqs, int64_t n_cols, int64_t n_q_heads, int64_t n_heads, int64_t d,
+                                                  int64_t max_visible) {
+    using namespace moeq8;
+    if (check_sizes(n_seqs, n_cols, n_q_heads, n_heads, d, max_visible) != MOEQ8_OK || n_seqs == 0) return 0;
+    return plan_for(n_seqs, n_cols, n_q_heads, n_heads, d, max_visible).bytes;
+}
+
+extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q_col_stride, int64_t q_head_stride,
+                                  int32_t dtype, int64_t n_seqs, int64_t n_cols, int64_t n_q_heads,
+                                  const moeq8_kv_cache* cache, const int32_t* pages, int64_t pages_row_stride, int64_t n_table,
+                                  const int32_t* visible, int64_t max_visible, double scale, void* out,
+                                  int64_t out_seq_stride, int64_t out_col_stride, int64_t out_head_stride, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    using namespace moeq8;
+    AttendArgs a;
+    if (dtype < MOEQ8_F32 || dtype > MOEQ8_BF16) return MOEQ8_EINVAL;
+    if (const int s = check_cache(cache, a.c)) return s;
+    const int64_t heads = a.c.n_heads, d = a.c.d;
+    if (const int s = check_sizes(n_seqs, n_cols, n_q_heads, heads, d, max_visible)) return s;
+    if (n_table < 0 || !(scale - scale == 0.0)) return MOEQ8_EINVAL;
+    if (n_seqs == 0) return MOEQ8_OK;
+    if (!q || !out || !visible || (n_table && !pages)) return MOEQ8_EINVAL;
+    if ((n_seqs > 1 && pages_row_stride < n_table)) return MOEQ8_EINVAL;
+    const int64_t strides[2][3] = {{q_seq_stride, q_col_stride, q_head_stride}, {out_seq_stride, out_col_stride, out_head_stride}};
+    const int64_t counts[3] = {n_seqs, n_cols, n_q_heads};
+    int64_t bytes[2];
+    const int64_t es = dtype_bytes(dtype);
+    for (int i = 0; i < 2; ++i) {
+        bytes[i] = d;
+        for (int j = 0; j < 3; ++j) {
+            if (counts[j] > 1 && strides[i][j] < d) return MOEQ8_EINVAL;
+            if (counts[j] > 1) bytes[i] += (counts[j] - 1) * strides[i][j];
+        }
+        bytes[i] *= es;
+    }
+    if (((uintptr_t)q | (uintptr_t)out) & (uintptr_t)(es - 1) || ((uintptr_t)pages | (uintptr_t)visible) & 3u) return MOEQ8_EALIGN;
+    if (ranges_overlap(q, bytes[0], out, bytes[1]) || clashes_with_cache(a.c, out, bytes[1])) return MOEQ8_EINVAL;
+    const Plan p = plan_for(n_seqs, n_cols, n_q_heads, heads, d, max_visible);
+    if (p.blocks > most_blocks(WAVES * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
+    if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MOEQ8_EINVAL;
+    if (p.bytes && (uintptr_t)workspace & 15u) return MOEQ8_EALIGN;
+    a.q = q; a.q_seq = q_seq_stride; a.q_col = q_col_stride; a.q_head = q_head_stride;
+    a.out = out; a.o_seq = out_seq_stride; a.o_col = out_col_stride; a.o_head = out_head_stride;
+    a.pages = pages; a.pages_row = pages_row_stride;
+    a.visible = visible;
+    a.sums = (float*)workspace;
+    a.stats = (float2*)((uint8_t*)workspace + p.sums_bytes);
+    a.cols = (uint32_t)n_cols; a.group = (uint32_t)(n_q_heads / heads); a.rows = (uint32_t)p.rows;
+    const int64_t positions = n_table << a.c.page_shift;
+    a.limit = (uint32_t)std::min(max_visible, positions);
+    a.span = (uint32_t)p.span; a.spans = (uint32_t)p.spans; a.seqs = (uint32_t)n_seqs;
+    a.factor = (float)(scale * 1.4426950408889634);
+    switch (dtype) {
+        case MOEQ8_F32: return attend<float>(a, p, (hipStream_t)stream);
+        case MOEQ8_F16: return attend<f16_t>(a, p, (hipStream_t)stream);
+        default: return attend<bf16_t>(a, p, (hipStream_t)stream);
+    }
+}

@@ -29,6 +29,12 @@ struct Library {
     decltype(&::i8_quantize_rows) i8_quantize_rows;
     decltype(&::gemm_i8) gemm_i8;
     decltype(&::logits_process) logits_process;
+    decltype(&::kv_cache_write_i8) kv_cache_write_i8;
+    decltype(&::kv_cache_read_i8) kv_cache_read_i8;
+    decltype(&::paged_attention_workspace_bytes) paged_attention_workspace_bytes;
+    decltype(&::paged_attention_i8) paged_attention_i8;
+    decltype(&::logits_sample_workspace_bytes) logits_sample_workspace_bytes;
+    decltype(&::logits_sample) logits_sample;
 };
 Library lib{};
 PyObject* fail = nullptr;                         // raises for (name, status)
@@ -158,10 +164,10 @@ const char* text(PyObject* o) {
 
 PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (!arguments("bind", n, 6)) return nullptr;
-    TORCH_CHECK_TYPE(PyCallable_Check(a[4]) && PyType_Check(a[5]) &&
-                         PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[5]), &PyTuple_Type),
-                     "bind takes four addresses, a callable and a tuple type");
+    if (!arguments("bind", n, 12)) return nullptr;
+    TORCH_CHECK_TYPE(PyCallable_Check(a[10]) && PyType_Check(a[11]) &&
+                         PyType_IsSubtype(reinterpret_cast<PyTypeObject*>(a[11]), &PyTuple_Type),
+                     "bind takes ten addresses, a callable and a tuple type");
     auto address = [&](int i) {
         void* p = PyLong_AsVoidPtr(a[i]);
         if (!p && PyErr_Occurred()) throw python_error();
@@ -171,12 +177,18 @@ PyObject* py_bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     lib.i8_quantize_rows = reinterpret_cast<decltype(lib.i8_quantize_rows)>(address(1));
     lib.gemm_i8 = reinterpret_cast<decltype(lib.gemm_i8)>(address(2));
     lib.logits_process = reinterpret_cast<decltype(lib.logits_process)>(address(3));
-    Py_INCREF(a[4]);
-    Py_INCREF(a[5]);
+    lib.kv_cache_write_i8 = reinterpret_cast<decltype(lib.kv_cache_write_i8)>(address(4));
+    lib.kv_cache_read_i8 = reinterpret_cast<decltype(lib.kv_cache_read_i8)>(address(5));
+    lib.paged_attention_workspace_bytes = reinterpret_cast<decltype(lib.paged_attention_workspace_bytes)>(address(6));
+    lib.paged_attention_i8 = reinterpret_cast<decltype(lib.paged_attention_i8)>(address(7));
+    lib.logits_sample_workspace_bytes = reinterpret_cast<decltype(lib.logits_sample_workspace_bytes)>(address(8));
+    lib.logits_sample = reinterpret_cast<decltype(lib.logits_sample)>(address(9));
+    Py_INCREF(a[10]);
+    Py_INCREF(a[11]);
     Py_XDECREF(fail);
     Py_XDECREF(reinterpret_cast<PyObject*>(norm_type));
-    fail = a[4];
-    norm_type = reinterpret_cast<PyTypeObject*>(a[5]);
+    fail = a[10];
+    norm_type = reinterpret_cast<PyTypeObject*>(a[11]);
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
@@ -368,6 +380,185 @@ PyObject* py_logits_process(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// Sizes and strides of a tensor whose last dimension's elements lie together.
+struct Block {
+    int64_t size[4], stride[4];
+};
+Block block(PyObject* o, const char* name, ScalarType dtype, int64_t dev, at::IntArrayRef shape) {
+    if (THPVariable_Check(o)) {
+        const Tensor& t = THPVariable_Unpack(o);
+        if (t.scalar_type() == dtype && t.get_device() == dev && t.sizes() == shape &&
+            (shape.back() <= 1 || t.stride(-1) == 1)) {
+            Block b;
+            for (size_t i = 0; i < shape.size(); ++i) {
+                b.size[i] = t.size(i);
+                b.stride[i] = t.stride(i);
+            }
+            return b;
+        }
+    }
+    refuse(o, name, dtype, dev, shape);
+}
+
+// A KVCacheI8, on the device of its keys.
+struct CacheArg {
+    moeq8_kv_cache c;
+    const Tensor* k;
+    int64_t dev;
+};
+CacheArg cache_of(PyObject* o) {
+    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4, "cache must be a KVCacheI8");
+    PyObject *k = PyTuple_GET_ITEM(o, 0), *ks = PyTuple_GET_ITEM(o, 1), *v = PyTuple_GET_ITEM(o, 2), *vs = PyTuple_GET_ITEM(o, 3);
+    TORCH_CHECK_VALUE(THPVariable_Check(k) && THPVariable_Unpack(k).is_cuda(), "cache.k must be a device tensor");
+    const Tensor& t = THPVariable_Unpack(k);
+    TORCH_CHECK_VALUE(t.dim() == 4, "cache.k must be 4-D, got ", t.sizes());
+    const int64_t dev = t.get_device(), shape[3] = {t.size(0), t.size(1), t.size(2)};
+    const Block b = block(k, "cache.k", ScalarType::Char, dev, t.sizes());
+    const Block bv = block(v, "cache.v", ScalarType::Char, dev, t.sizes());
+    const Block s = block(ks, "cache.k_scale", ScalarType::Float, dev, {shape, 3});
+    const Block sv = block(vs, "cache.v_scale", ScalarType::Float, dev, {shape, 3});
+    for (int i = 0; i < 3; ++i)
+        TORCH_CHECK_VALUE(shape[i] <= 1 || (b.stride[i] == bv.stride[i] && s.stride[i] == sv.stride[i]),
+                          "the cache's keys and values must have the same strides");
+    return {{(int8_t*)t.data_ptr(), (float*)THPVariable_Unpack(ks).data_ptr(), (int8_t*)THPVariable_Unpack(v).data_ptr(),
+             (float*)THPVariable_Unpack(vs).data_ptr(), shape[0], shape[1], shape[2], t.size(3), b.stride[0], b.stride[1],
+             shape[2] > 1 ? b.stride[2] : t.size(3), s.stride[0], s.stride[1]},
+            &t, dev};
+}
+
+// The workspace the caller gave, or a new one.
+Held workspace_of(PyObject* o, int64_t bytes, const Tensor& like) {
+    if (!given(o)) return bytes ? given_or_new(o, {bytes}, like, ScalarType::Byte) : keep(Py_None);
+    const int64_t n = count_of(o, "workspace");
+    vector(o, "workspace", ScalarType::Byte, like.get_device(), n);
+    TORCH_CHECK_VALUE(n >= bytes, "workspace must have ", bytes, " bytes, got ", n);
+    return keep(o);
+}
+
+// kv_cache_write_i8(k, v, cache, slots)
+PyObject* py_kv_cache_write_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments("kv_cache_write_i8", n, 4)) return nullptr;
+    const CacheArg c = cache_of(a[2]);
+    TORCH_CHECK_VALUE(THPVariable_Check(a[0]) && THPVariable_Unpack(a[0]).is_cuda(), "k must be a device tensor");
+    const Tensor& k = THPVariable_Unpack(a[0]);
+    const int32_t code = dtype_code(k, "k");
+    TORCH_CHECK_VALUE(k.dim() == 3, "k must be 3-D, got ", k.sizes());
+    const int64_t shape[3] = {k.size(0), c.c.n_heads, c.c.d};
+    const Block bk = block(a[0], "k", k.scalar_type(), c.dev, {shape, 3}), bv = block(a[1], "v", k.scalar_type(), c.dev, {shape, 3});
+    const void* slots = vector(a[3], "slots", ScalarType::Long, c.dev, shape[0]);
+    if (shape[0]) {
+        const at::DeviceGuard guard(k.device());
+        const void *pk = k.data_ptr(), *pv = THPVariable_Unpack(a[1]).data_ptr();
+        void* stream = stream_of(c.dev);
+        run("kv_cache_write_i8", [=, &c] {
+            return lib.kv_cache_write_i8(pk, bk.stride[0], bk.stride[1], pv, bv.stride[0], bv.stride[1], code, shape[0],
+                                         (const int64_t*)slots, &c.c, stream);
+        });
+    }
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+// kv_cache_read_i8(cache, slots, dtype, k_out, v_out) -> (k_out, v_out)
+PyObject* py_kv_cache_read_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments("kv_cache_read_i8", n, 5)) return nullptr;
+    const CacheArg c = cache_of(a[0]);
+    const int64_t shape[3] = {count_of(a[1], "slots"), c.c.n_heads, c.c.d};
+    const void* slots = vector(a[1], "slots", ScalarType::Long, c.dev, shape[0]);
+    PyObject* one = given(a[3]) ? a[3] : a[4];
+    TORCH_CHECK_VALUE(!given(one) || THPVariable_Check(one), "k_out must be a device tensor, on the same device as the others");
+    const ScalarType t = given(one) ? THPVariable_Unpack(one).scalar_type() : type_of(a[2]);
+    const int32_t code = t == ScalarType::Float ? MOEQ8_F32 : t == ScalarType::Half ? MOEQ8_F16 : MOEQ8_BF16;
+    TORCH_CHECK_TYPE(code != MOEQ8_BF16 || t == ScalarType::BFloat16, "k_out must be a float32, float16 or bfloat16 tensor");
+    const at::DeviceGuard guard(c.k->device());
+    Held k = given_or_new(a[3], {shape, 3}, *c.k, t), v = given_or_new(a[4], {shape, 3}, *c.k, t);
+    const Block bk = block(k.o, "k_out", t, c.dev, {shape, 3}), bv = block(v.o, "v_out", t, c.dev, {shape, 3});
+    if (shape[0]) {
+        void *pk = k.data(), *pv = v.data(), *stream = stream_of(c.dev);
+        run("kv_cache_read_i8", [=, &c] {
+            return lib.kv_cache_read_i8(&c.c, (const int64_t*)slots, shape[0], code, pk, bk.stride[0], bk.stride[1], pv,
+                                        bv.stride[0], bv.stride[1], stream);
+        });
+    }
+    return PyTuple_Pack(2, k.o, v.o);
+    END_HANDLE_TH_ERRORS
+}
+
+// paged_attention_i8(q, cache, pages, visible, scale, max_visible, out, workspace) -> out
+PyObject* py_paged_attention_i8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments("paged_attention_i8", n, 8)) return nullptr;
+    TORCH_CHECK_VALUE(THPVariable_Check(a[0]) && THPVariable_Unpack(a[0]).is_cuda(), "q must be a device tensor");
+    const Tensor& q = THPVariable_Unpack(a[0]);
+    const int32_t code = dtype_code(q, "q");
+    TORCH_CHECK_VALUE(q.dim() == 4, "q must be 4-D, got ", q.sizes());
+    const CacheArg c = cache_of(a[1]);
+    const int64_t seqs = q.size(0), cols = q.size(1), heads = q.size(2), shape[4] = {seqs, cols, heads, c.c.d};
+    const Block bq = block(a[0], "q", q.scalar_type(), c.dev, {shape, 4});
+    TORCH_CHECK_VALUE(c.c.n_heads > 0 && heads > 0 && heads % c.c.n_heads == 0, "q's heads (", heads,
+                      ") must be a multiple of the cache's (", c.c.n_heads, ")");
+    TORCH_CHECK_VALUE(THPVariable_Check(a[2]) && THPVariable_Unpack(a[2]).dim() == 2, "pages must be a 2-D device tensor");
+    const int64_t table = THPVariable_Unpack(a[2]).size(1);
+    const int64_t ps = matrix(a[2], "pages", ScalarType::Int, c.dev, seqs, table);
+    TORCH_CHECK_VALUE(matrix(a[3], "visible", ScalarType::Int, c.dev, seqs, cols) == cols, "visible rows must be contiguous");
+    const double scale = given(a[4]) ? PyFloat_AsDouble(a[4]) : 1.0 / std::sqrt((double)c.c.d);
+    if (scale == -1.0 && PyErr_Occurred()) return nullptr;
+    const int64_t most = given(a[5]) ? integer(a[5]) : std::min<int64_t>(table * c.c.page_size, (1 << 30) - 1);
+    const at::DeviceGuard guard(q.device());
+    Held out = given_or_new(a[6], {shape, 4}, q, q.scalar_type());
+    const Block bo = block(out.o, "out", q.scalar_type(), c.dev, {shape, 4});
+    if (seqs) {
+        const size_t bytes = lib.paged_attention_workspace_bytes(seqs, cols, heads, c.c.n_heads, c.c.d, most);
+        Held ws = workspace_of(a[7], (int64_t)bytes, q);
+        const size_t have = ws.data() ? (size_t)THPVariable_Unpack(ws.o).numel() : 0;
+        const void *pq = q.data_ptr(), *pp = THPVariable_Unpack(a[2]).data_ptr(), *pv = THPVariable_Unpack(a[3]).data_ptr();
+        void *po = out.data(), *pw = ws.data(), *stream = stream_of(c.dev);
+        run("paged_attention_i8", [=, &c] {
+            return lib.paged_attention_i8(pq, bq.stride[0], bq.stride[1], bq.stride[2], code, seqs, cols, heads, &c.c,
+                                          (const int32_t*)pp, ps, table, (const int32_t*)pv, most, scale, po, bo.stride[0],
+                                          bo.stride[1], bo.stride[2], pw, have, stream);
+        });
+    }
+    return out.give();
+    END_HANDLE_TH_ERRORS
+}
+
+// logits_sample(logits, u, temperature, top_k, top_p, min_p, token, logprob, workspace) -> (token, logprob)
+PyObject* py_logits_sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    if (!arguments("logits_sample", n, 9)) return nullptr;
+    const Tensor& z = first(a[0], "logits");
+    const int32_t code = dtype_code(z, "logits");
+    const int64_t dev = z.get_device(), rows = z.size(0), vocab = z.size(1);
+    const int64_t zs = matrix(a[0], "logits", z.scalar_type(), dev, rows, vocab);
+    const void* u = vector(a[1], "u", ScalarType::Float, dev, rows);
+    const void* temperature = vector_or_null(a[2], "temperature", ScalarType::Float, dev, rows);
+    const void* top_k = vector_or_null(a[3], "top_k", ScalarType::Int, dev, rows);
+    const void* top_p = vector_or_null(a[4], "top_p", ScalarType::Float, dev, rows);
+    const void* min_p = vector_or_null(a[5], "min_p", ScalarType::Float, dev, rows);
+    const at::DeviceGuard guard(z.device());
+    Held token = given_or_new(a[6], {rows}, z, ScalarType::Int);
+    Held logprob = given_or_new(a[7], {rows}, z, ScalarType::Float);
+    void* pt = vector(token.o, "token", ScalarType::Int, dev, rows);
+    void* pl = vector(logprob.o, "logprob", ScalarType::Float, dev, rows);
+    if (rows) {
+        const size_t bytes = lib.logits_sample_workspace_bytes(rows, vocab);
+        Held ws = workspace_of(a[8], (int64_t)bytes, z);
+        const size_t have = ws.data() ? (size_t)THPVariable_Unpack(ws.o).numel() : 0;
+        const void* pz = z.data_ptr();
+        void *pw = ws.data(), *stream = stream_of(dev);
+        run("logits_sample", [=] {
+            return lib.logits_sample(pz, zs, code, rows, vocab, (const float*)u, (const float*)temperature,
+                                     (const int32_t*)top_k, (const float*)top_p, (const float*)min_p, (int32_t*)pt,
+                                     (float*)pl, pw, have, stream);
+        });
+    }
+    return PyTuple_Pack(2, token.o, logprob.o);
+    END_HANDLE_TH_ERRORS
+}
+
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 constexpr PyMethodDef method(const char* name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
@@ -376,6 +567,8 @@ constexpr PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {method<py_bind>("bind"), method<py_matrix>("matrix"), method<py_vector>("vector"),
                          method<py_rms_norm_q8>("rms_norm_q8"), method<py_i8_quantize_rows>("i8_quantize_rows"),
                          method<py_gemm_i8>("gemm_i8"), method<py_logits_process>("logits_process"),
+                         method<py_kv_cache_write_i8>("kv_cache_write_i8"), method<py_kv_cache_read_i8>("kv_cache_read_i8"),
+                         method<py_paged_attention_i8>("paged_attention_i8"), method<py_logits_sample>("logits_sample"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -791,8 +791,10 @@ def _binding():
     if _BINDING is None:
         m = load_binding()
         address = lambda name: ctypes.cast(getattr(lib(), name), ctypes.c_void_p).value
-        m.bind(address("rms_norm_q8"), address("i8_quantize_rows"), address("gemm_i8"), address("logits_process"),
-               _raise, NormQ8)
+        m.bind(*(address(name) for name in (
+            "rms_norm_q8", "i8_quantize_rows", "gemm_i8", "logits_process", "kv_cache_write_i8", "kv_cache_read_i8",
+            "paged_attention_workspace_bytes", "paged_attention_i8", "logits_sample_workspace_bytes", "logits_sample")),
+            _raise, NormQ8)
         _BINDING = m
     return _BINDING
 
@@ -862,6 +864,89 @@ def logits_process(logits: torch.Tensor, *, tokens: torch.Tensor | None = None, 
     the penalties fp32."""
     return _binding().logits_process(logits, tokens, begin, end, prompt_end, repetition, frequency, presence, bias_ids,
                                      bias_values, bias_offsets, mask, out)
+
+
+class KVCacheI8(NamedTuple):
+    """A paged cache of keys and values: int8 rows with an fp32 scale each, of
+    pages of a power of two from 16 positions on and heads of a multiple of 16
+    up to 256 values.  Views are fine while the values of a row (and the scales
+    of a page's head) lie together, k and v have the same strides, and those are
+    multiples of 16 bytes.  A slot is page * page_size + place."""
+    k: torch.Tensor                    # int8 [pages, heads, page_size, d]
+    k_scale: torch.Tensor              # fp32 [pages, heads, page_size]
+    v: torch.Tensor
+    v_scale: torch.Tensor
+
+
+def kv_cache_i8(pages: int, heads: int, page_size: int, d: int, device) -> KVCacheI8:
+    """An empty cache: zeros."""
+    codes = lambda: torch.zeros((pages, heads, page_size, d), dtype=torch.int8, device=device)
+    scale = lambda: torch.zeros((pages, heads, page_size), dtype=torch.float32, device=device)
+    return KVCacheI8(codes(), scale(), codes(), scale())
+
+
+def kv_cache_write_i8(k: torch.Tensor, v: torch.Tensor, cache: KVCacheI8, slots: torch.Tensor) -> KVCacheI8:
+    """Writes the keys and values [tokens, heads, d] (fp32, fp16 or bf16; the
+    values of a head together) into the cache's slots (int64 [tokens]), by the
+    rule of i8_quantize_rows.  A token whose slot is outside the cache (-1, a
+    padded entry) is skipped; the slots of the others must differ."""
+    _binding().kv_cache_write_i8(k, v, cache, slots)
+    return cache
+
+
+def kv_cache_read_i8(cache: KVCacheI8, slots: torch.Tensor, *, dtype: torch.dtype = torch.float32,
+                     k_out: torch.Tensor | None = None,
+                     v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The keys and values of slots (int64 [tokens]) as [tokens, heads, d], zeros
+    for a slot outside the cache.  k_out and v_out are float32, float16 or
+    bfloat16, both of one type (dtype if they are made here)."""
+    return _binding().kv_cache_read_i8(cache, slots, dtype, k_out, v_out)
+
+
+def paged_attention_workspace_bytes(seqs: int, cols: int, heads: int, kv_heads: int, d: int, max_visible: int) -> int:
+    """Bytes of workspace that paged_attention_i8 needs at these sizes."""
+    return lib().paged_attention_workspace_bytes(seqs, cols, heads, kv_heads, d, max_visible)
+
+
+def paged_attention_i8(q: torch.Tensor, cache: KVCacheI8, pages: torch.Tensor, visible: torch.Tensor, *,
+                       scale: float | None = None, max_visible: int | None = None, out: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [seqs, cols, heads, d] (fp32, fp16 or bf16; up to 8 columns)
+    over the cache; heads is a multiple of the cache's.
+
+    Position i of sequence s lies in page pages[s, i // page_size] (int32 [seqs,
+    n]); column c of it sees the positions before visible[s, c] (int32 [seqs,
+    cols]), so a step's own columns are causal with visible[s, c] = length -
+    (cols - 1 - c).  A column that sees nothing gives zeros, and pages outside
+    the cache are not seen.  scale is d ** -0.5 unless given.  max_visible bounds
+    visible (by default what the table holds); a close one is faster.  workspace:
+    uint8, of paged_attention_workspace_bytes; made here if not given, and not to
+    be shared by calls that may run at the same time."""
+    return _binding().paged_attention_i8(q, cache, pages, visible, scale, max_visible, out, workspace)
+
+
+def logits_sample_workspace_bytes(rows: int, vocab: int) -> int:
+    """Bytes of workspace that logits_sample needs at these sizes."""
+    return lib().logits_sample_workspace_bytes(rows, vocab)
+
+
+def logits_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor | None = None,
+                  top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                  min_p: torch.Tensor | None = None, token: torch.Tensor | None = None,
+                  logprob: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Draws a token for each row of logits [rows, vocab] (fp32, fp16 or bf16)
+    from the given numbers u [rows] in [0, 1): (token int32 [rows], logprob fp32
+    [rows], the logarithm of the probability it was drawn with).
+
+    The rules, each a vector [rows] or left out: temperature (0: the largest
+    logit), top_k (int32, 0: all), top_p (1: all) of what top-k leaves, min_p
+    relative to the largest; fp32 but top_k.  Equal logits rank by index.  The
+    token is the first, in the order of the indexes, up to which there is more
+    than u of the mass that is left; -1 where a row has no finite logit.
+    workspace: uint8, of logits_sample_workspace_bytes, as for
+    paged_attention_i8."""
+    return _binding().logits_sample(logits, u, temperature, top_k, top_p, min_p, token, logprob, workspace)
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,633 @@
+"""The cache, attention and sampling operators on the GPU, against their numpy
+forms: the cache exactly, tokens exactly, attention within a bound that counts
+the roundings (attention_bound)."""
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import quantized_moe_expert_q8_amd as moeq8  # noqa: E402
+from oracle import decode_ref as ref  # noqa: E402
+from _gpu import DEV, say  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+CANARY = 77
+
+
+def typed(a, dtype):
+    """fp32 numpy values -> (CPU tensor of dtype, the fp32 values it holds)."""
+    t = torch.from_numpy(np.ascontiguousarray(a, dtype=np.float32)).to(dtype)
+    return t, t.float().numpy()
+
+
+def make_cache(pages, heads, size, d, layout="head", seed=0, lead=0, gap=0):
+    """A cache of random codes on the device (views of canaried buffers) and its numpy copy.
+
+    layout "head": [page][head][place]; "token": [page][place][head]; gap: bytes between rows."""
+    rng = np.random.default_rng(seed)
+    out, buffers = [], []
+    row = d + gap
+    for _ in range(2):
+        codes = rng.integers(-127, 128, (pages, heads, size, d)).astype(np.int8)
+        scale = rng.uniform(0.005, 0.03, (pages, heads, size)).astype(np.float32)
+        buf = torch.full((lead + pages * heads * size * row + 64,), CANARY, dtype=torch.int8, device=DEV)
+        strides = (heads * size * row, size * row, row, 1) if layout == "head" else (heads * size * row, row, heads * row, 1)
+        view = buf.as_strided((pages, heads, size, d), strides, lead)
+        view.copy_(torch.from_numpy(codes))
+        sbuf = torch.full((lead + pages * heads * size + 64,), float(CANARY), device=DEV)
+        sview = sbuf[lead:lead + scale.size].view(pages, heads, size)
+        sview.copy_(torch.from_numpy(scale))
+        out += [view, sview]
+        buffers += [(buf, view), (sbuf, sview)]
+    arrays = [t.cpu().numpy().copy() for t in out]
+    return moeq8.KVCacheI8(*out), arrays, buffers
+
+
+def frames_kept(buffers):
+    """Whether everything in the buffers outside the views is as it was."""
+    for buf, view in buffers:
+        inside = torch.zeros(buf.numel(), dtype=torch.bool, device=DEV)
+        inside.as_strided(view.shape, view.stride(), view.storage_offset()).fill_(True)
+        if not bool((buf[~inside] == CANARY).all()):
+            return False
+    return True
+
+
+def same(a, b):
+    """Equal values, NaN where NaN."""
+    a, b = np.asarray(a), np.asarray(b)
+    return a.shape == b.shape and bool(np.all((a == b) | (np.isnan(a) & np.isnan(b))))
+
+
+# ---- the cache ---------------------------------------------------------------
+
+def check_cache(tokens, heads, d, size, dtype, layout="head", lead=0, gap=0, special=False, seed=0):
+    rng = np.random.default_rng(seed)
+    pages = 2 * (-(-tokens // size)) + 1
+    cache, arrays, buffers = make_cache(pages, heads, size, d, layout, seed, lead, gap)
+    slots = rng.permutation(pages * size)[:tokens].astype(np.int64)
+    if tokens > 3:
+        slots[rng.integers(0, tokens, 2)] = [-1, pages * size]
+        slots[tokens // 2] = -2**62
+    x = rng.standard_normal((2, tokens, heads, d)) * np.exp(rng.uniform(-6, 6, (2, tokens, heads, 1)))
+    if special:
+        x[0, 0, 0] = 0
+        x[0, 1 % tokens, 0, 3] = np.inf
+        x[1, 2 % tokens, -1, 1] = np.nan
+        x[1, 0, 0] = 1e-7 * np.arange(d)
+    # rows of a projection's output: queries before the keys and values
+    width = 2 * d + 2 * heads * d + 3
+    ft = torch.zeros((tokens, width), dtype=dtype)
+    xt, xv = typed(x, dtype)
+    ft[:, 2 * d + 1:2 * d + 1 + 2 * heads * d] = xt.permute(1, 0, 2, 3).reshape(tokens, -1)
+    fd = ft.to(DEV)
+    k, v = (fd[:, 2 * d + 1 + i * heads * d:][:, :heads * d].view(tokens, heads, d) for i in range(2))
+    st = torch.from_numpy(slots).to(DEV)
+    assert moeq8.kv_cache_write_i8(k, v, cache, st) is cache
+    torch.cuda.synchronize()
+    for i in range(2):
+        ref.cache_write(arrays[2 * i], arrays[2 * i + 1], xv[i], slots)
+    for t, a in zip(cache, arrays):
+        assert same(t.cpu().numpy(), a)
+    assert frames_kept(buffers)
+    # back: the written slots, some twice, some outside
+    back = np.concatenate([slots, slots[:3], [-5, pages * size, 0]]).astype(np.int64)
+    n = len(back)
+    bufs = [torch.full((n, heads, d + 5), float(CANARY), dtype=dtype, device=DEV) for _ in range(2)]
+    outs = moeq8.kv_cache_read_i8(cache, torch.from_numpy(back).to(DEV), k_out=bufs[0][..., :d], v_out=bufs[1][..., :d])
+    torch.cuda.synchronize()
+    for i in range(2):
+        want = torch.from_numpy(ref.cache_read(arrays[2 * i], arrays[2 * i + 1], back)).to(dtype).float().numpy()
+        assert same(outs[i].float().cpu().numpy(), want)
+        assert bool((bufs[i][..., d:] == CANARY).all())
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("tokens,heads,d,size", [(1, 1, 16, 16), (1, 8, 128, 16), (5, 3, 80, 32), (17, 2, 32, 16),
+                                                 (33, 4, 64, 128), (70, 5, 256, 16), (130, 1, 144, 64), (300, 2, 112, 16)])
+def test_cache_rows(tokens, heads, d, size, dtype):
+    check_cache(tokens, heads, d, size, TYPES[dtype], special=True, seed=tokens + d)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("layout,lead,gap", [("token", 0, 0), ("head", 16, 16), ("token", 32, 48)])
+def test_cache_layouts(layout, lead, gap, dtype):
+    check_cache(40, 3, 96, 16, TYPES[dtype], layout, lead, gap, seed=5)
+
+
+def test_cache_rows_equal_the_int8_rows():
+    torch.manual_seed(1)
+    x = torch.randn(50, 4, 128, device=DEV).to(torch.bfloat16)
+    cache = moeq8.kv_cache_i8(4, 4, 16, 128, DEV)
+    moeq8.kv_cache_write_i8(x, 2 * x, cache, torch.arange(50, device=DEV))
+    for i, y in enumerate((x, 2 * x)):
+        q, s = moeq8.i8_quantize_rows(y.reshape(200, 128))
+        codes = cache[2 * i].transpose(1, 2).reshape(64, 4, 128)
+        assert torch.equal(codes[:50].reshape(200, 128), q) and not codes[50:].any()
+        assert torch.equal(cache[2 * i + 1].transpose(1, 2).reshape(64, 4)[:50].reshape(200), s)
+
+
+def test_cache_made_outputs_and_nothing_to_do():
+    cache = moeq8.kv_cache_i8(2, 1, 16, 32, DEV)
+    none = torch.empty(0, dtype=torch.int64, device=DEV)
+    moeq8.kv_cache_write_i8(torch.empty(0, 1, 32, device=DEV), torch.empty(0, 1, 32, device=DEV), cache, none)
+    k, v = moeq8.kv_cache_read_i8(cache, none, dtype=torch.float16)
+    assert k.shape == v.shape == (0, 1, 32) and k.dtype == torch.float16
+    k, v = moeq8.kv_cache_read_i8(cache, torch.tensor([3, -1], device=DEV), dtype=torch.bfloat16)
+    assert k.dtype == v.dtype == torch.bfloat16 and not k.any() and not v.any()
+
+
+# ---- attention ---------------------------------------------------------------
+
+def attention_bound(out, sizes, dtype, d):
+    """How far a result may be off, from the roundings of the operator.
+
+    A score t (in units of the exponent): its inner product is a sum of d fp32
+    terms (d 2^-23 of the sum of |q||k|, with products and sums rounded or cut),
+    fp32 queries are held to 2^-22 of each value, the two scales, the factor and
+    the subtraction of the maximum round once each (5 2^-24 of twice the largest
+    |t|).  A weight's relative error is that, 2^-22 for the exponential, and its
+    fp16 parts (2^-11 for bf16 outputs, else 2^-21); the sum of weights has the
+    first two, so they count twice.  Sums over positions run through chains of at
+    most 64 + n / 32 additions of 2^-23 each.  Parts below the fp16 range lose
+    2^-37 of the largest weight each.  At last the output's own half step."""
+    absolute, dots, largest, count = sizes
+    n = count[..., None]
+    score = (d * 2.0**-23 + (2.0**-22 if dtype == torch.float32 else 0.0)) * dots + 10 * 2.0**-24 * largest
+    weight = 2 * np.expm1(score[..., None] + 2.0**-22) + (2.0**-11 if dtype == torch.bfloat16 else 2.0**-21)
+    relative = weight + 2 * (64 + n / 32) * 2.0**-23 + 4 * 2.0**-24
+    tiny = n * 2.0**-37 * 127 * 0.03
+    return absolute * relative + tiny + (torch.finfo(dtype).eps / 2) * (np.abs(out) + absolute * relative) + 2.0**-25
+
+
+def check_attention(seqs, cols, heads, kv, d, size, visible, dtype, *, layout="head", lead=0, gap=0, loud=1.5, scale=None,
+                    most=None, bad=(), spoil=False, seed=0, extra=1):
+    """bad: (sequence, entry, page) put into the table; spoil: NaN and infinite scales where nothing is seen."""
+    rng = np.random.default_rng(seed)
+    visible = np.asarray(visible, np.int64).reshape(seqs, cols)
+    count = [-(-max(int(v.max()), 0) // size) for v in visible]
+    width = max(max(count), 1) + extra
+    pages = sum(count) + 2
+    cache, arrays, buffers = make_cache(pages, kv, size, d, layout, seed, lead, gap)
+    free = rng.permutation(pages)
+    table = np.full((seqs, width), -1, np.int32)
+    at = 0
+    for s, n in enumerate(count):
+        table[s, :n] = free[at:at + n]
+        at += n
+    for s, entry, page in bad:
+        table[s, entry] = page
+    if spoil:
+        used = np.zeros((pages, size), bool)
+        for s in range(seqs):
+            for i in range(max(int(visible[s].max()), 0)):
+                if 0 <= table[s, i // size] < pages:
+                    used[table[s, i // size], i % size] = True
+        for i, value in ((1, np.nan), (3, np.inf)):
+            a = arrays[i]
+            a.transpose(0, 2, 1)[~used] = value
+            cache[i].copy_(torch.from_numpy(a))
+    q, qv = typed(loud * rng.standard_normal((seqs, cols, heads, d)), dtype)
+    wide = torch.full((seqs, cols, heads + 3, d), float(CANARY), dtype=dtype, device=DEV)
+    wide[:, :, 1:heads + 1] = q.to(DEV)
+    obuf = torch.full((seqs, cols, heads + 2, d), float(CANARY), dtype=dtype, device=DEV)
+    got = moeq8.paged_attention_i8(wide[:, :, 1:heads + 1], cache, torch.from_numpy(table).to(DEV),
+                                   torch.from_numpy(visible.astype(np.int32)).to(DEV), scale=scale, max_visible=most,
+                                   out=obuf[:, :, 1:heads + 1])
+    torch.cuda.synchronize()
+    seen = visible if most is None else np.minimum(visible, most)
+    want, sizes = ref.attention(qv, *arrays, table, seen, d ** -0.5 if scale is None else scale)
+    err = np.abs(got.float().cpu().numpy().astype(np.float64) - want)
+    bound = attention_bound(want, sizes, dtype, d)
+    worst = float((err / bound).max())
+    say(f"attention {seqs}x{cols} heads {heads}/{kv} d {d} page {size} {dtype}: {worst:.3f} of the bound")
+    assert worst <= 1.0
+    assert not got[torch.from_numpy(sizes[3] == 0).to(DEV)].any()
+    assert bool((obuf[:, :, 0] == CANARY).all()) and bool((obuf[:, :, -1] == CANARY).all())
+    assert frames_kept(buffers)
+    return got
+
+
+def causal(lengths, cols):
+    return [[n - (cols - 1 - c) for c in range(cols)] for n in lengths]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("n", [1, 15, 16, 17, 31, 32, 33, 127, 128, 129, 300])
+def test_attention_lengths(n, dtype):
+    check_attention(2, 1, 4, 2, 64, 16, [[n], [max(n - 1, 0)]], TYPES[dtype], seed=n)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128, 144, 192, 208, 256])
+def test_attention_head_sizes(d, dtype):
+    check_attention(2, 2, 6, 3, d, 16, causal([75, 40], 2), TYPES[dtype], seed=d)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("cols,heads,kv,d", [(1, 1, 1, 64), (1, 16, 1, 64), (1, 17, 1, 128), (5, 32, 8, 128), (8, 16, 4, 64),
+                                             (8, 16, 2, 128), (7, 7, 1, 128), (8, 16, 2, 256), (3, 40, 2, 80), (8, 17, 1, 64),
+                                             (8, 20, 1, 128), (8, 9, 1, 256)])
+def test_attention_rows(cols, heads, kv, d, dtype):
+    check_attention(2, cols, heads, kv, d, 32, causal([90, 6], cols), TYPES[dtype], seed=cols * heads)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("size", [16, 32, 64, 256])
+def test_attention_spans_and_pages(size, dtype):
+    """Enough positions for several spans, joined, beside short and empty sequences."""
+    check_attention(4, 2, 4, 2, 64, size, causal([2100, 0, 700, 257], 2), TYPES[dtype], seed=size, spoil=True)
+
+
+def test_attention_one_long_sequence():
+    check_attention(1, 1, 2, 1, 64, 64, [[9001]], torch.float32, seed=3)
+    check_attention(1, 5, 4, 1, 128, 16, causal([3001], 5), torch.bfloat16, seed=4)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("layout,lead,gap", [("token", 0, 0), ("head", 16, 16), ("token", 32, 48)])
+def test_attention_layouts(layout, lead, gap, dtype):
+    check_attention(2, 2, 6, 3, 96, 16, causal([333, 70], 2), TYPES[dtype], layout=layout, lead=lead, gap=gap, seed=6)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_columns_that_see_nothing_or_anything(dtype):
+    visible = [[0, 5, 0, 40], [-3, 0, -2**31, 0], [64, 1, 33, 2**31 - 1], [100, 700, 3, 16]]
+    check_attention(4, 4, 4, 2, 64, 16, np.minimum(visible, 800), TYPES[dtype], seed=8, spoil=True)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_bad_pages_are_not_seen(dtype):
+    bad = [(0, 1, -1), (0, 3, 2**31 - 1), (0, 5, -2**31), (1, 0, 100), (1, 1, 99), (2, 0, -7)]
+    check_attention(3, 2, 4, 2, 64, 16, causal([100, 32, 10], 2), TYPES[dtype], bad=bad, seed=9, spoil=True)
+    check_attention(3, 2, 4, 2, 64, 16, causal([2000, 32, 300], 2), TYPES[dtype], bad=bad, seed=9, spoil=True)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_bounds_of_what_is_seen(dtype):
+    """max_visible and the table's end bound what is seen."""
+    check_attention(2, 2, 2, 1, 64, 16, causal([500, 400], 2), TYPES[dtype], most=300, seed=10)
+    check_attention(2, 2, 2, 1, 64, 16, causal([500, 400], 2), TYPES[dtype], most=0, seed=10)
+    check_attention(2, 2, 2, 1, 64, 16, causal([500, 400], 2), TYPES[dtype], most=70000, seed=10, extra=0)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("loud,scale", [(40.0, None), (1e-4, None), (1.0, 0.0), (1.0, -0.2), (0.0, None), (1.0, 3.0)])
+def test_attention_scores_large_and_small(loud, scale, dtype):
+    check_attention(2, 2, 4, 2, 64, 16, causal([200, 90], 2), TYPES[dtype], loud=loud, scale=scale, seed=11)
+
+
+def test_attention_queries_far_from_one():
+    """Queries past what fp16 holds, and below it: the row's power of two is taken out."""
+    rng = np.random.default_rng(12)
+    cache, arrays, _ = make_cache(4, 1, 16, 64, seed=12)
+    table = np.arange(4, dtype=np.int32)[None]
+    base = rng.standard_normal((1, 1, 1, 64)).astype(np.float32)
+    for up in (-140, -100, -30, 20, 100, 120):
+        q = np.ldexp(base, up).astype(np.float32)
+        scale = min(2.0**-up * 0.2, 1e38)                  # what an fp32 factor holds
+        got = moeq8.paged_attention_i8(torch.from_numpy(q).to(DEV), cache, torch.from_numpy(table).to(DEV),
+                                       torch.full((1, 1), 60, dtype=torch.int32, device=DEV),
+                                       scale=scale)
+        want, sizes = ref.attention(q, *arrays, table, [[60]], scale)
+        err = np.abs(got.cpu().numpy() - want)
+        assert (err <= attention_bound(want, sizes, torch.float32, 64)).all(), up
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_not_finite_stays_with_who_sees_it(dtype):
+    torch.manual_seed(1)
+    t = TYPES[dtype]
+    cache, arrays, _ = make_cache(8, 1, 16, 64, seed=13)
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None]
+    q = torch.randn(1, 4, 2, 64, device=DEV).to(t)
+    visible = torch.tensor([[30, 40, 50, 120]], dtype=torch.int32, device=DEV)
+    run = lambda: moeq8.paged_attention_i8(q, cache, table, visible).float().cpu()
+    clean = run()
+    for value in (float("nan"), float("inf")):
+        for i in (1, 3):                                   # position 45: columns 2 and 3 see it
+            keep = cache[i][2, 0, 13].item()
+            cache[i][2, 0, 13] = value
+            got = run()
+            assert torch.equal(got[:, :2], clean[:, :2])
+            # an infinite key scale times a negative product is a score of -inf, whose weight
+            # is 0: that row stays finite, and is compared
+            arrays[i][2, 0, 13] = value
+            with np.errstate(all="ignore"):
+                want, sizes = ref.attention(q.float().cpu().numpy(), *arrays, table.cpu().numpy(), visible.cpu().numpy(), 0.125)
+                finite = np.isfinite(want)
+                assert np.array_equal(np.isfinite(got.numpy()), finite)
+                assert not finite[:, 2:].all() and finite[:, :2].all()
+                ordinary = lambda a: np.where(np.isfinite(a), a, 1e3)
+                bound = attention_bound(want, (sizes[0], ordinary(sizes[1]), ordinary(sizes[2]), sizes[3]), t, 64)
+                assert (np.abs(got.numpy() - want) <= bound)[finite].all()
+            arrays[i][2, 0, 13] = keep
+            cache[i][2, 0, 13] = keep
+    q[0, 1, 1, 7] = float("nan")
+    got = run()
+    assert torch.isnan(got[0, 1, 1]).all()
+    clean[0, 1, 1] = got[0, 1, 1] = 0
+    assert torch.equal(got, clean)
+
+
+def test_attention_scales_of_any_size():
+    """Value scales from below to above the normal range, zero rows, a largest scale that grows."""
+    torch.manual_seed(1)
+    cache, arrays, _ = make_cache(20, 1, 16, 64, seed=14)
+    table = torch.arange(20, dtype=torch.int32, device=DEV)[None]
+    q = torch.randn(1, 1, 2, 64, device=DEV)
+    for low, high in ((-140, -120), (-60, 60), (100, 115), (-5, -5)):
+        s = np.ldexp(1.0, np.linspace(low, high, 320).astype(int)).astype(np.float32).reshape(20, 1, 16)
+        arrays[3][:] = s
+        arrays[3][::3] = 0
+        cache.v_scale.copy_(torch.from_numpy(arrays[3]))
+        got = moeq8.paged_attention_i8(q, cache, table, torch.full((1, 1), 320, dtype=torch.int32, device=DEV))
+        want, sizes = ref.attention(q.cpu().numpy(), *arrays, table.cpu().numpy(), [[320]], 0.125)
+        err = np.abs(got.cpu().numpy() - want)
+        relative = attention_bound(np.zeros_like(want), (np.ones_like(want), *sizes[1:]), torch.float32, 64)
+        top = 127 * arrays[3].max()
+        assert (err <= relative * (sizes[0] + 2.0**-22 * top) + 320 * 2.0**-37 * top).all(), (low, high)
+
+
+def test_attention_cache_past_32_bits():
+    """Pages 3 GB apart, and a table whose entries reach them."""
+    torch.manual_seed(1)
+    size, d, apart = 16, 64, 3 << 30
+    buf = torch.empty(apart + size * d, dtype=torch.int8, device=DEV)
+    rng = np.random.default_rng(15)
+    codes = rng.integers(-127, 128, (2, 1, size, d)).astype(np.int8)
+    view = buf.as_strided((2, 1, size, d), (apart, size * d, d, 1))
+    view.copy_(torch.from_numpy(codes))
+    scale = torch.rand(2, 1, size, device=DEV) * 0.02
+    cache = moeq8.KVCacheI8(view, scale, view, scale)
+    q = torch.randn(1, 1, 1, d, device=DEV)
+    table = torch.tensor([[1, 0]], dtype=torch.int32, device=DEV)
+    got = moeq8.paged_attention_i8(q, cache, table, torch.full((1, 1), 29, dtype=torch.int32, device=DEV))
+    s = scale.cpu().numpy()
+    want, sizes = ref.attention(q.cpu().numpy(), codes, s, codes, s, [[1, 0]], [[29]], d ** -0.5)
+    assert (np.abs(got.cpu().numpy() - want) <= attention_bound(want, sizes, torch.float32, d)).all()
+    k, _ = moeq8.kv_cache_read_i8(cache, torch.tensor([size + 3, 2], device=DEV))
+    assert same(k.cpu().numpy(), ref.cache_read(codes, s, [size + 3, 2]))
+
+
+def test_attention_workspace_is_kept_within():
+    torch.manual_seed(1)
+    args = (1, 2, 4, 2, 64, 3000)
+    n = moeq8.paged_attention_workspace_bytes(*args)
+    assert n > 0
+    buf = torch.full((n + 64,), CANARY, dtype=torch.uint8, device=DEV)
+    cache, _, _ = make_cache(200, 2, 16, 64, seed=16)
+    table = torch.randperm(200, device=DEV).to(torch.int32)[None]
+    q = torch.randn(1, 2, 4, 64, device=DEV)
+    visible = torch.tensor([[2999, 3000]], dtype=torch.int32, device=DEV)
+    a = moeq8.paged_attention_i8(q, cache, table, visible, max_visible=3000)
+    b = moeq8.paged_attention_i8(q, cache, table, visible, max_visible=3000, workspace=buf[:n])
+    assert torch.equal(a, b) and bool((buf[n:] == CANARY).all())
+    with pytest.raises(ValueError):
+        moeq8.paged_attention_i8(q, cache, table, visible, max_visible=3000, workspace=buf[:n - 1])
+    none = torch.empty(0, 2, 4, 64, device=DEV)
+    assert moeq8.paged_attention_i8(none, cache, table[:0], visible[:0]).shape == none.shape
+
+
+# ---- sampling ----------------------------------------------------------------
+
+def check_sample(z, u, dtype, lead=0, pad=0, **rules):
+    rows, vocab = z.shape
+    zt, zv = typed(z, dtype)
+    buf = torch.full((lead + rows * (vocab + pad) + 8,), 1e30 if dtype != torch.float16 else 6e4, dtype=dtype, device=DEV)
+    zd = buf[lead:lead + rows * (vocab + pad)].view(rows, vocab + pad)[:, :vocab]
+    zd.copy_(zt)
+    u = np.asarray(u, np.float32)
+    types = dict(temperature=np.float32, top_k=np.int32, top_p=np.float32, min_p=np.float32)
+    rules = {k: np.broadcast_to(np.asarray(v, types[k]), (rows,)).copy() for k, v in rules.items()}
+    token, logprob = moeq8.logits_sample(zd, torch.from_numpy(u).to(DEV),
+                                         **{k: torch.from_numpy(v).to(DEV) for k, v in rules.items()})
+    token, logprob = token.cpu().numpy(), logprob.cpu().numpy()
+    for r in range(rows):
+        want, log = ref.sample_row(zv[r], float(u[r]), **{k: v[r].item() for k, v in rules.items()})
+        assert token[r] == want, (r, token[r], want)
+        # x = (z - max) / T and the logarithm of the mass in 64 bits, one rounding to fp32
+        assert logprob[r] == log or abs(logprob[r] - log) <= 2.0**-23 * max(abs(log), 1e-7), (r, logprob[r], log)
+    return token
+
+
+def some_logits(rows, vocab, seed, loud=3.0):
+    rng = np.random.default_rng(seed)
+    return loud * rng.standard_normal((rows, vocab)), rng.uniform(0, 1, rows)
+
+
+RULES = [dict(), dict(temperature=0.7), dict(top_k=5), dict(top_k=40, temperature=1.3), dict(top_p=0.9),
+         dict(top_p=0.5, temperature=2.0), dict(min_p=0.05), dict(top_k=50, top_p=0.8, min_p=0.02, temperature=0.9),
+         dict(temperature=0.0), dict(top_k=1), dict(top_k=3000, top_p=0.99), dict(top_p=0.9999, temperature=5.0)]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rules", RULES, ids=lambda r: "-".join(f"{k}{v}" for k, v in r.items()) or "none")
+def test_sample_rules(rules, dtype):
+    z, u = some_logits(6, 5003, 21)
+    check_sample(z, u, TYPES[dtype], **rules)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [1, 2, 63, 64, 65, 511, 512, 513, 1024, 4097, 32000])
+def test_sample_sizes(vocab, dtype):
+    z, u = some_logits(3, vocab, vocab)
+    for rules in (dict(), dict(top_k=7), dict(top_p=0.9), dict(top_k=20, top_p=0.7, min_p=0.1)):
+        check_sample(z, u, TYPES[dtype], **rules)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("lead,pad", [(0, 0), (1, 0), (3, 5), (8, 8), (2, 1)])
+def test_sample_strides(lead, pad, dtype):
+    z, u = some_logits(5, 2051, 22)
+    check_sample(z, u, TYPES[dtype], lead, pad)
+    check_sample(z, u, TYPES[dtype], lead, pad, top_k=30, top_p=0.9)
+    check_sample(z, u, TYPES[dtype], lead, pad, top_p=0.95)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_sample_rows_of_their_own_rules(dtype):
+    z, u = some_logits(24, 3001, 23)
+    rng = np.random.default_rng(24)
+    check_sample(z, u, TYPES[dtype], temperature=np.where(rng.random(24) < 0.2, 0, rng.uniform(0.3, 2, 24)),
+                 top_k=np.where(rng.random(24) < 0.5, 0, rng.integers(1, 400, 24)),
+                 top_p=np.where(rng.random(24) < 0.5, 1, rng.uniform(0.1, 0.999, 24)),
+                 min_p=np.where(rng.random(24) < 0.5, 0, rng.uniform(0.001, 0.5, 24)))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [5, 700, 9000])
+def test_sample_equal_logits(vocab, dtype):
+    """Ties at every border: all equal, and few distinct values."""
+    u = np.array([0.0, 0.25, 0.5, 0.999, 0.75], np.float32)
+    for z in (np.zeros((5, vocab)), np.random.default_rng(25).integers(0, 4, (5, vocab)).astype(float),
+              -np.broadcast_to(np.arange(vocab) // 3, (5, vocab)).astype(float)):
+        for rules in (dict(), dict(top_k=3), dict(top_k=vocab // 2), dict(top_p=0.37), dict(top_p=1e-6), dict(min_p=1.0),
+                      dict(min_p=0.3), dict(top_k=vocab // 2 + 1, top_p=0.61), dict(temperature=0.0), dict(top_k=vocab + 9)):
+            check_sample(z, u, TYPES[dtype], **rules)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [40, 3000])
+def test_sample_masked_and_not_finite(vocab, dtype):
+    z, u = some_logits(7, vocab, 26)
+    rng = np.random.default_rng(27)
+    z[0, rng.random(vocab) < 0.7] = -np.inf
+    z[1, :] = -np.inf
+    z[1, vocab - 1] = -3.0
+    z[2, :] = -np.inf
+    z[3, 5], z[3, vocab // 2], z[3, 9] = np.inf, np.inf, -np.inf
+    z[4, ::2] = np.nan
+    z[5, :] = np.nan
+    z[6, :] = -0.0
+    z[6, 1::2] = 0.0
+    for rules in (dict(), dict(top_k=10), dict(top_p=0.8), dict(min_p=0.1), dict(temperature=0.0), dict(top_k=2, top_p=0.5)):
+        token = check_sample(z, u, TYPES[dtype], **rules)
+        assert token[2] == token[5] == -1
+
+
+def test_sample_the_types_lowest_values():
+    """Masks of the lowest value, and logits past the range of the weights."""
+    for t in TYPES.values():
+        low = float(torch.finfo(t).min)
+        z, u = some_logits(4, 600, 28)
+        z[0, 100:] = low
+        z[1, :] = low
+        z[2, :] = low
+        z[2, 77] = float(torch.finfo(t).max)
+        z[3] *= 100
+        for rules in (dict(), dict(top_k=200), dict(top_p=0.9), dict(temperature=1e-3), dict(temperature=1e30), dict(top_k=550, top_p=0.9)):
+            check_sample(z, u, t, **rules)
+
+
+def test_sample_values_out_of_range():
+    z, _ = some_logits(8, 900, 29)
+    nan = float("nan")
+    check_sample(z, [0, 1 - 2.0**-24, 0.5, 0.5, 0.5, 0.5, 0.5, 0.5], torch.float32, top_k=[-5, 2**31 - 1, 0, 1, 900, 901, 899, -2**31],
+                 top_p=[2.0, 1.5, 0.0, -1.0, 1.0, 0.5, 0.999, 0.9], min_p=[-1, 0, 5, 1, 0, 0, 0, 0.5])
+    token, _ = moeq8.logits_sample(torch.from_numpy(z).float().to(DEV), torch.full((8,), nan, device=DEV),
+                                   temperature=torch.full((8,), nan, device=DEV))
+    assert token.tolist() == z.astype(np.float32).argmax(1).tolist()
+    token, _ = moeq8.logits_sample(torch.from_numpy(z).float().to(DEV), torch.full((8,), 1.0, device=DEV),
+                                   top_k=torch.full((8,), 3, dtype=torch.int32, device=DEV))
+    assert token.tolist() == [int(np.sort(np.argsort(-r, kind="stable")[:3])[-1]) for r in z.astype(np.float32)]
+
+
+def test_sample_no_vocabulary_and_no_rows():
+    token, logprob = moeq8.logits_sample(torch.empty(3, 0, device=DEV), torch.zeros(3, device=DEV))
+    assert token.tolist() == [-1] * 3 and logprob.tolist() == [float("-inf")] * 3
+    token, logprob = moeq8.logits_sample(torch.empty(0, 9, device=DEV), torch.zeros(0, device=DEV))
+    assert token.shape == logprob.shape == (0,)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sample_full_vocabulary(dtype):
+    z, u = some_logits(3, 131072, 30)
+    for rules in (dict(), dict(temperature=0.6, top_k=50, top_p=0.9), dict(top_p=0.95, min_p=0.02), dict(top_k=5000, top_p=0.9)):
+        check_sample(z, u, TYPES[dtype], **rules)
+
+
+def test_sample_frequencies_follow_the_weights():
+    """Equally spaced numbers draw each token as often as its weight says, to one each side."""
+    z = np.log([4.0, 1.0, 0.0 + 1e-30, 3.0, 2.0])
+    n = 4000
+    u = (np.arange(n) + 0.5) / n
+    token, _ = moeq8.logits_sample(torch.from_numpy(np.tile(z, (n, 1))).float().to(DEV), torch.from_numpy(u).float().to(DEV))
+    counts = np.bincount(token.cpu().numpy(), minlength=5)
+    assert np.abs(counts - n * np.array([0.4, 0.1, 0, 0.3, 0.2])).max() <= 1
+
+
+# ---- together, streams and graphs ----------------------------------------------
+
+def test_graph_replays_and_streams_equal_eager():
+    cache = moeq8.kv_cache_i8(64, 2, 16, 64, DEV)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV)
+    k, v, q = rand(3, 2, 64), rand(3, 2, 64), rand(1, 3, 4, 64)
+    slots = torch.tensor([700, 701, -1], device=DEV)
+    table = torch.arange(64, dtype=torch.int32, device=DEV)[None]
+    visible = torch.tensor([[700, 701, 702]], dtype=torch.int32, device=DEV)
+    z, u = rand(2, 20000), torch.rand(2, generator=g, device=DEV)
+    p = torch.full((2,), 0.9, device=DEV)
+    ws = torch.empty(moeq8.paged_attention_workspace_bytes(1, 3, 4, 2, 64, 1024), dtype=torch.uint8, device=DEV)
+    ws2 = torch.empty(moeq8.logits_sample_workspace_bytes(2, 20000), dtype=torch.uint8, device=DEV)
+
+    def step():
+        moeq8.kv_cache_write_i8(k, v, cache, slots)
+        return (moeq8.paged_attention_i8(q, cache, table, visible, workspace=ws), *moeq8.kv_cache_read_i8(cache, slots),
+                *moeq8.logits_sample(z, u, top_p=p, workspace=ws2))
+
+    for name in ("k", "v"):
+        getattr(cache, name).copy_(torch.randint(-127, 128, cache.k.shape, generator=g, device=DEV))
+        getattr(cache, name + "_scale").copy_(torch.rand(cache.k_scale.shape, generator=g, device=DEV) * 0.02)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    side = torch.cuda.Stream()
+    for i in range(4):
+        k.copy_(rand(3, 2, 64))
+        q.copy_(rand(1, 3, 4, 64))
+        z.copy_(rand(2, 20000))
+        slots.copy_(torch.tensor([700 + i, 900 - i, -1]))
+        visible.copy_(torch.tensor([[700 + i, 0, 1000 - i]]))
+        u.copy_(torch.rand(2, generator=g, device=DEV))
+        want = [t.clone() for t in step()]
+        torch.cuda.synchronize()
+        for t in held:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, want)), i
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            other = step()
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(other, want)), i
+
+
+def test_refusals():
+    cache = moeq8.kv_cache_i8(4, 2, 16, 32, DEV)
+    x, s = torch.zeros(3, 2, 32, device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV)
+    q, i = torch.zeros(1, 1, 4, 32, device=DEV), torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    z = torch.zeros(2, 9, device=DEV)
+    bad = [
+        (ValueError, lambda: moeq8.kv_cache_write_i8(x[:, :1], x, cache, s)),
+        (ValueError, lambda: moeq8.kv_cache_write_i8(x, x[:2], cache, s)),
+        (ValueError, lambda: moeq8.kv_cache_write_i8(x, x, cache, s[:2])),
+        (TypeError, lambda: moeq8.kv_cache_write_i8(x, x.half(), cache, s)),
+        (TypeError, lambda: moeq8.kv_cache_write_i8(x.double(), x.double(), cache, s)),
+        (TypeError, lambda: moeq8.kv_cache_write_i8(x, x, cache, s.int())),
+        (TypeError, lambda: moeq8.kv_cache_write_i8(x, x, cache[:3], s)),
+        (ValueError, lambda: moeq8.kv_cache_write_i8(torch.zeros(3, 2, 64, device=DEV)[..., ::2], x, cache, s)),
+        (ValueError, lambda: moeq8.kv_cache_write_i8(x, x, cache._replace(v=cache.v[:2]), s)),
+        (ValueError, lambda: moeq8.kv_cache_write_i8(x, x, cache._replace(v=cache.v.transpose(1, 2).contiguous().transpose(1, 2)), s)),
+        (TypeError, lambda: moeq8.kv_cache_write_i8(x, x, cache._replace(k_scale=cache.k_scale.half()), s)),
+        (moeq8.MoeQ8Error, lambda: moeq8.kv_cache_write_i8(x, x, moeq8.kv_cache_i8(4, 2, 8, 32, DEV), s)),
+        (TypeError, lambda: moeq8.kv_cache_read_i8(cache, s, dtype=torch.float64)),
+        (TypeError, lambda: moeq8.kv_cache_read_i8(cache, s, k_out=x.half(), v_out=x)),
+        (ValueError, lambda: moeq8.kv_cache_read_i8(cache, s, k_out=x[:2], v_out=x)),
+        (ValueError, lambda: moeq8.paged_attention_i8(q[:, :, :3], cache, i, i)),
+        (ValueError, lambda: moeq8.paged_attention_i8(q[..., :16], cache, i, i)),
+        (ValueError, lambda: moeq8.paged_attention_i8(q[0], cache, i, i)),
+        (ValueError, lambda: moeq8.paged_attention_i8(q, cache, i[0], i)),
+        (TypeError, lambda: moeq8.paged_attention_i8(q, cache, i.long(), i)),
+        (ValueError, lambda: moeq8.paged_attention_i8(q, cache, i, i.expand(1, 2))),
+        (moeq8.MoeQ8Error, lambda: moeq8.paged_attention_i8(q, cache, i, i, out=q)),
+        (moeq8.MoeQ8Error, lambda: moeq8.paged_attention_i8(q, cache, i, i, scale=float("nan"))),
+        (moeq8.MoeQ8Error, lambda: moeq8.paged_attention_i8(q, cache, i, i, max_visible=-1)),
+        (moeq8.MoeQ8Error, lambda: moeq8.paged_attention_i8(q.expand(1, 9, 4, 32).contiguous(), cache, i, i.expand(1, 9).contiguous())),
+        (ValueError, lambda: moeq8.logits_sample(z, z[0])),
+        (ValueError, lambda: moeq8.logits_sample(z[0], z[:, 0].contiguous())),
+        (TypeError, lambda: moeq8.logits_sample(z, z[:, 0].contiguous(), top_k=z[:, 0].contiguous())),
+        (TypeError, lambda: moeq8.logits_sample(z.double(), z[:, 0].contiguous())),
+    ]
+    for n, (err, call) in enumerate(bad):
+        with pytest.raises(err):
+            call()
+            say(f"refusal {n} did not raise")
+    torch.cuda.synchronize()
