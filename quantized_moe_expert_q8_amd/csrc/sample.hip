@@ -32,7 +32,7 @@ namespace {
 constexpr int SEG = 512;                          // logits a segment: 8 a lane
 constexpr int MAX_SEGS = 1024;                    // more: the slow way
 constexpr int BINS = 1024, PER_OCTAVE = 64;       // steps of the exponent's table; a bin is 4 of them
-constexpr int CAP = 6144;                         // candidates that k_pick holds
+constexpr int CAP = 4096;                         // candidates that k_pick holds
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
 constexpr int FEW_HITS = 96;                      // segments that pass min-p: candidates at once
 
@@ -60,7 +60,7 @@ __device__ __forceinline__ uint32_t key_of(float z) {
 __device__ __forceinline__ float logit_of(uint32_t key) {
     return __uint_as_float(key ^ (key >> 31 ? 0x80000000u : 0xffffffffu));
 }
-constexpr uint32_t KEY_INF = 0xff800000u;
+constexpr uint32_t KEY_INF = 0xff800000u, KEY_FIRST = 0x00800000u;       // of +inf and of the lowest finite logit
 
 // A row's rules.
 struct Rules {
@@ -73,19 +73,20 @@ struct Rules {
     // whether k_scan sums the masses: for the draw, or for top-p beside min-p
     __device__ bool masses() const { return !greedy && !k && (p < 1.0f) == (least > 0.0f); }
 };
-__device__ Rules rules_of(const SampleArgs& a, int64_t row) {
+__device__ __forceinline__ Rules rules_of(const SampleArgs& a, int64_t row) {
     Rules r;
-    const float t = a.temperature ? a.temperature[row] : 1.0f;
+    // a rule that is left out reads u's bits instead: loads under a branch each would
+    // be waited for one after another (2 us of the 20 that a row took)
+    const float* none = a.u;
+    float t = (a.temperature ? a.temperature : none)[row], p = (a.top_p ? a.top_p : none)[row], least = (a.min_p ? a.min_p : none)[row];
+    const int32_t k = (a.top_k ? a.top_k : (const int32_t*)none)[row];
+    t = a.temperature ? t : 1.0f;
     r.greedy = !(t > 0.0f);
-    r.k = a.top_k ? a.top_k[row] : 0;
-    if (r.k < 0 || r.k >= a.vocab) r.k = 0;
-    r.p = a.top_p ? a.top_p[row] : 1.0f;
-    if (!(r.p < 1.0f)) r.p = 1.0f;
-    r.least = a.min_p ? a.min_p[row] : 0.0f;
-    if (!(r.least > 0.0f)) r.least = 0.0f;
-    if (r.least > 1.0f) r.least = 1.0f;
+    r.k = a.top_k && k > 0 && k < a.vocab ? k : 0;
+    r.p = a.top_p && p < 1.0f ? p : 1.0f;
+    r.least = a.min_p && least > 0.0f ? fminf(least, 1.0f) : 0.0f;
     r.per_nat = 1.0 / (double)t;
-    r.per_logit = (PER_OCTAVE * 1.4426950408889634) / (double)t;
+    r.per_logit = (PER_OCTAVE * 1.4426950408889634) * r.per_nat;
     return r;
 }
 
@@ -127,23 +128,58 @@ __device__ __forceinline__ int bin_of(int i) {    // i <= 0
 }
 __device__ __forceinline__ int bin_of(const Weigh& w, float z) { return bin_of((int)rint(w.steps(z))); }
 
+// 2^(j / 64), correctly rounded.  From memory into LDS: a kernel that computed them
+// spent half a microsecond on that.
+__device__ const double POWERS[PER_OCTAVE] = {
+    0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
+    0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
+    0x1.172b83c7d517bp+0, 0x1.1a35beb6fcb75p+0, 0x1.1d4873168b9aap+0, 0x1.2063b88628cd6p+0,
+    0x1.2387a6e756238p+0, 0x1.26b4565e27cddp+0, 0x1.29e9df51fdee1p+0, 0x1.2d285a6e4030bp+0,
+    0x1.306fe0a31b715p+0, 0x1.33c08b26416ffp+0, 0x1.371a7373aa9cbp+0, 0x1.3a7db34e59ff7p+0,
+    0x1.3dea64c123422p+0, 0x1.4160a21f72e2ap+0, 0x1.44e086061892dp+0, 0x1.486a2b5c13cd0p+0,
+    0x1.4bfdad5362a27p+0, 0x1.4f9b2769d2ca7p+0, 0x1.5342b569d4f82p+0, 0x1.56f4736b527dap+0,
+    0x1.5ab07dd485429p+0, 0x1.5e76f15ad2148p+0, 0x1.6247eb03a5585p+0, 0x1.6623882552225p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.6dfb23c651a2fp+0, 0x1.71f75e8ec5f74p+0, 0x1.75feb564267c9p+0,
+    0x1.7a11473eb0187p+0, 0x1.7e2f336cf4e62p+0, 0x1.82589994cce13p+0, 0x1.868d99b4492edp+0,
+    0x1.8ace5422aa0dbp+0, 0x1.8f1ae99157736p+0, 0x1.93737b0cdc5e5p+0, 0x1.97d829fde4e50p+0,
+    0x1.9c49182a3f090p+0, 0x1.a0c667b5de565p+0, 0x1.a5503b23e255dp+0, 0x1.a9e6b5579fdbfp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b33a2b84f15fbp+0, 0x1.b7f76f2fb5e47p+0, 0x1.bcc1e904bc1d2p+0,
+    0x1.c199bdd85529cp+0, 0x1.c67f12e57d14bp+0, 0x1.cb720dcef9069p+0, 0x1.d072d4a07897cp+0,
+    0x1.d5818dcfba487p+0, 0x1.da9e603db3285p+0, 0x1.dfc97337b9b5fp+0, 0x1.e502ee78b3ff6p+0,
+    0x1.ea4afa2a490dap+0, 0x1.efa1bee615a27p+0, 0x1.f50765b6e4540p+0, 0x1.fa7c1819e90d8p+0,
+};
 __device__ __forceinline__ void fill_table(double* table) {
-    if (threadIdx.x < PER_OCTAVE) table[threadIdx.x] = exp2((double)threadIdx.x / PER_OCTAVE);
+    if (threadIdx.x < PER_OCTAVE) table[threadIdx.x] = POWERS[threadIdx.x];
 }
 
-// Eight logits of a segment from element `at` on; NaN past the row.
+// A lane's eight logits of segment `seg`, and the index of the first.  Where the row
+// ends inside them they are its last eight, of which those of another lane are NaN,
+// and past the row all are: loads without a branch, none of which waits for another.
 template <typename T>
-__device__ __forceinline__ void load8(float (&v)[8], const T* z, int64_t at, int64_t vocab) {
-    if (at + 8 <= vocab) {
-        T raw[8];
-        load_vec(raw, z + at);
+struct Eight {
+    T raw[8];
+    uint32_t first;
+    __device__ __forceinline__ void load(const T* z, uint32_t seg, uint32_t vocab) {
+        const uint32_t at = seg * SEG + (threadIdx.x & 63) * 8;
+        first = at + 8 <= vocab ? at : vocab - 8;
+        if (vocab >= 8) {
+            load_vec(raw, z + first);
+        } else {
+            first = at;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = to_f32(raw[j]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = at + j < vocab ? to_f32(z[at + j]) : __builtin_nanf("");
+            for (uint32_t j = 0; j < 8; ++j) raw[j] = z[at + j < vocab ? at + j : 0];
+        }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8], uint32_t seg, uint32_t vocab) const {
+#pragma unroll
+        for (uint32_t j = 0; j < 8; ++j) v[j] = to_f32(raw[j]);
+        if ((seg + 1) * SEG > vocab) {
+            const uint32_t at = seg * SEG + (threadIdx.x & 63) * 8;
+#pragma unroll
+            for (uint32_t j = 0; j < 8; ++j) v[j] = first + j >= at && first + j < vocab ? v[j] : __builtin_nanf("");
+        }
+    }
+};
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = larger(v, moved<XOR1>(v));
@@ -154,6 +190,16 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = larger(s[0], s[1]);
     s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
     return larger(s[0], s[1]);
+}
+__device__ __forceinline__ uint32_t wave_or(uint32_t v) {
+    v |= moved<XOR1>(v);
+    v |= moved<XOR2>(v);
+    v |= moved<HALF_MIRROR>(v);
+    v |= moved<MIRROR>(v);
+    auto s = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = s[0] | s[1];
+    s = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return s[0] | s[1];
 }
 __device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
     v += moved<XOR1>(v);
@@ -171,14 +217,42 @@ __device__ __forceinline__ uint64_t wave_sum(uint64_t v) {
     };
     return cross(cross(v, false), true);
 }
-// Sum over the lanes up to this one.
+// Sum over the lanes up to this one: within rows of 16 lanes, then over the rows.
+template <int CTRL, int ROWS, typename V>
+__device__ __forceinline__ V shifted(V v) {       // 0 where no lane is named
+    const uint2 u = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.x, CTRL, ROWS, 0xf, false),
+                                       (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u.y, CTRL, ROWS, 0xf, false)});
+}
+template <typename V>
+__device__ __forceinline__ V row_scan(V v) {
+    static_assert(sizeof(V) == 8, "two dwords");
+    v += shifted<0x111, 0xf>(v);                  // row_shr 1, 2, 4, 8
+    v += shifted<0x112, 0xf>(v);
+    v += shifted<0x114, 0xf>(v);
+    v += shifted<0x118, 0xf>(v);
+    return v;
+}
 template <typename V>
 __device__ __forceinline__ V wave_scan(V v) {
-    for (int i = 1; i < 64; i <<= 1) {
-        const V t = __shfl_up(v, i);
-        if ((int)(threadIdx.x & 63) >= i) v += t;
-    }
+    v = row_scan(v);
+    v += shifted<0x142, 0xa>(v);                  // the last lane of a row to the next one: rows 1 and 3
+    v += shifted<0x143, 0xc>(v);                  // of the first two to the last two
     return v;
+}
+__device__ __forceinline__ uint32_t wave_scan32(uint32_t v) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xf, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xa, 0xf, false);
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xc, 0xf, false);
+    return v;
+}
+template <typename V>
+__device__ __forceinline__ V of_lane(V v, int lane) {
+    const uint2 u = __builtin_bit_cast(uint2, v);
+    return __builtin_bit_cast(V, uint2{(uint32_t)__builtin_amdgcn_readlane((int)u.x, lane), (uint32_t)__builtin_amdgcn_readlane((int)u.y, lane)});
 }
 
 // ---- segments --------------------------------------------------------------------
@@ -187,12 +261,12 @@ template <typename T, int PER>
 __global__ __launch_bounds__(256) void k_scan(SampleArgs a, uint32_t blocks) {
     __shared__ double table[PER_OCTAVE];
     const uint32_t row = blockIdx.x / blocks, block = blockIdx.x - row * blocks;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const T* z = (const T*)a.z + row * a.z_stride;
-    const uint32_t first = (block * 4 + wave) * PER;
-    float v[PER][8];
+    const uint32_t first = (block * 4 + wave) * PER, vocab = (uint32_t)a.vocab;
+    Eight<T> e[PER];
 #pragma unroll
-    for (int s = 0; s < PER; ++s) load8(v[s], z, (int64_t)(first + s) * SEG + lane * 8, a.vocab);
+    for (int s = 0; s < PER; ++s) e[s].load(z, first + s < a.segs ? first + s : a.segs - 1, vocab);
     const Rules r = rules_of(a, row);
     const bool masses = r.masses();
     if (masses) {
@@ -202,15 +276,16 @@ __global__ __launch_bounds__(256) void k_scan(SampleArgs a, uint32_t blocks) {
 #pragma unroll
     for (int s = 0; s < PER; ++s) {
         if (first + s >= a.segs) break;
-        uint32_t top = 0;
+        float v[8], most = -__builtin_inff();
+        e[s].values(v, first + s, vocab);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = larger(top, key_of(v[s][j]));
-        top = wave_max(top);
+        for (int j = 0; j < 8; ++j) most = fmaxf(most, v[j]);
+        const uint32_t top = wave_max(key_of(most));
         uint64_t sum = 0;
         if (masses && top) {
             const Weigh w{(double)logit_of(top), r.per_logit, table};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) sum += v[s][j] > -__builtin_inff() ? w.units(v[s][j], 51) : 0;
+            for (int j = 0; j < 8; ++j) sum += v[j] > -__builtin_inff() ? w.units(v[j], 51) : 0;
             sum = wave_sum(sum);
         }
         if (lane == 0) {
@@ -225,36 +300,53 @@ __global__ __launch_bounds__(256) void k_scan(SampleArgs a, uint32_t blocks) {
 enum Way { NONE, GREEDY, PURE, LIST, BY_BINS, SLOW };
 
 struct Row {
-    uint32_t key;                                 // largest key of this thread's segment
+    uint32_t key;                                 // largest key of segment threadIdx.x (blocks of MAX_SEGS threads)
     uint32_t top;                                 // of the row
     Way way;
 };
 
-// Needs 2 * WAVES dwords of LDS; every thread of the block calls it.
-__device__ Row row_of(const SampleArgs& a, const Rules& r, int64_t row, uint32_t* lds, const double* table) {
+// Needs 2 * N / 64 dwords of LDS; every thread of the block calls it.
+template <int N>
+__device__ __forceinline__ Row row_of(const SampleArgs& a, const Rules& r, int64_t row, uint32_t* lds, const double* table) {
+    constexpr int PER = MAX_SEGS / N, W = N / 64;
+    static_assert(W == 4 || W == 16, "lanes that have a wave's result each: a quad or a row");
     Row o;
     const uint32_t tid = threadIdx.x;
-    o.key = tid < a.segs ? a.seg_top[row * a.segs + tid] : 0u;
-    const uint32_t most = wave_max(o.key);
+    uint32_t key[PER], most = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        key[i] = tid + i * N < a.segs ? a.seg_top[row * a.segs + tid + i * N] : 0u;
+        most = larger(most, key[i]);
+    }
+    o.key = key[0];
+    most = wave_max(most);
     if ((tid & 63) == 0) lds[tid >> 6] = most;
     __syncthreads();
-    o.top = 0;
-    for (int i = 0; i < WAVES; ++i) o.top = larger(o.top, lds[i]);
+    o.top = wave_max(lds[tid & (W - 1)]);
     // segments with a logit to draw, and those that pass min-p
     const Weigh w{(double)logit_of(o.top), r.per_logit, table};
-    const bool some = o.key != 0, passes = some && o.top != KEY_INF && w.real(logit_of(o.key)) >= (double)r.least;
-    const uint32_t packed = (uint32_t)__popcll(__ballot(some)) | (uint32_t)__popcll(__ballot(passes)) << 16;
-    if ((tid & 63) == 0) lds[WAVES + (tid >> 6)] = packed;
-    __syncthreads();
     uint32_t counts = 0;
-    for (int i = 0; i < WAVES; ++i) counts += lds[WAVES + i];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool some = key[i] != 0, passes = some && o.top != KEY_INF && w.real(logit_of(key[i])) >= (double)r.least;
+        counts += (uint32_t)__popcll(__ballot(some)) | (uint32_t)__popcll(__ballot(passes)) << 16;
+    }
+    if ((tid & 63) == 0) lds[W + (tid >> 6)] = counts;
+    __syncthreads();
+    counts = lds[W + (tid & (W - 1))];
+    counts += moved<XOR1>(counts);
+    counts += moved<XOR2>(counts);
+    if constexpr (W == 16) {
+        counts += moved<HALF_MIRROR>(counts);
+        counts += moved<MIRROR>(counts);
+    }
     const uint32_t segs = counts & 0xffffu, hits = counts >> 16;
     if (o.top == 0) o.way = NONE;
     else if (r.greedy) o.way = GREEDY;
     else if (o.top == KEY_INF) o.way = SLOW;
     else if (r.pure()) o.way = PURE;
     else if (segs <= CAP / SEG) o.way = LIST;
-    else if (r.k) o.way = r.k <= segs * 3 / 4 ? LIST : BY_BINS;
+    else if (r.k) o.way = r.k <= (segs <= 256 ? segs : segs * 3 / 4) ? LIST : BY_BINS;
     else if (r.least > 0.0f && hits <= FEW_HITS) o.way = LIST;
     else o.way = BY_BINS;
     return o;
@@ -263,90 +355,124 @@ __device__ Row row_of(const SampleArgs& a, const Rules& r, int64_t row, uint32_t
 // ---- bins --------------------------------------------------------------------------
 
 template <typename T>
-__global__ __launch_bounds__(THREADS) void k_bins(SampleArgs a) {
+__global__ __launch_bounds__(256) void k_bins(SampleArgs a) {
     __shared__ double table[PER_OCTAVE];
-    __shared__ uint32_t words[2 * WAVES];
+    __shared__ uint32_t words[8];
     __shared__ unsigned long long mass[BINS];
     __shared__ uint32_t count[BINS];
     const uint32_t row = blockIdx.x / a.tiles, tile = blockIdx.x - row * a.tiles, tid = threadIdx.x;
     const Rules r = rules_of(a, row);
-    if (r.greedy || (!r.k && r.p == 1.0f)) return;        // min-p alone needs no bins
+    if (r.greedy || r.pure()) return;
     fill_table(table);
-    mass[tid] = 0;
-    count[tid] = 0;
     __syncthreads();
-    const Row o = row_of(a, r, row, words, table);
+    const Row o = row_of<256>(a, r, row, words, table);
     if (o.way != BY_BINS) return;
+#pragma unroll
+    for (int i = 0; i < BINS; i += 256) mass[tid + i] = count[tid + i] = 0;
+    __syncthreads();
     const Weigh w{(double)logit_of(o.top), r.per_logit, table};
     const T* z = (const T*)a.z + row * a.z_stride;
     const uint32_t first = tile * a.tile_segs, last = first + a.tile_segs < a.segs ? first + a.tile_segs : a.segs;
-    for (int64_t at = (int64_t)first * SEG + tid * 8; at < (int64_t)last * SEG; at += THREADS * 8) {
-        float v[8];
-        load8(v, z, at, a.vocab);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6), vocab = (uint32_t)a.vocab;
+    constexpr uint32_t AHEAD = 4;
+#pragma unroll 1
+    for (uint32_t seg = first + wave; seg < last; seg += 4 * AHEAD) {
+        Eight<T> e[AHEAD];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!(v[j] > -__builtin_inff())) continue;
-            int i;
-            const uint64_t u = w.units(v[j], a.bits, i);
-            const int b = bin_of(i);
-            atomicAdd(&mass[b], (unsigned long long)u);
-            if (r.k) atomicAdd(&count[b], 1u);
+        for (uint32_t i = 0; i < AHEAD; ++i) e[i].load(z, seg + 4 * i < last ? seg + 4 * i : seg, vocab);
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            if (seg + 4 * i >= last) break;
+            float v[8];
+            e[i].values(v, seg + 4 * i, vocab);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (!(v[j] > -__builtin_inff())) continue;
+                int n;
+                const uint64_t u = w.units(v[j], a.bits, n);
+                const int b = bin_of(n);
+                atomicAdd(&mass[b], (unsigned long long)u);
+                if (r.k) atomicAdd(&count[b], 1u);
+            }
         }
     }
     __syncthreads();
     const int64_t at = ((int64_t)row * a.tiles + tile) * BINS + tid;
-    a.bin_mass[at] = mass[tid];
-    if (r.k) a.bin_count[at] = count[tid];
+#pragma unroll
+    for (int i = 0; i < BINS; i += 256) {
+        a.bin_mass[at + i] = mass[tid + i];
+        if (r.k) a.bin_count[at + i] = count[tid + i];
+    }
 }
 
 // ---- the pick ------------------------------------------------------------------------
 
 struct Lds {
     double table[PER_OCTAVE];
-    uint64_t seg_sum[MAX_SEGS];
     uint64_t hist[256];
     uint64_t sums[WAVES];
-    uint64_t pick_before;
+    uint64_t rest, pick_before, pick_unit;
     uint32_t words[2 * WAVES];
-    uint32_t pick_key, n, seg;
-    uint64_t rest;
+    uint32_t pick_key, n, seg, hits, from, floor, least;
+    uint32_t limit;
+    uint64_t seg_sum[64];
+    uint32_t top[MAX_SEGS];                       // the segments' largest keys
     uint16_t hit[MAX_SEGS];
+    uint64_t weight[CAP];
     uint32_t key[CAP], index[CAP];
 };
 
-// Sum over the block; every thread gets it.
-__device__ uint64_t block_sum(uint64_t v, Lds& s) {
-    v = wave_sum(v);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s.sums[threadIdx.x >> 6] = v;
-    __syncthreads();
-    uint64_t t = 0;
-    for (int i = 0; i < WAVES; ++i) t += s.sums[i];
-    return t;
-}
 // Sum over the threads before this one, and over all.
 template <typename V>
-__device__ V block_scan(V v, Lds& s, V& all) {
+__device__ __forceinline__ V block_scan(V v, Lds& s, V& all) {
     const V up_to = wave_scan(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 63) s.sums[threadIdx.x >> 6] = __builtin_bit_cast(uint64_t, up_to);
     __syncthreads();
-    V before = 0;
-    all = 0;
-    for (int i = 0; i < WAVES; ++i) {
-        const V t = __builtin_bit_cast(V, s.sums[i]);
-        if (i < (int)(threadIdx.x >> 6)) before += t;
-        all += t;
-    }
-    return before + up_to - v;
+    static_assert(WAVES == 16, "a row of lanes");
+    const V waves = row_scan(__builtin_bit_cast(V, s.sums[threadIdx.x & 15]));
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    all = of_lane(waves, 15);
+    return (wave ? of_lane(waves, wave - 1) : (V)0) + (up_to - v);
+}
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, Lds& s) {
+    uint64_t all;
+    block_scan(v, s, all);
+    return all;
+}
+
+__device__ __forceinline__ void wave_order() {    // this wave's LDS operations before are seen by those after
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+// By one wave: the digit up to which, from 255 down, there is `want` in s.hist (or 0);
+// `before`, what is before s.hist's, grows by what is before the digit.
+__device__ __forceinline__ uint32_t digit_reaching(Lds& s, uint64_t want, uint64_t& before) {
+    const uint32_t lane = threadIdx.x & 63;       // lane l has the four digits from 255 - 4 l down
+    uint64_t h[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += h[j] = s.hist[255 - 4 * lane - j];
+    uint64_t at = before + wave_scan(sum) - sum;
+    const uint64_t reach = __ballot(at + sum >= want);
+    const int from = reach ? (int)__builtin_ctzll(reach) : 63;
+    int digit = 0;
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+        if (digit == j && at + h[j] < want) {
+            at += h[j];
+            digit = j + 1;
+        }
+    before = of_lane(at, from);
+    return (uint32_t)(255 - 4 * from - __builtin_amdgcn_readlane(digit, from));
 }
 
 // The key from which on, in falling order, the sum reaches `want` (or the last one),
 // and the sum before it.  each(f) calls f(key, amount) for this thread's part.
 template <typename E>
-__device__ uint32_t select(Lds& s, uint64_t want, uint64_t& before, E each) {
+__device__ __forceinline__ uint32_t select(Lds& s, uint64_t want, uint64_t& before, E each) {
     uint32_t prefix = 0;
     before = 0;
+#pragma unroll 1
     for (int shift = 24; shift >= 0; shift -= 8) {
         __syncthreads();
         if (threadIdx.x < 256) s.hist[threadIdx.x] = 0;
@@ -356,16 +482,11 @@ __device__ uint32_t select(Lds& s, uint64_t want, uint64_t& before, E each) {
                 atomicAdd((unsigned long long*)&s.hist[key >> shift & 255], (unsigned long long)amount);
         });
         __syncthreads();
-        if (threadIdx.x < 64) {                   // lane l has the four digits from 255 - 4 l down
-            uint64_t h[4], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum += h[j] = s.hist[255 - 4 * threadIdx.x - j];
-            uint64_t at = before + wave_scan((unsigned long long)sum) - sum;
-            const uint64_t reach = __ballot(at + sum >= want);
-            if (threadIdx.x == (reach ? (uint32_t)__builtin_ctzll(reach) : 63u)) {
-                int j = 0;
-                while (j < 3 && at + h[j] < want) at += h[j++];
-                s.pick_key = prefix | (255 - 4 * threadIdx.x - j) << shift;
+        if (threadIdx.x < 64) {
+            uint64_t at = before;
+            const uint32_t digit = digit_reaching(s, want, at);
+            if (threadIdx.x == 0) {
+                s.pick_key = prefix | digit << shift;
                 s.pick_before = at;
             }
         }
@@ -376,34 +497,95 @@ __device__ uint32_t select(Lds& s, uint64_t want, uint64_t& before, E each) {
     return prefix;
 }
 
-template <typename T>
-__device__ void pick_slow(const SampleArgs& a, const Rules& r, int64_t row, Lds& s);
-
-template <typename T>
-__global__ __launch_bounds__(THREADS) void k_pick(SampleArgs a) {
-    __shared__ Lds s;
-    const int64_t row = blockIdx.x;
-    const T* z = (const T*)a.z + row * a.z_stride;
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const Rules r = rules_of(a, row);
-    fill_table(s.table);
-    __syncthreads();
-    if (a.segs > MAX_SEGS) {
-        pick_slow<T>(a, r, row, s);
-        return;
+// The same by one wave, which needs no barriers: a list of a few hundred takes half a
+// microsecond where the block takes five.
+template <typename E>
+__device__ __forceinline__ uint32_t wave_select(Lds& s, uint64_t want, uint64_t& before, E each) {
+    const uint32_t lane = threadIdx.x & 63;
+    // only the bits that differ: the keys of a list share most of the upper ones
+    uint32_t any = 0, all = ~0u;
+    each([&](uint32_t key, uint64_t) {
+        any |= key;
+        all &= key;
+    });
+    any = wave_or(any);
+    all = ~wave_or(~all);
+    int left = 32 - __builtin_clz((any & ~all) | 1u);            // bits still open
+    uint32_t prefix = (uint32_t)((uint64_t)all >> left << left);
+    before = 0;
+#pragma unroll 1
+    while (left > 0) {
+        const int from = left > 8 ? left - 8 : 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s.hist[lane + 64 * j] = 0;
+        wave_order();
+        each([&](uint32_t key, uint64_t amount) {
+            if ((uint64_t)(key ^ prefix) >> left == 0)
+                atomicAdd((unsigned long long*)&s.hist[key >> from & 255], (unsigned long long)amount);
+        });
+        wave_order();
+        prefix |= digit_reaching(s, want, before) << from;
+        wave_order();
+        left = from;
     }
-    const Row o = row_of(a, r, row, s.words, s.table);
+    return prefix;
+}
+
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+    for (int i = 32; i; i >>= 1) {
+        const uint64_t t = __shfl_xor((unsigned long long)v, i);
+        v = t > v ? t : v;
+    }
+    return v;
+}
+
+// By one wave: the token of a segment, the first in order up to which there is more
+// than `rest` (the last one with a weight, where roundings left none).
+template <typename T, typename D>
+__device__ __forceinline__ void pick_in_segment(const SampleArgs& a, const Rules& r, int64_t row, const T* z, uint32_t seg, uint64_t rest,
+                                double top, double mass, D drawn) {
+    const uint32_t lane = threadIdx.x & 63;
+    Eight<T> e;
+    float v[8];
+    e.load(z, seg, (uint32_t)a.vocab);
+    e.values(v, seg, (uint32_t)a.vocab);
+    uint64_t u[8], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += u[j] = drawn(v[j], e.first + j);
+    uint64_t at = wave_scan(sum) - sum;
+    const uint64_t past = __ballot(at + sum > rest), any = __ballot(sum > 0);
+    const uint32_t has = past ? (uint32_t)__builtin_ctzll(past) : 63u - (uint32_t)__builtin_clzll(any);
+    if (lane != has) return;
+    int pick = 0;
+    float value = 0.0f;
+    bool done = false;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (u[j] && !done) {
+            pick = j;
+            value = v[j];
+        }
+        at += u[j];
+        done |= at > rest;
+    }
+    a.token[row] = (int32_t)(e.first + pick);
+    if (a.logprob) a.logprob[row] = (float)(((double)value - top) * r.per_nat - log(mass));
+}
+
+// False, with nothing written, for a row that has to go the slow way.
+template <typename T>
+__device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, int64_t row, Lds& s) {
+    const T* z = (const T*)a.z + row * a.z_stride;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), vocab = (uint32_t)a.vocab;
+    const Row o = row_of<THREADS>(a, r, row, s.words, s.table);
     if (o.way == NONE) {
         if (tid == 0) {
             a.token[row] = -1;
             if (a.logprob) a.logprob[row] = -__builtin_inff();
         }
-        return;
+        return true;
     }
-    if (o.way == SLOW) {
-        pick_slow<T>(a, r, row, s);
-        return;
-    }
+    if (o.way == SLOW) return false;
     const float top = logit_of(o.top);
     const Weigh w{(double)top, r.per_logit, s.table};
 
@@ -414,40 +596,25 @@ __global__ __launch_bounds__(THREADS) void k_pick(SampleArgs a) {
         if (o.key == o.top) atomicMin(&s.seg, tid);
         __syncthreads();
         if (wave == 0) {
+            Eight<T> e;
             float v[8];
-            load8(v, z, (int64_t)s.seg * SEG + lane * 8, a.vocab);
+            e.load(z, s.seg, vocab);
+            e.values(v, s.seg, vocab);
             uint32_t at = ~0u;
 #pragma unroll
             for (int j = 7; j >= 0; --j)
-                if (key_of(v[j]) == o.top) at = lane * 8 + j;
+                if (v[j] == logit_of(o.top)) at = e.first + j;
             const uint64_t has = __ballot(at != ~0u);
             if (lane == (uint32_t)__builtin_ctzll(has)) {
-                a.token[row] = (int32_t)(s.seg * SEG + at);
+                a.token[row] = (int32_t)at;
                 if (a.logprob) a.logprob[row] = 0.0f;
             }
         }
-        return;
+        return true;
     }
 
     float uf = a.u[row];
     if (!(uf > 0.0f)) uf = 0.0f;
-
-    // thresholds: kept are, of the keys from `from` on, those above `floor` and those
-    // equal to it up to index `limit`, and of these the ones that pass min-p
-    uint32_t floor = 0, from = 1;
-    int64_t limit = a.vocab;
-    auto kept = [&](float v, int64_t i) {
-        const uint32_t key = key_of(v);
-        return key >= from && (key > floor || (key == floor && i <= limit));
-    };
-    // weight of a logit in the draw
-    auto drawn = [&](float v, int64_t i) -> uint64_t {
-        if (!kept(v, i)) return 0;
-        if (r.least > 0.0f && !(w.real(v) >= (double)r.least)) return 0;
-        return w.units(v, a.bits);
-    };
-    // the mass that is drawn from, in units of the largest weight
-    double mass = 0.0;
 
     if (o.way == PURE) {
         const double factor = o.key ? w.real(logit_of(o.key)) : 0.0;
@@ -475,276 +642,378 @@ __global__ __launch_bounds__(THREADS) void k_pick(SampleArgs a) {
             s.rest = rest > 0.0 ? (uint64_t)fmin(rest, 0x1p61) : 0;
             s.pick_key = o.key;
         }
-        mass = all;
-    } else {
-        // ---- candidates ----
-        const bool by_bins = o.way == BY_BINS;
-        uint64_t bin_mass = 0;                    // of bin `tid`
-        uint32_t bin_count = 0;
-        if (by_bins && (r.k || r.p < 1.0f)) {
-            for (uint32_t t = 0; t < a.tiles; ++t) {
-                bin_mass += a.bin_mass[(row * a.tiles + t) * BINS + tid];
-                if (r.k) bin_count += a.bin_count[(row * a.tiles + t) * BINS + tid];
+        __syncthreads();
+        if (wave == 0) {
+            const Weigh own{(double)logit_of(s.pick_key), w.c, s.table};
+            pick_in_segment(a, r, row, z, seg, s.rest, (double)top, all,
+                            [&](float v, uint32_t) { return v > -__builtin_inff() ? own.units(v, 51) : 0; });
+        }
+        return true;
+    }
+
+    // keys from `least` on pass min-p; a bin's keys are those from_bin(b) .. from_bin(b - 1)
+    auto first_key = [&](auto pass) {             // by a wave: the smallest key with pass, which larger ones have too
+        uint32_t lo = KEY_FIRST - 1, hi = o.top;
+#pragma unroll 1
+        while (hi - lo > 1) {
+            const uint32_t step = (hi - lo + 63) / 64, at = hi - lo > step * (lane + 1) ? lo + step * (lane + 1) : hi;
+            const int first = __builtin_ctzll(__ballot(at == hi || pass(logit_of(at))));
+            hi = (uint32_t)__builtin_amdgcn_readlane((int)at, first);
+            lo = first ? (uint32_t)__builtin_amdgcn_readlane((int)at, first - 1) : lo;
+        }
+        return hi;
+    };
+    s.top[tid] = o.key;
+    if (wave == 0) {
+        const uint32_t least = r.least > 0.0f ? first_key([&](float v) { return w.real(v) >= (double)r.least; }) : KEY_FIRST;
+        if (lane == 0) s.least = least;
+    }
+
+    // The segments with keys from lo on, in order; every thread calls it.
+    auto hit_segments = [&](uint32_t lo) {
+        if (wave == 0) {
+            uint32_t hits = 0;
+#pragma unroll 1
+            for (uint32_t from = 0; from < a.segs; from += 64) {
+                const bool hit = from + lane < a.segs && s.top[from + lane] >= lo;
+                const uint64_t all = __ballot(hit);
+                if (hit)
+                    s.hit[hits + __builtin_amdgcn_mbcnt_hi((uint32_t)(all >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)all, 0))] = (uint16_t)(from + lane);
+                hits += (uint32_t)__popcll(all);
+            }
+            if (lane == 0) {
+                s.hits = hits;
+                s.n = 0;
             }
         }
-        uint32_t held_bin = ~0u;                  // the bin whose logits are in the list
-
-        // the candidates: logits that pass(value, key) in the segments with use(largest key)
-        auto gather = [&](auto use, auto pass) {
-            if (tid == 0) s.n = 0;
-            const bool hit = o.key && use(o.key);
-            uint64_t all;
-            const uint64_t at = block_scan((uint64_t)hit, s, all);
-            if (hit) s.hit[at] = (uint16_t)tid;
-            __syncthreads();
-            constexpr int AHEAD = 4;
-            for (uint32_t h = wave; h < all; h += WAVES * AHEAD) {
-                float v[AHEAD][8];
+        __syncthreads();
+    };
+    // Candidates: the keys from lo to below hi into the list, with their weights; their
+    // order there does not matter.  False if they are too many.
+    auto gather = [&](uint32_t lo, uint32_t hi) {
+        hit_segments(lo);
+        const uint32_t hits = s.hits;
+        const float least = logit_of(lo), past = logit_of(hi);
+        constexpr uint32_t AHEAD = 4;
+#pragma unroll 1
+        for (uint32_t h = wave; h < hits; h += WAVES * AHEAD) {
+            Eight<T> e[AHEAD];
+            uint32_t seg[AHEAD];
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    const uint32_t e = h + i * WAVES < all ? h + i * WAVES : h;
-                    load8(v[i], z, (int64_t)s.hit[e] * SEG + lane * 8, a.vocab);
+            for (uint32_t i = 0; i < AHEAD; ++i) {
+                seg[i] = __builtin_amdgcn_readfirstlane(s.hit[h + i * WAVES < hits ? h + i * WAVES : h]);
+                e[i].load(z, seg[i], vocab);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < AHEAD; ++i) {
+                if (h + i * WAVES >= hits) break;
+                float v[8];
+                e[i].values(v, seg[i], vocab);
+                uint64_t in[8];                   // lanes with a candidate
+                uint32_t n = 0;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) {
+                    in[j] = __ballot(v[j] >= least && v[j] < past);
+                    n += (uint32_t)__popcll(in[j]);
                 }
+                if (!n) continue;
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&s.n, n);
+                at = __builtin_amdgcn_readfirstlane(at);
 #pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    if (h + i * WAVES >= all) break;
-                    const uint32_t base = s.hit[h + i * WAVES] * SEG + lane * 8;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t key = key_of(v[i][j]);
-                        if (key && pass(v[i][j], key)) {
-                            const uint32_t e = atomicAdd(&s.n, 1u);
-                            if (e < CAP) {
-                                s.key[e] = key;
-                                s.index[e] = base + j;
-                            }
+                for (uint32_t j = 0; j < 8; ++j) {
+                    if (in[j] >> lane & 1) {
+                        const uint32_t to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[j], 0));
+                        if (to < CAP) {
+                            s.key[to] = key_of(v[j]);
+                            s.index[to] = e[i].first + j;
                         }
                     }
+                    at += (uint32_t)__popcll(in[j]);
                 }
             }
-            __syncthreads();
-            return s.n <= CAP;
-        };
-        auto listed = [&](auto f) {
-            for (uint32_t e = tid; e < s.n; e += THREADS) f(s.key[e], s.index[e]);
-        };
+        }
+        __syncthreads();
+        const uint32_t n = s.n;
+        if (n > CAP) return false;
+#pragma unroll 1
+        for (uint32_t e = tid; e < n; e += THREADS) s.weight[e] = w.units(logit_of(s.key[e]), a.bits);
+        __syncthreads();
+        return true;
+    };
 
-        // the first bin up to which there are `want`, and what lies before it
-        auto bin_reaching = [&](uint64_t amount, uint64_t want, uint64_t& before) {
+    // ---- wave 0's work on the list ----
+    auto listed = [&](auto f) {                   // four entries' loads at a time
+        const uint32_t n = s.n;
+#pragma unroll 1
+        for (uint32_t e = lane; e < n; e += 256) {
+            uint32_t key[4], index[4];
+            uint64_t u[4];
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i) {
+                const uint32_t at = e + 64 * i < n ? e + 64 * i : e;
+                key[i] = s.key[at];
+                index[i] = s.index[at];
+                u[i] = s.weight[at];
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 4; ++i)
+                if (e + 64 * i < n) f(key[i], index[i], u[i]);
+        }
+    };
+    // the threshold that `count` keys are at or above
+    auto cut_by_count = [&](uint64_t count, uint32_t& floor, uint64_t& ties, uint64_t above = 0) {
+        uint64_t before;
+        floor = wave_select(s, count - above, before, [&](auto add) { listed([&](uint32_t key, uint32_t, uint64_t) { add(key, 1); }); });
+        ties = count - above - before;
+    };
+    // the mass above `floor`, how many keys are equal to it, and the weight of each
+    auto mass_of = [&](uint32_t floor, uint64_t& equal, uint64_t& unit) {
+        uint64_t sum = 0;
+        uint32_t n = 0;
+        unit = 0;
+        listed([&](uint32_t key, uint32_t, uint64_t u) {
+            sum += key > floor ? u : 0;
+            unit = key == floor ? u : unit;
+            n += key == floor;
+        });
+        unit = wave_max64(unit);
+        equal = of_lane((uint64_t)wave_scan32(n), 63);
+        return wave_sum(sum);
+    };
+    // of the listed keys above `floor`, and `ties` of those equal to it (of weight
+    // `unit`), those before which there is less than `want` of mass
+    auto cut_by_mass = [&](uint64_t want, uint32_t& floor, uint64_t& ties, uint64_t unit) {
+        uint64_t before, equal;
+        const uint32_t key = wave_select(s, want, before, [&](auto add) {
+            listed([&](uint32_t key, uint32_t, uint64_t u) { if (key > floor) add(key, u); });
+            if (unit && lane == 0) add(floor, ties * unit);
+        });
+        mass_of(key, equal, unit);
+        const uint64_t n = unit ? (want - before + unit - 1) / unit : ~0ull;
+        ties = key == floor && ties < n ? ties : n;
+        floor = key;
+    };
+    auto part_of = [&](uint64_t all) {            // top-p's
+        const uint64_t want = (uint64_t)ceil(fmax(r.p, 0.0f) * (double)all);
+        return want < 1 ? (uint64_t)1 : want;
+    };
+    // the index of the last of the ties (all keys equal to the threshold are listed)
+    auto last_tie = [&](uint32_t floor, uint64_t ties, uint64_t equal) -> uint32_t {
+        uint64_t before;
+        if (ties >= equal) return vocab;
+        return 0xffffffu - wave_select(s, ties, before, [&](auto add) {
+            listed([&](uint32_t key, uint32_t i, uint64_t) { if (key == floor) add(0xffffffu - i, 1); });
+        });
+    };
+
+    if (o.way == LIST) {
+        const bool by_least = !r.k && r.least > 0.0f;
+        double all = 0.0;
+        if (by_least && r.p < 1.0f)               // top-p is a part of all logits, not of the list
+            block_scan(o.key ? (double)a.seg_mass[row * a.segs + tid] * 0x1p-51 * w.real(logit_of(o.key)) : 0.0, s, all);
+        __syncthreads();
+        if (r.k && wave == 0) {
+            // the k-th largest; where fewer segments than k have a logit all of their logits
+            uint64_t before;
+            uint32_t some = 0;
+            auto tops = [&](auto f) {
+#pragma unroll 1
+                for (uint32_t e = lane; e < a.segs; e += 256) {
+                    uint32_t key[4];
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i) key[i] = s.top[e + 64 * i < a.segs ? e + 64 * i : e];
+#pragma unroll
+                    for (uint32_t i = 0; i < 4; ++i)
+                        if (e + 64 * i < a.segs && key[i]) f(key[i]);
+                }
+            };
+            tops([&](uint32_t) { ++some; });
+            uint32_t from = KEY_FIRST;
+            if (of_lane((uint64_t)wave_scan32(some), 63) >= (uint64_t)r.k)
+                from = wave_select(s, (uint64_t)r.k, before, [&](auto add) { tops([&](uint32_t key) { add(key, 1); }); });
+            if (lane == 0) s.from = from;
+        }
+        __syncthreads();
+        if (!gather(r.k ? s.from : s.least, KEY_INF)) return false;
+        if (wave != 0) return true;
+        uint32_t floor = 0;
+        uint64_t ties = ~0ull, before, unit, equal;
+        if (r.k && (uint64_t)r.k < s.n) cut_by_count((uint64_t)r.k, floor, ties);
+        if (r.p < 1.0f) {
+            uint64_t have = mass_of(floor, equal, unit);
+            have += unit ? ties * unit : 0;
+            const uint64_t want = part_of(by_least ? (uint64_t)rint(__builtin_ldexp(all, a.bits)) : have);
+            if (have >= want) cut_by_mass(want, floor, ties, unit);       // else min-p cuts above top-p
+        }
+        uint32_t limit = vocab;
+        if (floor) {
+            mass_of(floor, equal, unit);
+            limit = last_tie(floor, ties, equal);
+        }
+        // the draw: by index, the first up to which there is more than the target
+        const uint32_t least = s.least;
+        auto drawn = [&](uint32_t key, uint32_t i, uint64_t u) { return key >= least && (key > floor || (key == floor && i <= limit)) ? u : 0; };
+        uint64_t total = 0;
+        listed([&](uint32_t key, uint32_t i, uint64_t u) { total += drawn(key, i, u); });
+        total = wave_sum(total);
+        uint64_t target = (uint64_t)((double)uf * (double)total);
+        if (target >= total) target = total - 1;
+        const uint32_t token = 0xffffffu - wave_select(s, target + 1, before, [&](auto add) {
+            listed([&](uint32_t key, uint32_t i, uint64_t u) {
+                const uint64_t d = drawn(key, i, u);
+                if (d) add(0xffffffu - i, d);
+            });
+        });
+        if (lane == 0) {
+            a.token[row] = (int32_t)token;
+            if (a.logprob)
+                a.logprob[row] = (float)(((double)to_f32(z[token]) - (double)top) * r.per_nat - log(__builtin_ldexp((double)total, -a.bits)));
+        }
+        return true;
+    }
+
+    // ---- by bins: thread b has bin b ----
+    uint64_t bin_mass = 0, bin_count = 0;
+#pragma unroll 4
+    for (uint32_t t = 0; t < a.tiles; ++t) {
+        bin_mass += a.bin_mass[(row * a.tiles + t) * BINS + tid];
+        if (r.k) bin_count += a.bin_count[(row * a.tiles + t) * BINS + tid];
+    }
+    uint32_t held = ~0u;                          // the bin in the list
+    if (tid == 0) {
+        s.floor = 0;
+        s.limit = vocab;
+        s.pick_before = ~0ull;                    // the ties
+        s.n = 0;
+    }
+    // top-k by the counts, then top-p by the masses, then min-p
+#pragma unroll 1
+    for (int step = 0; step < 3; ++step) {
+        if (step == 0 ? r.k == 0 : step == 1 ? r.p == 1.0f : r.least == 0.0f) continue;
+        uint64_t want = 0, before = 0;
+        uint32_t bin;
+        if (step < 2) {
+            const uint64_t amount = step ? bin_mass : bin_count;
             uint64_t all;
             const uint64_t at = block_scan(amount, s, all);
-            __syncthreads();
-            if (tid == 0) s.seg = BINS - 1;
-            __syncthreads();
+            if (!step && (uint64_t)r.k >= all) continue;
+            want = step ? part_of(all) : (uint64_t)r.k;
             if (at < want && at + amount >= want) {
                 s.seg = tid;
                 s.rest = at;
             }
             __syncthreads();
+            bin = s.seg;
             before = s.rest;
-            return s.seg;
-        };
-
-        uint64_t ties = ~0ull;                    // of those equal to the threshold
-        uint64_t z_mass = 0;                      // what top-p is a part of
-        bool whole = false;                       // every logit above the threshold is in the list
-        if (!by_bins) {
-            if (r.k && r.k <= (int64_t)a.segs) {
-                uint64_t before;
-                from = select(s, (uint64_t)r.k, before, [&](auto add) { if (o.key) add(o.key, 1); });
-                // fewer segments than k have a logit: all of their logits
-                uint64_t all;
-                block_scan((uint64_t)(o.key != 0), s, all);
-                if (all < (uint64_t)r.k) from = 1;
-            }
-            const bool by_least = !r.k && r.least > 0.0f;
-            const bool fits = gather([&](uint32_t key) { return key >= from && (!by_least || w.real(logit_of(key)) >= (double)r.least); },
-                                     [&](float v, uint32_t key) { return key >= from && (!by_least || w.real(v) >= (double)r.least); });
-            if (!fits) {
-                pick_slow<T>(a, r, row, s);
-                return;
-            }
-            whole = true;
-            if (r.k && (uint64_t)r.k < s.n) {
-                uint64_t before;
-                floor = select(s, (uint64_t)r.k, before, [&](auto add) { listed([&](uint32_t key, uint32_t) { add(key, 1); }); });
-                ties = (uint64_t)r.k - before;
-            }
-            if (r.p < 1.0f) {
-                if (by_least) {                   // of all logits, not of the list
-                    double all;
-                    block_scan(o.key ? (double)a.seg_mass[row * a.segs + tid] * 0x1p-51 * w.real(logit_of(o.key)) : 0.0, s, all);
-                    z_mass = (uint64_t)rint(__builtin_ldexp(all, a.bits));
-                } else {
-                    uint64_t sum = 0;
-                    listed([&](uint32_t key, uint32_t) { if (key > floor) sum += w.units(logit_of(key), a.bits); });
-                    z_mass = block_sum(sum, s) + (floor ? ties * w.units(logit_of(floor), a.bits) : 0);
-                }
-            }
         } else {
-            // the logits of one bin; false if they are too many
-            auto hold = [&](uint32_t bin) {
-                held_bin = bin;
-                return gather([&](uint32_t key) { return bin_of(w, logit_of(key)) <= (int)bin; },
-                              [&](float v, uint32_t) { return bin_of(w, v) == (int)bin; });
-            };
-            uint64_t above = 0;                   // mass above the held bin
-            if (r.k) {
-                uint64_t all, before;
-                block_scan((uint64_t)bin_count, s, all);
-                if ((uint64_t)r.k < all) {
-                    const uint32_t bin = bin_reaching(bin_count, (uint64_t)r.k, before);
-                    if (!hold(bin)) {
-                        pick_slow<T>(a, r, row, s);
-                        return;
-                    }
-                    uint64_t in_bin;
-                    floor = select(s, (uint64_t)r.k - before, in_bin, [&](auto add) { listed([&](uint32_t key, uint32_t) { add(key, 1); }); });
-                    ties = (uint64_t)r.k - before - in_bin;
-                    // the bins' masses without what top-k drops
-                    uint64_t sum = 0;
-                    listed([&](uint32_t key, uint32_t) { if (key > floor) sum += w.units(logit_of(key), a.bits); });
-                    sum = block_sum(sum, s) + ties * w.units(logit_of(floor), a.bits);
-                    bin_mass = tid < bin ? bin_mass : (tid == bin ? sum : 0);
-                }
-            }
-            if (r.p < 1.0f) {
-                block_scan(bin_mass, s, z_mass);
-                uint64_t want = (uint64_t)ceil(fmax(r.p, 0.0f) * (double)z_mass);
-                if (want < 1) want = 1;
-                const uint32_t bin = bin_reaching(bin_mass, want, above);
-                if (bin != held_bin && !hold(bin)) {
-                    pick_slow<T>(a, r, row, s);
-                    return;
-                }
-                // (top-k's threshold and ties, if in this bin, count as in the list's case)
-                uint64_t in_bin;
-                const uint32_t k_floor = floor;
-                const uint64_t k_ties = ties;
-                const uint64_t floor_units = k_floor ? w.units(logit_of(k_floor), a.bits) : 0;
-                const bool floor_here = k_floor && bin_of(w, logit_of(k_floor)) == (int)bin;
-                const uint32_t key = select(s, want - above, in_bin, [&](auto add) {
-                    listed([&](uint32_t key, uint32_t) { if (key > k_floor) add(key, w.units(logit_of(key), a.bits)); });
-                    if (floor_here && tid == 0) add(k_floor, k_ties * floor_units);
-                });
-                const uint64_t unit = w.units(logit_of(key), a.bits);
-                const uint64_t n = unit ? (want - above - in_bin + unit - 1) / unit : ~0ull;
-                if (key == floor) ties = n < ties ? n : ties;
-                else {
-                    floor = key;
-                    ties = n;
-                }
-            }
+            __syncthreads();
+            if (s.least <= s.floor) continue;     // the others cut above it
+            bin = (uint32_t)bin_of(w, logit_of(s.least));
         }
-        if (!by_bins && r.p < 1.0f) {
-            uint64_t want = (uint64_t)ceil(fmax(r.p, 0.0f) * (double)z_mass), sum = 0;
-            if (want < 1) want = 1;
-            listed([&](uint32_t key, uint32_t) { if (key > floor) sum += w.units(logit_of(key), a.bits); });
-            const uint64_t floor_units = floor ? w.units(logit_of(floor), a.bits) : 0;
-            sum = block_sum(sum, s) + (floor ? ties * floor_units : 0);
-            if (sum >= want) {                    // else min-p cuts above top-p
-                uint64_t before;
-                const uint32_t key = select(s, want, before, [&](auto add) {
-                    listed([&](uint32_t key, uint32_t) { if (key > floor) add(key, w.units(logit_of(key), a.bits)); });
-                    if (floor && tid == 0) add(floor, ties * floor_units);
-                });
-                const uint64_t unit = w.units(logit_of(key), a.bits);
-                const uint64_t n = unit ? (want - before + unit - 1) / unit : ~0ull;
-                if (key == floor) ties = n < ties ? n : ties;
-                else {
-                    floor = key;
-                    ties = n;
+        if (bin != held) {
+            if (wave == 0) {
+                const uint32_t lo = first_key([&](float v) { return bin_of(w, v) <= (int)bin; });
+                const uint32_t hi = bin ? first_key([&](float v) { return bin_of(w, v) < (int)bin; }) : KEY_INF;
+                if (lane == 0) {
+                    s.from = lo;
+                    s.pick_key = hi;
                 }
             }
+            __syncthreads();
+            if (!gather(s.from, s.pick_key)) return false;
         }
-        // the index of the last of the ties (all keys equal to the threshold are listed)
-        if (floor) {
-            uint64_t n = 0;
-            listed([&](uint32_t key, uint32_t) { n += key == floor; });
-            n = block_sum(n, s);
-            if (ties < n) {
-                uint64_t before;
-                limit = ~select(s, ties, before, [&](auto add) { listed([&](uint32_t key, uint32_t i) { if (key == floor) add(~i, 1); }); });
+        if (wave == 0) {
+            uint32_t floor = bin == held ? s.floor : 0;
+            uint64_t ties = bin == held ? s.pick_before : ~0ull, unit = bin == held ? s.pick_unit : 0, equal;
+            if (step == 0) cut_by_count(want, floor, ties, before);
+            else if (step == 1) cut_by_mass(want - before, floor, ties, unit);
+            else {
+                floor = s.least;                  // all that are equal to it
+                ties = ~0ull;
             }
-        }
-        // ---- the kept mass by segments ----
-        __syncthreads();
-        s.seg_sum[tid] = 0;
-        __syncthreads();
-        if (whole) {
-            listed([&](uint32_t key, uint32_t i) {
-                const uint64_t d = drawn(logit_of(key), i);
-                if (d) atomicAdd((unsigned long long*)&s.seg_sum[i / SEG], (unsigned long long)d);
-            });
-        } else {
-            constexpr int AHEAD = 4;
-            for (uint32_t h = wave; h < a.segs; h += WAVES * AHEAD) {
-                float v[AHEAD][8];
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i)
-                    if (h + i * WAVES < a.segs) load8(v[i], z, (int64_t)(h + i * WAVES) * SEG + lane * 8, a.vocab);
-#pragma unroll
-                for (int i = 0; i < AHEAD; ++i) {
-                    if (h + i * WAVES >= a.segs) break;
-                    uint64_t sum = 0;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) sum += drawn(v[i][j], (int64_t)(h + i * WAVES) * SEG + lane * 8 + j);
-                    sum = wave_sum(sum);
-                    if (lane == 0) s.seg_sum[h + i * WAVES] = sum;
-                }
+            const uint64_t mass = mass_of(floor, equal, unit);
+            const uint32_t limit = last_tie(floor, ties, equal);
+            ties = ties < equal ? ties : equal;
+            if (lane == 0) {
+                s.floor = floor;
+                s.limit = limit;
+                s.pick_before = ties;
+                s.pick_unit = unit;
+                s.rest = mass + ties * unit;
             }
         }
         __syncthreads();
-        const uint64_t mine = s.seg_sum[tid];
-        uint64_t all;
-        const uint64_t before = block_scan(mine, s, all);
-        uint64_t target = (uint64_t)((double)uf * (double)all);
-        if (target >= all) target = all - 1;
-        if (mine && before <= target && target < before + mine) {
-            s.seg = tid;
-            s.rest = target - before;
-        }
-        mass = __builtin_ldexp((double)all, -a.bits);
+        held = bin;
+        // the bins' masses without what is dropped
+        bin_mass = tid < bin ? bin_mass : (tid == bin ? s.rest : 0);
     }
     __syncthreads();
-
-    // ---- the token of the segment, in order: the first up to which there is more than the rest ----
-    if (wave == 0) {
-        const uint32_t seg = s.seg;
-        const int64_t base = (int64_t)seg * SEG + lane * 8;
-        float v[8];
-        load8(v, z, base, a.vocab);
-        const Weigh own{o.way == PURE ? (double)logit_of(s.pick_key) : w.top, w.c, s.table};
-        uint64_t u[8], sum = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (o.way == PURE) u[j] = v[j] > -__builtin_inff() ? own.units(v[j], 51) : 0;
-            else u[j] = drawn(v[j], base + j);
-            sum += u[j];
+    const uint32_t floor = s.floor;
+    const uint32_t limit = s.limit;
+    const float above = floor ? logit_of(floor) : -__builtin_inff();
+    auto drawn = [&](float v, uint32_t i) -> uint64_t {
+        return v > above || (floor && v == above && i <= limit) ? w.units(v, a.bits) : 0;
+    };
+    // ---- the kept mass by tiles, a wave each: of the bins above the held one as they are,
+    // of that one by the list; then by the segments of the tile that the draw falls into,
+    // and in the segment ----
+    static_assert(WAVES == 16, "a wave a tile");
+    if (wave < a.tiles) {
+        uint64_t sum = 0;
+#pragma unroll 4
+        for (uint32_t b = lane; b < BINS; b += 64) sum += b < held ? a.bin_mass[(row * a.tiles + wave) * BINS + b] : 0;
+        const uint32_t n = held == ~0u ? 0 : s.n, first = wave * a.tile_segs * SEG, past = first + a.tile_segs * SEG;
+#pragma unroll 1
+        for (uint32_t e = lane; e < n; e += 64) {
+            const uint32_t key = s.key[e], i = s.index[e];
+            if (i >= first && i < past && (key > floor || (key == floor && i <= limit))) sum += s.weight[e];
         }
-        uint64_t at = wave_scan((unsigned long long)sum) - sum;
-        const uint64_t past = __ballot(at + sum > s.rest), any = __ballot(sum > 0);
-        const uint32_t has = past ? (uint32_t)__builtin_ctzll(past) : 63u - (uint32_t)__builtin_clzll(any);
-        if (lane == has) {
-            int pick = 0;
-            for (int j = 0; j < 8; ++j) {
-                if (u[j]) pick = j;
-                at += u[j];
-                if (u[j] && at > s.rest) break;
-            }
-            a.token[row] = (int32_t)(base + pick);
-            if (a.logprob) a.logprob[row] = (float)(((double)v[pick] - (double)top) * r.per_nat - log(mass));
+        sum = wave_sum(sum);
+        if (lane == 0) s.seg_sum[wave] = sum;
+    }
+    __syncthreads();
+    const uint64_t tile_mass = lane < a.tiles ? s.seg_sum[lane] : 0, tile_upto = wave_scan(tile_mass), all = of_lane(tile_upto, 63);
+    uint64_t target = (uint64_t)((double)uf * (double)all);
+    if (target >= all) target = all - 1;
+    const uint32_t tile = (uint32_t)__builtin_ctzll(__ballot(tile_upto > target));
+    target -= of_lane(tile_upto - tile_mass, tile);
+    __syncthreads();
+    const uint32_t first = tile * a.tile_segs, segs = a.segs - first < a.tile_segs ? a.segs - first : a.tile_segs;      // at most 64
+    constexpr uint32_t AHEAD = 4;
+    {
+        Eight<T> e[AHEAD];
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) e[i].load(z, first + (wave + i * WAVES < segs ? wave + i * WAVES : 0), vocab);
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            if (wave + i * WAVES >= segs) break;
+            float v[8];
+            e[i].values(v, first + wave + i * WAVES, vocab);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += drawn(v[j], e[i].first + j);
+            sum = wave_sum(sum);
+            if (lane == 0) s.seg_sum[wave + i * WAVES] = sum;
         }
     }
+    __syncthreads();
+    if (wave == 0) {
+        const uint64_t mine = lane < segs ? s.seg_sum[lane] : 0, upto = wave_scan(mine);
+        const uint32_t seg = (uint32_t)__builtin_ctzll(__ballot(upto > target));
+        pick_in_segment(a, r, row, z, first + seg, target - of_lane(upto - mine, seg), (double)top, __builtin_ldexp((double)all, -a.bits), drawn);
+    }
+    return true;
 }
 
 // Selections over the whole row: any number of equal logits, infinite ones, any vocabulary.
 template <typename T>
-__device__ __attribute__((noinline)) void pick_slow(const SampleArgs& a, const Rules& r, int64_t row, Lds& s) {
+__device__ __forceinline__ void pick_slow(const SampleArgs& a, const Rules& r, int64_t row, Lds& s) {
     const int64_t vocab = a.vocab;
     const T* z = (const T*)a.z + row * a.z_stride;
     const uint32_t tid = threadIdx.x;
     auto each = [&](auto f) {
+#pragma unroll 1
         for (int64_t i = tid; i < vocab; i += THREADS) {
             const uint32_t key = key_of(to_f32(z[i]));
             if (key) f(key, i);
@@ -760,7 +1029,7 @@ __device__ __attribute__((noinline)) void pick_slow(const SampleArgs& a, const R
     __syncthreads();
     if ((tid & 63) == 0) s.words[tid >> 6] = top;
     __syncthreads();
-    for (int i = 0; i < WAVES; ++i) top = larger(top, s.words[i]);
+    top = wave_max(s.words[tid & (WAVES - 1)]);
     valid = block_sum(valid, s);
     if (top == 0) {
         if (tid == 0) {
@@ -818,6 +1087,7 @@ __device__ __attribute__((noinline)) void pick_slow(const SampleArgs& a, const R
     uint64_t target = (uint64_t)((double)uf * (double)total);
     if (target >= total) target = total - 1;
     uint64_t done = 0;
+#pragma unroll 1
     for (int64_t from = 0; from < vocab; from += THREADS) {
         const int64_t i = from + tid;
         const uint32_t key = i < vocab ? key_of(to_f32(z[i])) : 0u;
@@ -834,6 +1104,16 @@ __device__ __attribute__((noinline)) void pick_slow(const SampleArgs& a, const R
     }
 }
 
+template <typename T>
+__global__ __launch_bounds__(THREADS) void k_pick(SampleArgs a) {
+    __shared__ Lds s;
+    const int64_t row = blockIdx.x;
+    const Rules r = rules_of(a, row);
+    fill_table(s.table);
+    __syncthreads();
+    if (a.segs > MAX_SEGS || !pick_fast<T>(a, r, row, s)) pick_slow<T>(a, r, row, s);
+}
+
 // How a call's work is laid out.
 struct Plan {
     int64_t segs, tiles, tile_segs;
@@ -843,8 +1123,7 @@ Plan plan_for(int64_t rows, int64_t vocab) {
     Plan p{};
     p.segs = (vocab + SEG - 1) / SEG;
     if (p.segs > MAX_SEGS || p.segs == 0) return p;
-    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(16, 1024 / rows));
-    p.tile_segs = (p.segs + want - 1) / want;
+    p.tile_segs = (p.segs + 15) / 16;             // 16 tiles of up to 64 segments
     p.tiles = (p.segs + p.tile_segs - 1) / p.tile_segs;
     auto round = [](int64_t n) { return (n + 15) / 16 * 16; };
     p.top_bytes = round(rows * p.segs * 4);
@@ -861,12 +1140,12 @@ int launch_sample(const SampleArgs& a, int64_t rows, hipStream_t stream) {
         const int64_t waves = rows * a.segs;
         const int per = waves >= 16384 ? 4 : 1;
         const int64_t blocks = ((int64_t)a.segs + 4 * per - 1) / (4 * per);
-        if (rows * blocks > most_blocks(256) || rows * a.tiles > most_blocks(THREADS)) return MOEQ8_EUNSUPPORTED;
+        if (rows * blocks > most_blocks(256) || rows * a.tiles > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
         const dim3 grid((uint32_t)(rows * blocks));
         if (per == 4) hipLaunchKernelGGL((k_scan<T, 4>), grid, dim3(256), 0, stream, a, (uint32_t)blocks);
         else hipLaunchKernelGGL((k_scan<T, 1>), grid, dim3(256), 0, stream, a, (uint32_t)blocks);
         if (a.top_k || a.top_p || a.min_p)
-            hipLaunchKernelGGL((k_bins<T>), dim3((uint32_t)(rows * a.tiles)), dim3(THREADS), 0, stream, a);
+            hipLaunchKernelGGL((k_bins<T>), dim3((uint32_t)(rows * a.tiles)), dim3(256), 0, stream, a);
     }
     hipLaunchKernelGGL((k_pick<T>), dim3((uint32_t)rows), dim3(THREADS), 0, stream, a);
     return check_launch();
