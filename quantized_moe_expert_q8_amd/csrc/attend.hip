@@ -58,7 +58,7 @@ struct AttendArgs {
     float* sums;                                  // [seqs][heads][rows][spans][d], then {m, l} [...][spans]
     float2* stats;
     uint32_t cols, group, rows, limit;            // rows: cols * group; limit: what visible is taken within
-    uint32_t span, spans, seqs;
+    uint32_t span, spans, seqs, parts;            // parts: of the rows, 16 * NT each
     float factor;                                 // scale * log2(e)
 };
 
@@ -89,6 +89,14 @@ __device__ __forceinline__ float quad_sum(float v) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
+// Largest of lanes 0 to 7, in every lane.
+__device__ __forceinline__ uint32_t eight_max(uint32_t v) {
+    v = larger(v, moved<XOR1>(v));
+    v = larger(v, moved<XOR2>(v));
+    v = larger(v, moved<HALF_MIRROR>(v));
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
 // The four codes of a dword, their sign bits flipped, as fp16 numbers: two a dword.
 __device__ __forceinline__ half2v halves(uint32_t bytes, uint32_t select) {
     const uint32_t u = __builtin_amdgcn_perm(0x64646464u, bytes, select);      // 1024 + 128 + code
@@ -115,8 +123,12 @@ constexpr int lds_bytes(int waves) {
     return queries > join ? queries : join;
 }
 
+// Waves a SIMD that the registers have to leave room for: what keeps loads in flight.
+template <int NC, int NT>
+constexpr int min_waves() { return NC * NT <= 1 ? 4 : NC * NT <= 2 ? 3 : NC * NT <= 4 ? 2 : 1; }
+
 template <typename T, int NC, int NT, int W>
-__global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(AttendArgs a) {
     constexpr int DV = 4 * NC;                    // values of a V row a lane loads
     constexpr int QP = Parts<T>::Q, PP = Parts<T>::P;
     __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes<T, NC, NT>(W)];
@@ -124,19 +136,26 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
 
-    // block: the rows' part slowest, then sequence, key head and span
+    // block: key heads fastest, then the rows' part, the sequence and, slowest, the span:
+    // blocks go to the 8 XCDs in turn, and with the spans fastest the XCDs that got a
+    // short sequence's last spans had nothing to do
     uint32_t id = blockIdx.x;
-    const uint32_t split = id % a.spans;
-    id /= a.spans;
     const uint32_t head = id % a.c.n_heads;
     id /= a.c.n_heads;
-    const uint32_t seq = id % a.seqs, row0 = id / a.seqs * (16 * NT);
-    const uint32_t length = seen_by_any(a, seq);
+    const uint32_t row0 = id % a.parts * (16 * NT);
+    id /= a.parts;
+    const uint32_t seq = id % a.seqs, split = id / a.seqs;
     const uint32_t begin = split * a.span;
-    if (begin >= length && a.spans > 1) return;   // k_join reads spans with a position only
-    const uint32_t end = length - begin < a.span ? length : begin + a.span;      // 0 for a sequence of no position
 
-    // ---- queries: fp16 operands and their rows' factors, in LDS -----------------
+    // what depends on nothing is loaded first: what the columns see (a lane each), the
+    // pages of the first positions (a lane for every 16), the queries
+    const int32_t sees = a.visible[(int64_t)seq * a.cols + (lane < (int)a.cols ? lane : 0)];
+    auto page_of = [&](uint32_t from) {
+        const uint32_t i = from + 16 * lane;
+        return i < a.limit ? (uint32_t)a.pages[seq * a.pages_row + (i >> a.c.page_shift)] : ~0u;
+    };
+    uint32_t page = page_of(begin);
+
     half8* const query = reinterpret_cast<half8*>(lds);          // [part][tile][chunk][step][lane]
     float* const factors = reinterpret_cast<float*>(lds + query_bytes<T, NC, NT>());
     for (uint32_t t = wave; t < NT; t += waves) {
@@ -176,20 +195,74 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
                 if constexpr (QP == 2) o[NT * NC * 2 * 64] = lo;
             }
     }
-    __syncthreads();
 
-    float factor[NT];
-    uint32_t seen[NT], least = ~0u;               // positions that this lane's rows see; the fewest of any row
+    // positions that any column sees; the fewest that one does
+    const uint32_t mine = sees < 0 ? 0u : ((uint32_t)sees < a.limit ? (uint32_t)sees : a.limit);
+    const uint32_t length = eight_max(mine), least = ~eight_max(~mine);
+    if (begin >= length && a.spans > 1) return;   // k_join reads spans with a position only
+    const uint32_t end = length - begin < a.span ? length : begin + a.span;      // 0 for a sequence of no position
+
+    // a lane's part of a row: 16 values of each 64 of K, DV values of V; a row
+    // shorter than that reads its first values again, against queries of 0 and
+    // into outputs that no one stores
+    const uint32_t in_page = (1u << a.c.page_shift) - 1u, stride = (uint32_t)a.c.token_stride;
+    uint32_t k_at[NC];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const uint32_t row = row0 + 16 * t + n;
-        factor[t] = factors[16 * t + n];
-        seen[t] = row < a.rows ? seen_by(a, seq, row / a.group) : ~0u;
-    }
-    for (uint32_t c = 0; c < a.cols; ++c) {
-        const uint32_t s = seen_by(a, seq, c);
-        least = s < least ? s : least;
-    }
+    for (int c = 0; c < NC; ++c) k_at[c] = n * stride + (64u * c + 16u * g < a.c.d ? 64u * c + 16u * g : 0u);
+    const uint32_t v_at = 4 * g * stride + ((uint32_t)(DV * n) < a.c.d ? DV * n : 0u);
+
+    // a tile: its pages and, of K and V, the operands and scales
+    struct Place {
+        uint32_t page[2];
+        bool ok[2];
+    };
+    auto place_of = [&](uint32_t at, uint32_t from) {
+        Place p;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            p.page[h] = (uint32_t)__builtin_amdgcn_readlane((int)page, (int)((at - from) / 16 + h));
+            p.ok[h] = p.page[h] < a.c.n_pages;
+            p.page[h] = p.ok[h] ? p.page[h] : 0u;
+        }
+        return p;
+    };
+    u32x4 kq[2][NC];
+    uint32_t vq[8][NC];
+    f32x4 kd[2], vd[2];
+    auto load_k = [&](uint32_t at, const Place& p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t place = (at + 16 * h) & in_page;
+            const int8_t* k = a.c.k + (p.page[h] * a.c.page_stride + head * a.c.head_stride + place * a.c.token_stride);
+#pragma unroll
+            for (int c = 0; c < NC; ++c) kq[h][c] = *reinterpret_cast<const u32x4*>(k + k_at[c]);
+            const float* d = a.c.k_scale + (p.page[h] * a.c.scale_page_stride + head * a.c.scale_head_stride + place);
+            kd[h] = *reinterpret_cast<const f32x4*>(d + 4u * g);
+        }
+    };
+    auto load_v = [&](uint32_t at, const Place& p) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t place = (at + 16 * h) & in_page;
+            const int8_t* v = a.c.v + (p.page[h] * a.c.page_stride + head * a.c.head_stride + place * a.c.token_stride);
+            const float* d = a.c.v_scale + (p.page[h] * a.c.scale_page_stride + head * a.c.scale_head_stride + place);
+            vd[h] = *reinterpret_cast<const f32x4*>(d + 4u * g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j, v += stride) {
+                if constexpr (NC == 1) {
+                    vq[4 * h + j][0] = *reinterpret_cast<const uint32_t*>(v + v_at);
+                } else if constexpr (NC == 2) {
+                    const u32x2 u = *reinterpret_cast<const u32x2*>(v + v_at);
+                    vq[4 * h + j][0] = u[0];
+                    vq[4 * h + j][1] = u[1];
+                } else {
+                    const u32x4 u = *reinterpret_cast<const u32x4*>(v + v_at);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) vq[4 * h + j][i] = u[i];
+                }
+            }
+        }
+    };
 
     f32x4 o[NT][DV];
     float m[NT], l[NT];
@@ -202,53 +275,39 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
     }
     int up = 127 + WEIGHT_BITS;                   // weights are scaled by 2^up, for scales below the normal range
 
-    // a lane's part of a row: 16 values of each 64 of K, DV values of V; a row
-    // shorter than that reads its first values again, against queries of 0 and
-    // into outputs that no one stores
-    const int64_t k_lane = n * a.c.token_stride, v_lane = (uint32_t)(DV * n) < a.c.d ? DV * n : 0;
-    const uint32_t in_page = (1u << a.c.page_shift) - 1u;
+    // the first tile is on its way while the queries are written
+    Place here = place_of(begin + TILE * wave, begin);
+    if (begin + TILE * wave < end) {
+        load_k(begin + TILE * wave, here);
+        load_v(begin + TILE * wave, here);
+    }
+    lds_barrier();
+    float factor[NT];
+    uint32_t seen[NT];                            // positions that this lane's rows see
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const uint32_t row = row0 + 16 * t + n;
+        factor[t] = factors[16 * t + n];
+        seen[t] = (uint32_t)__shfl((int)mine, (int)(row < a.rows ? row / a.group : 0u));
+        if (row >= a.rows) seen[t] = ~0u;
+    }
 
     for (uint32_t from = begin; from < end; from += SEGMENT) {
         const uint32_t to = end - from < SEGMENT ? end : from + SEGMENT;
-        // the page of every 16 positions, one a lane
-        uint32_t page = ~0u;
-        if (from + 16 * lane < to) page = (uint32_t)a.pages[seq * a.pages_row + ((from + 16 * lane) >> a.c.page_shift)];
-        for (uint32_t at = from + TILE * wave; at < to; at += TILE * waves) {
-            u32x4 kq[2][NC];
-            uint32_t vq[8][NC];
-            f32x4 kd[2], vd[2];
-            bool ok[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p = (uint32_t)__builtin_amdgcn_readlane((int)page, (int)((at - from) / 16 + h));
-                ok[h] = p < a.c.n_pages;
-                p = ok[h] ? p : 0u;
-                const uint32_t place = (at + 16 * h) & in_page;
-                const int64_t row = p * a.c.page_stride + head * a.c.head_stride + place * a.c.token_stride;
-                const int64_t scale = p * a.c.scale_page_stride + head * a.c.scale_head_stride + place + 4 * g;
-#pragma unroll
-                for (int c = 0; c < NC; ++c) {
-                    const uint32_t d = 64 * c + 16 * g;
-                    kq[h][c] = *reinterpret_cast<const u32x4*>(a.c.k + row + k_lane + (d < a.c.d ? d : 0u));
-                }
-                kd[h] = *reinterpret_cast<const f32x4*>(a.c.k_scale + scale);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int8_t* v = a.c.v + row + (4 * g + j) * a.c.token_stride + v_lane;
-                    if constexpr (NC == 1) {
-                        vq[4 * h + j][0] = *reinterpret_cast<const uint32_t*>(v);
-                    } else if constexpr (NC == 2) {
-                        const u32x2 u = *reinterpret_cast<const u32x2*>(v);
-                        vq[4 * h + j][0] = u[0];
-                        vq[4 * h + j][1] = u[1];
-                    } else {
-                        const u32x4 u = *reinterpret_cast<const u32x4*>(v);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) vq[4 * h + j][i] = u[i];
-                    }
-                }
-                vd[h] = *reinterpret_cast<const f32x4*>(a.c.v_scale + scale);
+        if (from != begin) {
+            page = page_of(from);
+            here = place_of(from + TILE * wave, from);
+            if (from + TILE * wave < to) {
+                load_k(from + TILE * wave, here);
+                load_v(from + TILE * wave, here);
             }
+        }
+        for (uint32_t at = from + TILE * wave; at < to; at += TILE * waves) {
+            // the next tile's loads are issued whether there is one or not (then this one's
+            // again): under a branch, what is waited for before would be unknown, and
+            // every wait would be for all of them (64 x 1 x 8192: 157 us and not 187)
+            const uint32_t next = at + TILE * waves < to ? at + TILE * waves : at;
+            const Place then = place_of(next, from);
 
             // scores
             f32x4 s[NT][2];
@@ -274,25 +333,34 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
                                 s[t][h] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k[h], b, s[t][h], 0, 0, 0);
                         }
                 }
+            const bool whole = at + TILE <= least && here.ok[0] && here.ok[1];
+            float x[NT][8];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[t][i] = s[t][i / 4][i % 4] * kd[i / 4][i % 4] * factor[t];
+            load_k(next, then);                   // K's registers are free again
 
-            // values past the length: 0, whatever their scales hold
-            const bool whole = at + TILE <= least && ok[0] && ok[1];
+            float ve[8];                          // the value scales, past the length 0, whatever is there
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ve[i] = vd[i / 4][i % 4];
             if (!whole) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t pos = at + 16 * (i / 4) + 4 * g + i % 4;
+                    ve[i] = here.ok[i / 4] && pos < length ? ve[i] : 0.0f;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (!ok[h] || at + 16 * h + 4 * g + r >= length) vd[h][r] = 0.0f;
+                    for (int t = 0; t < NT; ++t) x[t][i] = here.ok[i / 4] && pos < seen[t] ? x[t][i] : -__builtin_inff();
+                }
             }
             // the power of two that keeps weights in fp16
             float most = 0.0f;
+            const float bound = ldexpf(1.0f, WEIGHT_BITS + 1 - up);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) most = fmaxf(most, fabsf(vd[h][r]) < __builtin_inff() ? fabsf(vd[h][r]) : 0.0f);
-            const uint32_t top = __builtin_amdgcn_readfirstlane(__float_as_uint(quad_max(most)));
-            const int want = WEIGHT_BITS + 127 - (int)(top >> 23);       // 2^want * top in [2^13, 2^14); top >= 0
-            if (want < up) {
+            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(ve[i]) < __builtin_inff() ? fabsf(ve[i]) : 0.0f);
+            if (__any(most >= bound)) {
+                const uint32_t top = __builtin_amdgcn_readfirstlane(__float_as_uint(quad_max(most)));
+                const int want = WEIGHT_BITS + 127 - (int)(top >> 23);   // 2^want * top in [2^13, 2^14); top >= 0
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -302,21 +370,14 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
                 up = want;
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) vd[h][r] = ldexpf(vd[h][r], up);
+            for (int i = 0; i < 8; ++i) ve[i] = ldexpf(ve[i], up);
 
             half8 w[PP][NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                float x[8];
-                float top_t = -__builtin_inff();
+                float top_t = x[t][0];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    x[i] = s[t][i / 4][i % 4] * kd[i / 4][i % 4] * factor[t];
-                    if (!whole && !(ok[i / 4] && at + 16 * (i / 4) + 4 * g + i % 4 < seen[t])) x[i] = -__builtin_inff();
-                    top_t = fmaxf(top_t, x[i]);
-                }
+                for (int i = 1; i < 8; ++i) top_t = fmaxf(top_t, x[t][i]);
                 const float now = fmaxf(m[t], quad_max(top_t)), base = now == -__builtin_inff() ? 0.0f : now;
                 if (__any(now > m[t])) {
                     const float keep = __builtin_amdgcn_exp2f(m[t] - base);
@@ -325,16 +386,22 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
                     for (int i = 0; i < DV; ++i) o[t][i] *= keep;
                     m[t] = now;
                 }
+                float v[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(x[i] - base);
+                    const float p = __builtin_amdgcn_exp2f(x[t][i] - base);
                     l[t] += p;
-                    float v = p * vd[i / 4][i % 4];
-                    // a position that others see may have a scale that is not finite
-                    if (!whole && x[i] == -__builtin_inff()) v = 0.0f;
-                    const _Float16 hi = (_Float16)v;
+                    v[i] = p * ve[i];
+                }
+                if (!whole) {                     // a position that others see may have a scale that is not finite
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[i] = x[t][i] == -__builtin_inff() ? 0.0f : v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const _Float16 hi = (_Float16)v[i];
                     w[0][t][i] = hi;
-                    if constexpr (PP == 2) w[1][t][i] = (_Float16)(v - (float)hi);
+                    if constexpr (PP == 2) w[1][t][i] = (_Float16)(v[i] - (float)hi);
                 }
             }
 
@@ -344,9 +411,9 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
                 uint32_t b01[4], b23[4];          // codes 0 and 1, 2 and 3 of two positions each
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const uint32_t x = vq[2 * j][d4] ^ FLIP, y = vq[2 * j + 1][d4] ^ FLIP;
-                    b01[j] = __builtin_amdgcn_perm(y, x, 0x05010400u);
-                    b23[j] = __builtin_amdgcn_perm(y, x, 0x07030602u);
+                    const uint32_t y0 = vq[2 * j][d4] ^ FLIP, y1 = vq[2 * j + 1][d4] ^ FLIP;
+                    b01[j] = __builtin_amdgcn_perm(y1, y0, 0x05010400u);
+                    b23[j] = __builtin_amdgcn_perm(y1, y0, 0x07030602u);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -360,6 +427,8 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
                             o[t][4 * d4 + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[p][t], o[t][4 * d4 + i], 0, 0, 0);
                 }
             }
+            load_v(next, then);
+            here = then;
         }
     }
 
@@ -422,22 +491,43 @@ __global__ __launch_bounds__(W * 64) void k_attend(AttendArgs a) {
 template <typename T>
 __global__ __launch_bounds__(256) void k_join(AttendArgs a) {
     __shared__ f32x4 part[256];
+    __shared__ float weight[256];
+    __shared__ float words[4];
     const uint32_t row_id = blockIdx.x, row = row_id % a.rows, pair = row_id / a.rows, head = pair % a.c.n_heads,
-                   seq = pair / a.c.n_heads;
+                   seq = pair / a.c.n_heads, tid = threadIdx.x;
     const uint32_t length = seen_by_any(a, seq), spans = (length + a.span - 1) / a.span;
-    const uint32_t vecs = a.c.d / 4, lanes = 256 / vecs, k = threadIdx.x / vecs, at = threadIdx.x - k * vecs;
+    const uint32_t vecs = a.c.d / 4, lanes = 256 / vecs, k = tid / vecs, at = tid - k * vecs;
     const float2* stats = a.stats + (int64_t)row_id * a.spans;
     const f32x4* sums = reinterpret_cast<const f32x4*>(a.sums) + (int64_t)row_id * a.spans * vecs;
     float m = -__builtin_inff(), l = 0.0f;
-    for (uint32_t s = 0; s < spans; ++s) m = fmaxf(m, stats[s].x);
+    for (uint32_t s = tid; s < spans; s += 256) m = fmaxf(m, stats[s].x);
+    for (int i = 32; i; i >>= 1) m = fmaxf(m, __shfl_xor(m, i));
+    if ((tid & 63) == 0) words[tid >> 6] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(words[0], words[1]), fmaxf(words[2], words[3]));
     const float base = m == -__builtin_inff() ? 0.0f : m;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t s = 0; s < spans; ++s) l += stats[s].y * __builtin_amdgcn_exp2f(stats[s].x - base);
-    if (k < lanes)
-        for (uint32_t s = k; s < spans; s += lanes) v += sums[(int64_t)s * vecs + at] * __builtin_amdgcn_exp2f(stats[s].x - base);
-    part[threadIdx.x] = v;
+    for (uint32_t from = 0; from < spans; from += 256) {         // 256 spans' weights at a time
+        __syncthreads();
+        if (from + tid < spans) {
+            const float2 st = stats[from + tid];
+            weight[tid] = __builtin_amdgcn_exp2f(st.x - base);
+            l += st.y * weight[tid];
+        }
+        __syncthreads();
+        const uint32_t n = spans - from < 256 ? spans - from : 256;
+        if (k < lanes) {
+#pragma unroll 4
+            for (uint32_t s = k; s < n; s += lanes) v += sums[(int64_t)(from + s) * vecs + at] * weight[s];
+        }
+    }
+    for (int i = 32; i; i >>= 1) l += __shfl_xor(l, i);
+    part[tid] = v;
+    __syncthreads();
+    if ((tid & 63) == 0) words[tid >> 6] = l;
     __syncthreads();
     if (k == 0) {
+        l = words[0] + words[1] + words[2] + words[3];
         for (uint32_t i = 1; i < lanes; ++i) v += part[i * vecs + at];
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const uint32_t col = row / a.group, sub = row - col * a.group;
@@ -449,7 +539,7 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs a) {
 
 // How a call's work is split.
 struct Plan {
-    int64_t rows, span, spans, blocks;
+    int64_t rows, parts, span, spans, blocks;
     int chunks, tiles;                            // 64 values of a row, 16 rows
     size_t sums_bytes, bytes;
 };
@@ -460,7 +550,8 @@ Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_
     p.chunks = d <= 64 ? 1 : d <= 128 ? 2 : 4;
     const int64_t tiles = (p.rows + 15) / 16, most = p.chunks == 4 ? 2 : 3;
     p.tiles = (int)std::min(tiles, most);
-    const int64_t pairs = seqs * heads * ((tiles + p.tiles - 1) / p.tiles);
+    p.parts = (tiles + p.tiles - 1) / p.tiles;
+    const int64_t pairs = seqs * heads * p.parts;
         // four blocks for each of 256 CUs, spans of at least 256 positions
     const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, pairs));
     p.span = std::max<int64_t>(256, ((limit + want - 1) / want + 127) / 128 * 128);
@@ -544,6 +635,7 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
         bytes[i] *= es;
     }
     if (((uintptr_t)q | (uintptr_t)out) & (uintptr_t)(es - 1) || ((uintptr_t)pages | (uintptr_t)visible) & 3u) return MOEQ8_EALIGN;
+    if (a.c.token_stride > (1ll << 26)) return MOEQ8_EUNSUPPORTED;        // a lane's offsets have 32 bits
     if (ranges_overlap(q, bytes[0], out, bytes[1]) || clashes_with_cache(a.c, out, bytes[1])) return MOEQ8_EINVAL;
     const Plan p = plan_for(n_seqs, n_cols, n_q_heads, heads, d, max_visible);
     if (p.blocks > most_blocks(WAVES * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
@@ -558,7 +650,7 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
     a.cols = (uint32_t)n_cols; a.group = (uint32_t)(n_q_heads / heads); a.rows = (uint32_t)p.rows;
     const int64_t positions = n_table << a.c.page_shift;
     a.limit = (uint32_t)std::min(max_visible, positions);
-    a.span = (uint32_t)p.span; a.spans = (uint32_t)p.spans; a.seqs = (uint32_t)n_seqs;
+    a.span = (uint32_t)p.span; a.spans = (uint32_t)p.spans; a.seqs = (uint32_t)n_seqs; a.parts = (uint32_t)p.parts;
     a.factor = (float)(scale * 1.4426950408889634);
     switch (dtype) {
         case MOEQ8_F32: return attend<float>(a, p, (hipStream_t)stream);
