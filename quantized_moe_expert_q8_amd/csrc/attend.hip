@@ -46,7 +46,6 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TILE = 32, SEGMENT = 1024;          // positions a tile; positions whose pages a wave holds at a time
-constexpr int WAVES = 4;
 constexpr int WEIGHT_BITS = 13;                   // weights stay below 2^14
 
 struct AttendArgs {
@@ -59,7 +58,8 @@ struct AttendArgs {
     float2* stats;
     uint32_t cols, group, rows, limit;            // rows: cols * group; limit: what visible is taken within
     uint32_t span, spans, seqs, parts;            // parts: of the rows, 16 * NT each
-    float factor;                                 // scale * log2(e)
+    float factor;                                 // |scale| * log2(e)
+    uint32_t flip;                                // the scale's sign bit, which the queries take
 };
 
 __device__ __forceinline__ uint32_t seen_by(const AttendArgs& a, uint32_t seq, uint32_t col) {
@@ -128,7 +128,7 @@ template <int NC, int NT>
 constexpr int min_waves() { return NC * NT <= 1 ? 4 : NC * NT <= 2 ? 3 : NC * NT <= 4 ? 2 : 1; }
 
 template <typename T, int NC, int NT, int W>
-__global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_attend(AttendArgs a) {
     constexpr int DV = 4 * NC;                    // values of a V row a lane loads
     constexpr int QP = Parts<T>::Q, PP = Parts<T>::P;
     __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes<T, NC, NT>(W)];
@@ -136,15 +136,17 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int lane = threadIdx.x & 63, g = lane >> 4, n = lane & 15;
 
-    // block: key heads fastest, then the rows' part, the sequence and, slowest, the span:
-    // blocks go to the 8 XCDs in turn, and with the spans fastest the XCDs that got a
-    // short sequence's last spans had nothing to do
-    uint32_t id = blockIdx.x;
-    const uint32_t head = id % a.c.n_heads;
+    // Units of work, a span of a sequence for a key head: heads fastest, then the
+    // sequence, the span slowest.  Blocks go to the 8 XCDs in turn: with the spans
+    // fastest, the XCDs that got short sequences' last spans had nothing to do (64 x 1 x
+    // 8192: 170 and 143 us).  The blocks of a unit that have different rows are 8 apart,
+    // and find its keys and values in their XCD's L2.
+    const uint32_t eight = blockIdx.x / 8, part = eight % a.parts;
+    uint32_t id = eight / a.parts * 8 + blockIdx.x % 8;
+    const uint32_t head = id % a.c.n_heads, row0 = part * (16 * NT);
     id /= a.c.n_heads;
-    const uint32_t row0 = id % a.parts * (16 * NT);
-    id /= a.parts;
     const uint32_t seq = id % a.seqs, split = id / a.seqs;
+    if (split >= a.spans) return;
     const uint32_t begin = split * a.span;
 
     // what depends on nothing is loaded first: what the columns see (a lane each), the
@@ -186,7 +188,7 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
                 half8 hi, lo;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float x = ldexpf(v[c][8 * s + i], up);
+                    const float x = __uint_as_float(__float_as_uint(ldexpf(v[c][8 * s + i], up)) ^ a.flip);
                     hi[i] = (_Float16)x;
                     lo[i] = (_Float16)(x - (float)hi[i]);
                 }
@@ -338,7 +340,7 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) x[t][i] = s[t][i / 4][i % 4] * kd[i / 4][i % 4] * factor[t];
+                for (int i = 0; i < 8; ++i) x[t][i] = s[t][i / 4][i % 4] * kd[i / 4][i % 4];
             load_k(next, then);                   // K's registers are free again
 
             float ve[8];                          // the value scales, past the length 0, whatever is there
@@ -357,17 +359,22 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
             float most = 0.0f;
             const float bound = ldexpf(1.0f, WEIGHT_BITS + 1 - up);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(ve[i]) < __builtin_inff() ? fabsf(ve[i]) : 0.0f);
-            if (__any(most >= bound)) {
+            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(ve[i]));
+            if (__any(most >= bound)) {           // infinite ones come here every time, and do not count
+                most = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(ve[i]) < __builtin_inff() ? fabsf(ve[i]) : 0.0f);
                 const uint32_t top = __builtin_amdgcn_readfirstlane(__float_as_uint(quad_max(most)));
                 const int want = WEIGHT_BITS + 127 - (int)(top >> 23);   // 2^want * top in [2^13, 2^14); top >= 0
+                if (want < up) {
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                    for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < DV; ++i)
+                        for (int i = 0; i < DV; ++i)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) o[t][i][r] = ldexpf(o[t][i][r], want - up);
-                up = want;
+                            for (int r = 0; r < 4; ++r) o[t][i][r] = ldexpf(o[t][i][r], want - up);
+                    up = want;
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) ve[i] = ldexpf(ve[i], up);
@@ -378,18 +385,25 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
                 float top_t = x[t][0];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) top_t = fmaxf(top_t, x[t][i]);
-                const float now = fmaxf(m[t], quad_max(top_t)), base = now == -__builtin_inff() ? 0.0f : now;
+                // maxima are of the scores before the factor, which is not negative
+                const float now = fmaxf(m[t], quad_max(top_t)), base = now == -__builtin_inff() ? 0.0f : now * factor[t];
                 if (__any(now > m[t])) {
-                    const float keep = __builtin_amdgcn_exp2f(m[t] - base);
+                    const float keep = m[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[t] * factor[t] - base);
                     l[t] *= keep;
 #pragma unroll
                     for (int i = 0; i < DV; ++i) o[t][i] *= keep;
                     m[t] = now;
                 }
-                float v[8];
+                float e[8], v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(x[t][i], factor[t], -base);
+                if (!whole) {                     // the factor may be 0
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] = x[t][i] == -__builtin_inff() ? x[t][i] : e[i];
+                }
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(x[t][i] - base);
+                    const float p = __builtin_amdgcn_exp2f(e[i]);
                     l[t] += p;
                     v[i] = p * ve[i];
                 }
@@ -439,6 +453,7 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const float total = quad_sum(l[t]);
+        m[t] = m[t] == -__builtin_inff() ? m[t] : m[t] * factor[t];      // from here on with the factor
         if (g == 0) stats[(wave * NT + t) * 16 + n] = float2{m[t], total};
     }
     __syncthreads();
@@ -487,48 +502,73 @@ __global__ __launch_bounds__(W * 64, (min_waves<NC, NT>())) void k_attend(Attend
     }
 }
 
-// A row's spans together: 256 threads, each with 4 values of every so many spans.
-template <typename T>
-__global__ __launch_bounds__(256) void k_join(AttendArgs a) {
-    __shared__ f32x4 part[256];
-    __shared__ float weight[256];
-    __shared__ float words[4];
-    const uint32_t row_id = blockIdx.x, row = row_id % a.rows, pair = row_id / a.rows, head = pair % a.c.n_heads,
-                   seq = pair / a.c.n_heads, tid = threadIdx.x;
-    const uint32_t length = seen_by_any(a, seq), spans = (length + a.span - 1) / a.span;
-    const uint32_t vecs = a.c.d / 4, lanes = 256 / vecs, k = tid / vecs, at = tid - k * vecs;
-    const float2* stats = a.stats + (int64_t)row_id * a.spans;
-    const f32x4* sums = reinterpret_cast<const f32x4*>(a.sums) + (int64_t)row_id * a.spans * vecs;
+// A row's spans together.  LANES threads have the same 4 values of a row, of every
+// LANES-th span each; a block has as many rows as fit.
+template <typename T, int LANES>
+__global__ __launch_bounds__(256) void k_join(AttendArgs a, uint32_t row_count) {
+    __shared__ f32x4 part[LANES > 1 ? 256 : 1];
+    const uint32_t vecs = a.c.d / 4, tid = threadIdx.x, slot = tid / (vecs * LANES), in = tid - slot * (vecs * LANES), k = in / vecs,
+                   at = in - k * vecs, per_block = 256 / (vecs * LANES);
+    const uint32_t row_id = blockIdx.x * per_block + slot;
+    const bool real = slot < per_block && row_id < row_count;
+    const uint32_t id = real ? row_id : 0u, row = id % a.rows, pair = id / a.rows, head = pair % a.c.n_heads, seq = pair / a.c.n_heads;
+    uint32_t length = 0;
+#pragma unroll
+    for (uint32_t c = 0; c < MOEQ8_MAX_COLS; ++c) {              // no load waits for another
+        const uint32_t n = seen_by(a, seq, c < a.cols ? c : 0u);
+        length = n > length ? n : length;
+    }
+    const uint32_t spans = (length + a.span - 1) / a.span;
+    const float2* stats = a.stats + (int64_t)id * a.spans;
+    const f32x4* sums = reinterpret_cast<const f32x4*>(a.sums) + (int64_t)id * a.spans * vecs;
+    // each span's statistics and values with the running maximum of those before
+    constexpr uint32_t AHEAD = 8;
     float m = -__builtin_inff(), l = 0.0f;
-    for (uint32_t s = tid; s < spans; s += 256) m = fmaxf(m, stats[s].x);
-    for (int i = 32; i; i >>= 1) m = fmaxf(m, __shfl_xor(m, i));
-    if ((tid & 63) == 0) words[tid >> 6] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(words[0], words[1]), fmaxf(words[2], words[3]));
-    const float base = m == -__builtin_inff() ? 0.0f : m;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (uint32_t from = 0; from < spans; from += 256) {         // 256 spans' weights at a time
-        __syncthreads();
-        if (from + tid < spans) {
-            const float2 st = stats[from + tid];
-            weight[tid] = __builtin_amdgcn_exp2f(st.x - base);
-            l += st.y * weight[tid];
+    for (uint32_t from = k; from < spans; from += LANES * AHEAD) {
+        float2 st[AHEAD];
+        f32x4 u[AHEAD];
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            const uint32_t s = from + i * LANES < spans ? from + i * LANES : from;
+            st[i] = stats[s];
+            u[i] = sums[(int64_t)s * vecs + at];
+            if (from + i * LANES >= spans) st[i] = float2{-__builtin_inff(), 0.0f};
         }
+        float now = m;
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) now = fmaxf(now, st[i].x);
+        const float base = now == -__builtin_inff() ? 0.0f : now, keep = __builtin_amdgcn_exp2f(m - base);
+        l *= keep;
+        v *= keep;
+#pragma unroll
+        for (uint32_t i = 0; i < AHEAD; ++i) {
+            const float w = __builtin_amdgcn_exp2f(st[i].x - base);
+            l += st[i].y * w;
+            v += u[i] * w;
+        }
+        m = now;
+    }
+    if constexpr (LANES > 1) {                    // the lanes' together, in their order
+        __shared__ float2 mine[256];
+        part[tid] = v;
+        mine[tid] = float2{m, l};
         __syncthreads();
-        const uint32_t n = spans - from < 256 ? spans - from : 256;
-        if (k < lanes) {
-#pragma unroll 4
-            for (uint32_t s = k; s < n; s += lanes) v += sums[(int64_t)(from + s) * vecs + at] * weight[s];
+        if (k == 0 && real) {
+            float now = m;
+            for (uint32_t i = 1; i < LANES; ++i) now = fmaxf(now, mine[tid + i * vecs].x);
+            const float base = now == -__builtin_inff() ? 0.0f : now, keep = __builtin_amdgcn_exp2f(m - base);
+            l *= keep;
+            v *= keep;
+            for (uint32_t i = 1; i < LANES; ++i) {
+                const float2 st = mine[tid + i * vecs];
+                const float w = __builtin_amdgcn_exp2f(st.x - base);
+                l += st.y * w;
+                v += part[tid + i * vecs] * w;
+            }
         }
     }
-    for (int i = 32; i; i >>= 1) l += __shfl_xor(l, i);
-    part[tid] = v;
-    __syncthreads();
-    if ((tid & 63) == 0) words[tid >> 6] = l;
-    __syncthreads();
-    if (k == 0) {
-        l = words[0] + words[1] + words[2] + words[3];
-        for (uint32_t i = 1; i < lanes; ++i) v += part[i * vecs + at];
+    if (k == 0 && real) {
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const uint32_t col = row / a.group, sub = row - col * a.group;
         T* out = (T*)a.out + seq * a.o_seq + col * a.o_col + ((int64_t)head * a.group + sub) * a.o_head + 4 * at;
@@ -540,7 +580,7 @@ __global__ __launch_bounds__(256) void k_join(AttendArgs a) {
 // How a call's work is split.
 struct Plan {
     int64_t rows, parts, span, spans, blocks;
-    int chunks, tiles;                            // 64 values of a row, 16 rows
+    int chunks, tiles, waves;                     // 64 values of a row, 16 rows; waves a block
     size_t sums_bytes, bytes;
 };
 
@@ -552,11 +592,17 @@ Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_
     p.tiles = (int)std::min(tiles, most);
     p.parts = (tiles + p.tiles - 1) / p.tiles;
     const int64_t pairs = seqs * heads * p.parts;
-        // four blocks for each of 256 CUs, spans of at least 256 positions
-    const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, pairs));
-    p.span = std::max<int64_t>(256, ((limit + want - 1) / want + 127) / 128 * 128);
+        const int64_t fill = 768;
+    p.waves = p.chunks * p.tiles > 4 || pairs * ((limit + 1023) / 1024) >= fill ? 4 : 8;
+    if (p.waves == 8) {
+        const int64_t want = std::max<int64_t>(1, 256 / pairs);
+        p.span = limit <= 1024 ? 1024 : std::max<int64_t>(512, ((limit + want - 1) / want + 255) / 256 * 256);
+    } else {
+        const int64_t want = std::max<int64_t>(1, 2048 / pairs);
+        p.span = std::max<int64_t>(512, ((limit + want - 1) / want + 127) / 128 * 128);
+    }
     p.spans = std::max<int64_t>(1, (limit + p.span - 1) / p.span);
-    p.blocks = pairs * p.spans;
+    p.blocks = (seqs * heads * p.spans + 7) / 8 * 8 * p.parts;
     p.sums_bytes = p.spans > 1 ? (size_t)(seqs * heads * p.rows * p.spans * d * 4) : 0;
     p.bytes = p.spans > 1 ? p.sums_bytes + (size_t)(seqs * heads * p.rows * p.spans * 8) : 0;
     return p;
@@ -564,7 +610,13 @@ Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_
 
 template <typename T, int NC, int NT>
 int launch_attend(const AttendArgs& a, const Plan& p, hipStream_t stream) {
-    hipLaunchKernelGGL((k_attend<T, NC, NT, WAVES>), dim3((uint32_t)p.blocks), dim3(WAVES * 64), 0, stream, a);
+    if constexpr (NC * NT <= 4) {
+        if (p.waves == 8) {
+            hipLaunchKernelGGL((k_attend<T, NC, NT, 8>), dim3((uint32_t)p.blocks), dim3(512), 0, stream, a);
+            return check_launch();
+        }
+    }
+    hipLaunchKernelGGL((k_attend<T, NC, NT, 4>), dim3((uint32_t)p.blocks), dim3(256), 0, stream, a);
     return check_launch();
 }
 
@@ -582,8 +634,15 @@ int attend(const AttendArgs& a, const Plan& p, hipStream_t stream) {
         default: s = launch_attend<T, 4, 2>(a, p, stream); break;
     }
     if (s != MOEQ8_OK || p.spans == 1) return s;
-    hipLaunchKernelGGL((k_join<T>), dim3((uint32_t)((int64_t)a.seqs * a.c.n_heads * a.rows)), dim3(256), 0, stream, a);
-    return check_launch();
+    const uint32_t rows = (uint32_t)((int64_t)a.seqs * a.c.n_heads * a.rows), vecs = a.c.d / 4;
+    auto join = [&](auto lanes) {
+        constexpr int L = decltype(lanes)::value;
+        const uint32_t per_block = 256 / (vecs * L);
+        hipLaunchKernelGGL((k_join<T, L>), dim3((rows + per_block - 1) / per_block), dim3(256), 0, stream, a, rows);
+        return check_launch();
+    };
+    // a row of 256 values takes 64 threads a lane
+    return p.spans <= 8 ? join(std::integral_constant<int, 1>{}) : join(std::integral_constant<int, 4>{});
 }
 
 // What both entry points refuse of the sizes.
@@ -638,7 +697,7 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
     if (a.c.token_stride > (1ll << 26)) return MOEQ8_EUNSUPPORTED;        // a lane's offsets have 32 bits
     if (ranges_overlap(q, bytes[0], out, bytes[1]) || clashes_with_cache(a.c, out, bytes[1])) return MOEQ8_EINVAL;
     const Plan p = plan_for(n_seqs, n_cols, n_q_heads, heads, d, max_visible);
-    if (p.blocks > most_blocks(WAVES * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
+    if (p.blocks > most_blocks(p.waves * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MOEQ8_EINVAL;
     if (p.bytes && (uintptr_t)workspace & 15u) return MOEQ8_EALIGN;
     a.q = q; a.q_seq = q_seq_stride; a.q_col = q_col_stride; a.q_head = q_head_stride;
@@ -651,7 +710,8 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
     const int64_t positions = n_table << a.c.page_shift;
     a.limit = (uint32_t)std::min(max_visible, positions);
     a.span = (uint32_t)p.span; a.spans = (uint32_t)p.spans; a.seqs = (uint32_t)n_seqs; a.parts = (uint32_t)p.parts;
-    a.factor = (float)(scale * 1.4426950408889634);
+    a.factor = (float)(std::abs(scale) * 1.4426950408889634);
+    a.flip = scale < 0.0 ? 0x80000000u : 0u;
     switch (dtype) {
         case MOEQ8_F32: return attend<float>(a, p, (hipStream_t)stream);
         case MOEQ8_F16: return attend<f16_t>(a, p, (hipStream_t)stream);
