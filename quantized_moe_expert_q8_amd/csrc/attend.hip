@@ -588,7 +588,7 @@ Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_
     Plan p;
     p.rows = cols * (q_heads / heads);
     p.chunks = d <= 64 ? 1 : d <= 128 ? 2 : 4;
-    const int64_t tiles = (p.rows + 15) / 16, most = p.chunks == 4 ? 2 : 3;
+    const int64_t tiles = (p.rows + 15) / 16, most = p.chunks == 4 ? 1 : 3;
     p.tiles = (int)std::min(tiles, most);
     p.parts = (tiles + p.tiles - 1) / p.tiles;
     const int64_t pairs = seqs * heads * p.parts;
@@ -630,8 +630,8 @@ int attend(const AttendArgs& a, const Plan& p, hipStream_t stream) {
         case 9: s = launch_attend<T, 2, 1>(a, p, stream); break;
         case 10: s = launch_attend<T, 2, 2>(a, p, stream); break;
         case 11: s = launch_attend<T, 2, 3>(a, p, stream); break;
-        case 17: s = launch_attend<T, 4, 1>(a, p, stream); break;
-        default: s = launch_attend<T, 4, 2>(a, p, stream); break;
+        default: s = launch_attend<T, 4, 1>(a, p, stream); break;
+
     }
     if (s != MOEQ8_OK || p.spans == 1) return s;
     const uint32_t rows = (uint32_t)((int64_t)a.seqs * a.c.n_heads * a.rows), vecs = a.c.d / 4;
