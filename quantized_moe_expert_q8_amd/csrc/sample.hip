@@ -70,6 +70,9 @@ struct Rules {
     double per_logit;                             // steps of the exponent's table a logit: 64 log2(e) / T
     double per_nat;                               // 1 / T
     __device__ bool pure() const { return !greedy && !k && p == 1.0f && least == 0.0f; }
+    // whether what min-p drops goes into the last bin (top-p counts it; not where top-p is
+    // a part of what top-k leaves of it)
+    __device__ bool rest() const { return least > 0.0f && !(k && p < 1.0f); }
     // whether k_scan sums the masses: for the draw, or for top-p beside min-p
     __device__ bool masses() const { return !greedy && !k && (p < 1.0f) == (least > 0.0f); }
 };
@@ -113,13 +116,13 @@ struct Weigh {
         return __builtin_ldexp(v, i >> 6);
     }
     // in units of 2^-bits, bits <= 51: rounded by adding 2^52, whose low bits they then are
-    __device__ __forceinline__ uint64_t units(float z, int bits, int& i) const {
-        const double v = __builtin_ldexp(at(steps(z), i), (i >> 6) + bits) + 0x1p52;
-        return __builtin_bit_cast(uint64_t, v) & ((1ull << 52) - 1);
+    static __device__ __forceinline__ uint64_t rounded(double v, int i, int bits) {
+        return __builtin_bit_cast(uint64_t, __builtin_ldexp(v, (i >> 6) + bits) + 0x1p52) & ((1ull << 52) - 1);
     }
     __device__ __forceinline__ uint64_t units(float z, int bits) const {
         int i;
-        return units(z, bits, i);
+        const double v = at(steps(z), i);
+        return rounded(v, i, bits);
     }
 };
 __device__ __forceinline__ int bin_of(int i) {    // i <= 0
@@ -389,8 +392,10 @@ __global__ __launch_bounds__(256) void k_bins(SampleArgs a) {
             for (int j = 0; j < 8; ++j) {
                 if (!(v[j] > -__builtin_inff())) continue;
                 int n;
-                const uint64_t u = w.units(v[j], a.bits, n);
-                const int b = bin_of(n);
+                const double real = w.at(w.steps(v[j]), n);
+                const uint64_t u = Weigh::rounded(real, n, a.bits);
+                // what min-p drops counts for top-p, behind all others
+                const int b = r.rest() && __builtin_ldexp(real, n >> 6) < (double)r.least ? BINS - 1 : bin_of(n);
                 atomicAdd(&mass[b], (unsigned long long)u);
                 if (r.k) atomicAdd(&count[b], 1u);
             }
@@ -651,8 +656,13 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
         return true;
     }
 
-    // keys from `least` on pass min-p; a bin's keys are those from_bin(b) .. from_bin(b - 1)
-    auto first_key = [&](auto pass) {             // by a wave: the smallest key with pass, which larger ones have too
+    // By a wave: the smallest key with pass, which larger ones have too, near the logit
+    // `guess`: 64 keys there at once, or else a search of 6 steps.
+    auto first_key = [&](double guess, auto pass) {
+        const float near = (float)guess;
+        const uint32_t mid = near > -__FLT_MAX__ ? key_of(near) : KEY_FIRST + 32, at0 = (mid < KEY_FIRST + 32 ? KEY_FIRST + 32 : mid) - 32 + lane;
+        const uint64_t in = __ballot(at0 >= o.top || pass(logit_of(at0)));
+        if (in && !(in & 1)) return (uint32_t)__builtin_amdgcn_readlane((int)at0, (int)__builtin_ctzll(in));
         uint32_t lo = KEY_FIRST - 1, hi = o.top;
 #pragma unroll 1
         while (hi - lo > 1) {
@@ -665,7 +675,7 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
     };
     s.top[tid] = o.key;
     if (wave == 0) {
-        const uint32_t least = r.least > 0.0f ? first_key([&](float v) { return w.real(v) >= (double)r.least; }) : KEY_FIRST;
+        const uint32_t least = r.least > 0.0f ? first_key((double)top + log((double)r.least) / r.per_nat, [&](float v) { return w.real(v) >= (double)r.least; }) : KEY_FIRST;
         if (lane == 0) s.least = least;
     }
 
@@ -887,10 +897,11 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
         s.pick_before = ~0ull;                    // the ties
         s.n = 0;
     }
-    // top-k by the counts, then top-p by the masses, then min-p
+    // top-k by the counts, then top-p by the masses, then min-p, whose bin the list has
+    // to hold unless what it drops is in the last bin
 #pragma unroll 1
     for (int step = 0; step < 3; ++step) {
-        if (step == 0 ? r.k == 0 : step == 1 ? r.p == 1.0f : r.least == 0.0f) continue;
+        if (step == 0 ? r.k == 0 : step == 1 ? r.p == 1.0f : r.least == 0.0f || r.rest()) continue;
         uint64_t want = 0, before = 0;
         uint32_t bin;
         if (step < 2) {
@@ -906,15 +917,17 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
             __syncthreads();
             bin = s.seg;
             before = s.rest;
+            if (r.rest() && bin == BINS - 1) continue;           // min-p cuts above
         } else {
             __syncthreads();
-            if (s.least <= s.floor) continue;     // the others cut above it
+            if (s.least <= s.floor) continue;     // the others cut above
             bin = (uint32_t)bin_of(w, logit_of(s.least));
         }
         if (bin != held) {
             if (wave == 0) {
-                const uint32_t lo = first_key([&](float v) { return bin_of(w, v) <= (int)bin; });
-                const uint32_t hi = bin ? first_key([&](float v) { return bin_of(w, v) < (int)bin; }) : KEY_INF;
+                // a bin has 4 steps, rounded to the nearest: from 4 bin + 3.5 to 4 bin - 0.5 below
+                const uint32_t lo = first_key((double)top - (4.0 * bin + 3.5) / w.c, [&](float v) { return bin_of(w, v) <= (int)bin; });
+                const uint32_t hi = bin ? first_key((double)top - (4.0 * bin - 0.5) / w.c, [&](float v) { return bin_of(w, v) < (int)bin; }) : KEY_INF;
                 if (lane == 0) {
                     s.from = lo;
                     s.pick_key = hi;
@@ -949,8 +962,10 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
         bin_mass = tid < bin ? bin_mass : (tid == bin ? s.rest : 0);
     }
     __syncthreads();
-    const uint32_t floor = s.floor;
-    const uint32_t limit = s.limit;
+    // where min-p cuts above the others: all that are equal to its key, of the bins all but the last
+    const bool by_least = r.rest() && s.least > s.floor;
+    const uint32_t floor = by_least ? s.least : s.floor, limit = by_least ? vocab : s.limit;
+    if (by_least) held = BINS - 1;
     const float above = floor ? logit_of(floor) : -__builtin_inff();
     auto drawn = [&](float v, uint32_t i) -> uint64_t {
         return v > above || (floor && v == above && i <= limit) ? w.units(v, a.bits) : 0;
@@ -963,7 +978,7 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
         uint64_t sum = 0;
 #pragma unroll 4
         for (uint32_t b = lane; b < BINS; b += 64) sum += b < held ? a.bin_mass[(row * a.tiles + wave) * BINS + b] : 0;
-        const uint32_t n = held == ~0u ? 0 : s.n, first = wave * a.tile_segs * SEG, past = first + a.tile_segs * SEG;
+        const uint32_t n = held == ~0u || by_least ? 0 : s.n, first = wave * a.tile_segs * SEG, past = first + a.tile_segs * SEG;
 #pragma unroll 1
         for (uint32_t e = lane; e < n; e += 64) {
             const uint32_t key = s.key[e], i = s.index[e];

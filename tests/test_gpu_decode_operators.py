@@ -530,6 +530,20 @@ def test_sample_full_vocabulary(dtype):
         check_sample(z, u, TYPES[dtype], **rules)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rules", [dict(top_p=0.6), dict(top_p=0.6, min_p=0.05), dict(top_p=0.99, min_p=0.3), dict(min_p=0.02),
+                                   dict(top_k=9000), dict(top_k=9000, top_p=0.7), dict(top_k=9000, min_p=0.03),
+                                   dict(top_k=30000, top_p=0.9, min_p=0.02), dict(top_k=30000, top_p=0.5, min_p=0.01),
+                                   dict(top_k=9000, top_p=0.97, min_p=0.4), dict(temperature=0.3, top_p=0.8)],
+                         ids=lambda r: "-".join(f"{k}{v}" for k, v in r.items()))
+def test_sample_broad_distributions(rules, dtype):
+    """No few likely tokens: what is kept are thousands, and the thresholds fall among many."""
+    z, u = some_logits(3, 60011, 31, 0.7)
+    z[1] = np.round(z[1] * 4) / 4                           # many equal ones
+    z[2, 1000:59000] = -np.inf
+    check_sample(z, u, TYPES[dtype], **rules)
+
+
 def test_sample_frequencies_follow_the_weights():
     """Equally spaced numbers draw each token as often as its weight says, to one each side."""
     z = np.log([4.0, 1.0, 0.0 + 1e-30, 3.0, 2.0])
