@@ -1,6 +1,16 @@
-"""The end of a verify / decode step as a fixed sequence of libmoeq8 calls: the
-norm in front of a routed MoE block, the block, the final norm, the vocabulary
-head and the sampling rules on its logits.
+"""A verify / decode step around the routed experts as fixed sequences of libmoeq8
+calls.
+
+attend(): the attention block in front of them, over a paged int8 cache.
+
+    q, s, r     = rms_norm_q8(x, w, residual)        int8 rows and the residual stream
+    qkv         = gemm_i8(q, s, Wqkv)                queries, keys and values of the columns
+    kv_cache_write_i8(k, v, cache, slots)            the columns' own rows
+    a           = paged_attention_i8(q, cache, pages, visible)
+    y           = gemm_i8(i8_quantize_rows(a), Wo)   into the next norm, with r
+
+forward(): the norm in front of a routed MoE block, the block, the final norm, the
+vocabulary head, the sampling rules on its logits, and the draw of the tokens.
 
     q, s, xq, r = rms_norm_q8(x, w, residual)        one pass: residual, int8 rows and q8_1 rows
     router      = gemm_i8(q, s, Wr)                  expert scores
@@ -8,6 +18,7 @@ head and the sampling rules on its logits.
     q, s, r     = rms_norm_q8(y, w_out, residual=r)
     z           = gemm_i8(q, s, Wv)                  vocabulary logits
     z           = logits_process(z, ...)             penalties, biases, grammar mask, in place
+    t, logprob  = logits_sample(z, u, ...)           where asked for
 
 Weights are int8 with a scale per output channel (quantize_dense, once at load
 time); buffers live in a workspace, so a step allocates nothing and can be
@@ -48,6 +59,59 @@ class VerifyWeights:
     head: DenseI8                    # [vocab, hidden]
 
 
+@dataclass
+class AttentionWeights:
+    norm: torch.Tensor               # [hidden], the activations' dtype
+    qkv: DenseI8                     # [(heads + 2 kv_heads) * d, hidden]: queries, keys, values
+    out: DenseI8                     # [hidden, heads * d]
+    heads: int
+    kv_heads: int
+    d: int
+
+
+class AttentionWorkspace:
+    """Buffers of attend() for seqs sequences of cols columns; no sequence sees
+    more than max_visible positions."""
+
+    def __init__(self, seqs: int, cols: int, weights: AttentionWeights, max_visible: int, device):
+        dev = torch.device(device)
+        w, n, hidden = weights, seqs * cols, weights.qkv.codes.shape[1]
+        new = lambda *s, dtype=torch.float32: torch.empty(s, dtype=dtype, device=dev)
+        self.seqs, self.cols, self.max_visible = seqs, cols, max_visible
+        self.q, self.scale = new(n, hidden, dtype=torch.int8), new(n)
+        self.qkv = new(n, (w.heads + 2 * w.kv_heads) * w.d)
+        self.attended = new(seqs, cols, w.heads, w.d)
+        self.rows, self.row_scale = new(n, w.heads * w.d, dtype=torch.int8), new(n)
+        self.out, self.residual = new(n, hidden), new(n, hidden)
+        self.workspace = new(ops.paged_attention_workspace_bytes(seqs, cols, w.heads, w.kv_heads, w.d, max_visible),
+                             dtype=torch.uint8)
+
+
+def attend(x: torch.Tensor, residual: torch.Tensor, weights: AttentionWeights, ws: AttentionWorkspace,
+           cache: ops.KVCacheI8, pages: torch.Tensor, visible: torch.Tensor, slots: torch.Tensor, *, eps: float = 1e-6,
+           scale: float | None = None, rotate=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Enqueue the attention block of seqs * cols tokens on the current stream: x
+    and residual [tokens, hidden] fp32, a sequence's columns in a row.
+
+    slots (int64 [tokens]) are where the tokens' own keys and values go, pages and
+    visible as for ops.paged_attention_i8.  rotate(q, k), if given, puts positions
+    into the views q [tokens, heads, d] and k [tokens, kv_heads, d] in place before
+    they are used.  Returns the block's output and the residual stream in front of
+    it, both [tokens, hidden], which forward takes."""
+    w, n = weights, ws.seqs * ws.cols
+    ops.rms_norm_q8(x, w.norm, eps=eps, residual=residual, residual_out=ws.residual, q=ws.q, scale=ws.scale)
+    ops.gemm_i8(ws.q, ws.scale, w.qkv.codes, w.qkv.scale, out=ws.qkv)
+    q, k, v = (t.view(n, -1, w.d) for t in ws.qkv.split([w.heads * w.d, w.kv_heads * w.d, w.kv_heads * w.d], dim=1))
+    if rotate is not None:
+        rotate(q, k)
+    ops.kv_cache_write_i8(k, v, cache, slots)
+    ops.paged_attention_i8(q.view(ws.seqs, ws.cols, w.heads, w.d), cache, pages, visible, scale=scale,
+                           max_visible=ws.max_visible, out=ws.attended, workspace=ws.workspace)
+    ops.i8_quantize_rows(ws.attended.view(n, -1), q=ws.rows, scale=ws.row_scale)
+    ops.gemm_i8(ws.rows, ws.row_scale, w.out.codes, w.out.scale, out=ws.out)
+    return ws.out, ws.residual
+
+
 class VerifyWorkspace:
     def __init__(self, ncols: int, weights: VerifyWeights, topk: int, device):
         dev = torch.device(device)
@@ -64,14 +128,18 @@ class VerifyWorkspace:
         self.out = new(ncols, hidden)
         self.residual = new(ncols, hidden)
         self.logits = new(ncols, vocab)
+        self.token, self.logprob = new(ncols, dtype=torch.int32), new(ncols)
+        self.sample = new(ops.logits_sample_workspace_bytes(ncols, vocab), dtype=torch.uint8)
 
 
 def forward(x: torch.Tensor, residual: torch.Tensor, weights: VerifyWeights, ws: VerifyWorkspace, *,
-            eps: float = 1e-6, rules: dict | None = None) -> torch.Tensor:
+            eps: float = 1e-6, rules: dict | None = None, sampling: dict | None = None) -> torch.Tensor:
     """Enqueue one step's end on the current stream: x and residual [ncols,
     hidden] fp32 (the columns of a verify step, at most 8), rules the keyword
-    arguments of ops.logits_process.  Returns ws.logits [ncols, vocab]; the
-    residual stream after the block is in ws.residual."""
+    arguments of ops.logits_process, sampling those of ops.logits_sample (u among
+    them).  Returns ws.logits [ncols, vocab]; the residual stream after the block is
+    in ws.residual, drawn tokens and their log probabilities in ws.token and
+    ws.logprob."""
     w, c, topk = weights, ws.ncols, ws.topk
     e = w.experts
     if e.packed or e.fmt != "q8_0":
@@ -91,4 +159,6 @@ def forward(x: torch.Tensor, residual: torch.Tensor, weights: VerifyWeights, ws:
     ops.gemm_i8(ws.q, ws.scale, w.head.codes, w.head.scale, out=ws.logits)
     if rules:
         ops.logits_process(ws.logits, out=ws.logits, **rules)
+    if sampling:
+        ops.logits_sample(ws.logits, token=ws.token, logprob=ws.logprob, workspace=ws.sample, **sampling)
     return ws.logits

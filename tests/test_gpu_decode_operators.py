@@ -604,6 +604,87 @@ def test_graph_replays_and_streams_equal_eager():
         assert all(torch.equal(a, b) for a, b in zip(other, want)), i
 
 
+def test_verify_step_from_hidden_states_to_tokens():
+    """Two sequences of three columns, five steps: each stage against its numpy form on
+    what the stage before gave, and the whole as a graph."""
+    from quantized_moe_expert_q8_amd import moe_layer as ml, verify_step as vs
+    torch.manual_seed(3)
+    randn = lambda *s: torch.randn(s, device=DEV)
+    seqs, cols, hidden, inter, n_exp, vocab = 2, 3, 512, 256, 16, 1003
+    heads, kv, d, page = 6, 2, 80, 16
+    tokens = seqs * cols
+    dense = lambda n, k: vs.quantize_dense(randn(n, k) / k ** 0.5)
+
+    def experts(matrix, rows, k):
+        t = torch.empty(n_exp * rows * (k // 32) * moeq8.Q8_0_BLOCK_BYTES, dtype=torch.uint8, device=DEV)
+        return moeq8.synth_q8_0_fill(t, n_exp, rows * k // 32, n_exp, 1, 0, 0, matrix)
+
+    aw = vs.AttentionWeights(1 + 0.1 * randn(hidden), dense((heads + 2 * kv) * d, hidden), dense(hidden, heads * d), heads, kv, d)
+    w = vs.VerifyWeights(1 + 0.1 * randn(hidden), dense(n_exp, hidden), None,
+                         ml.RoutedExperts(experts(0, inter, hidden), experts(1, inter, hidden), experts(2, hidden, inter),
+                                          n_exp, hidden, inter), 1 + 0.1 * randn(hidden), dense(vocab, hidden))
+    aws, ws = vs.AttentionWorkspace(seqs, cols, aw, 128, DEV), vs.VerifyWorkspace(tokens, w, 4, DEV)
+    cache = moeq8.kv_cache_i8(16, kv, page, d, DEV)
+    table = torch.randperm(16, device=DEV).int().view(seqs, 8)
+    x, residual = randn(tokens, hidden), randn(tokens, hidden)
+    visible, slots = torch.zeros(seqs, cols, dtype=torch.int32, device=DEV), torch.zeros(tokens, dtype=torch.int64, device=DEV)
+    u = torch.zeros(tokens, device=DEV)
+    sampling = dict(u=u, temperature=torch.full((tokens,), 0.9, device=DEV), top_p=torch.full((tokens,), 0.9, device=DEV),
+                    top_k=torch.full((tokens,), 50, dtype=torch.int32, device=DEV))
+    turn = lambda q, k: (q.mul_(0.5), k.neg_())            # in place of positions
+
+    def step():
+        y, r = vs.attend(x, residual, aw, aws, cache, table, visible, slots, rotate=turn)
+        vs.forward(y, r, w, ws, sampling=sampling)
+
+    arrays = [t.cpu().numpy().copy() for t in cache]
+    graph = None
+    for i, lengths in enumerate(([0, 5], [3, 8], [6, 11], [9, 14], [12, 100])):
+        pos = torch.tensor(lengths)[:, None] + torch.arange(cols)
+        visible.copy_(pos + 1)
+        t = table.cpu().long()
+        slots.copy_((t.gather(1, pos // page) * page + pos % page).view(-1))
+        x.copy_(randn(tokens, hidden))
+        u.copy_(torch.rand(tokens, device=DEV))
+        step()
+        torch.cuda.synchronize()
+        q, k, v = aws.qkv.view(tokens, heads + 2 * kv, d).split([heads, kv, kv], dim=1)
+        ref.cache_write(arrays[0], arrays[1], k.cpu().numpy(), slots.tolist())
+        ref.cache_write(arrays[2], arrays[3], v.cpu().numpy(), slots.tolist())
+        assert all(same(a.cpu().numpy(), b) for a, b in zip(cache, arrays))
+        want, sizes = ref.attention(q.reshape(seqs, cols, heads, d).cpu().numpy(), *arrays, table.cpu().numpy(),
+                                    visible.cpu().numpy(), d ** -0.5)
+        err = np.abs(aws.attended.cpu().numpy() - want)
+        assert (err <= attention_bound(want, sizes, torch.float32, d)).all()
+        z = ws.logits.cpu().numpy()
+        for r in range(tokens):
+            token, log = ref.sample_row(z[r], float(u[r]), float(sampling["temperature"][r]), 50, float(sampling["top_p"][r]))
+            assert int(ws.token[r]) == token and abs(float(ws.logprob[r]) - log) <= 2.0**-23 * max(abs(log), 1e-7)
+        kept = [t.clone() for t in (aws.attended, aws.out, ws.logits, ws.token, ws.logprob, *cache)]
+        if graph is None:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step()
+        for t in (aws.attended, aws.out, ws.logits, ws.token):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, (aws.attended, aws.out, ws.logits, ws.token, ws.logprob, *cache))), i
+
+
+def test_example_runs():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, os.path.join(root, "examples", "verify_step.py"), "--vocab", "4096", "--experts", "16",
+                          "--hidden", "512", "--inter", "256", "--heads", "8", "--kv-heads", "2", "--head-dim", "64",
+                          "--history", "300"], capture_output=True, text=True, timeout=100)
+    assert out.returncode == 0, out.stderr[-2000:]
+    lines = [line for line in out.stdout.splitlines() if line.startswith("tokens")]
+    assert len(lines) == 2 and lines[0] == lines[1]
+
+
 def test_refusals():
     cache = moeq8.kv_cache_i8(4, 2, 16, 32, DEV)
     x, s = torch.zeros(3, 2, 32, device=DEV), torch.zeros(3, dtype=torch.int64, device=DEV)
