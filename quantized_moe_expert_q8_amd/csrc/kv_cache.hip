@@ -6,8 +6,10 @@
 // A row, one token's key or value of one head, belongs to the 2 to 32 lanes that
 // its vectors of 8 values take (a power of two, so that the maximum goes through
 // lanes in registers); a wave has as many rows as fit.  Both calls do nothing but
-// move bytes, so what bounds them is memory, and for a step's few tokens the
-// launch.
+// move bytes, so what bounds them is memory (65536 x 8 x 128 back to bf16 83 us, 4.9
+// TB/s, the rate of a large copy; writing 8192 x 8 x 128 bf16 12.8 us, 4.0 TB/s, with
+// the arithmetic of the codes beside it), and for a step's few tokens the launch (5 x
+// 8 x 128 f32 2.2 us in a graph).
 #include "moeq8_cache.hpp"
 
 namespace moeq8 {
@@ -62,15 +64,15 @@ __global__ __launch_bounds__(THREADS) void k_cache_write(RowsArgs a) {
     const T* x = row.value ? (const T*)a.v + row.token * a.v_token + row.head * a.v_head
                            : (const T*)a.k + row.token * a.k_token + row.head * a.k_head;
     T raw[VEC];
-    load_vec(raw, x + (at < a.c.d ? at : 0));
+    load_vec(raw, x + (at < a.c.d ? at : 0));     // the lanes past the row have its first vector again
     float y[VEC];
     uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        y[i] = to_f32(raw[i]);
-        m = larger(m, magnitude(y[i]));
+    for (int j = 0; j < VEC; ++j) {
+        y[j] = to_f32(raw[j]);
+        m = larger(m, magnitude(y[j]));
     }
-    m = lanes_max<LANES>(m);                      // the lanes past the row have its first vector again
+    m = lanes_max<LANES>(m);
     if (r >= a.rows || at >= a.c.d || (uint64_t)slot >= (uint64_t)a.c.n_pages << a.c.page_shift) return;
     const float d = __uint_as_float(m) / 127.0f;
     int sum;
@@ -82,38 +84,62 @@ __global__ __launch_bounds__(THREADS) void k_cache_write(RowsArgs a) {
         (row.value ? a.c.v_scale : a.c.k_scale)[page * a.c.scale_page_stride + row.head * a.c.scale_head_stride + place] = d;
 }
 
-template <typename T, int LANES>
+// A thread has PER rows, a grid apart, whose chains of loads and a store run side by
+// side.  The rows are written nontemporally: what reads them next does so from memory.
+template <typename T, int LANES, int PER>
 __global__ __launch_bounds__(THREADS) void k_cache_read(RowsArgs a) {
-    const uint32_t r = (blockIdx.x * THREADS + threadIdx.x) / LANES, at = (threadIdx.x & (LANES - 1)) * VEC;
-    if (r >= a.rows || at >= a.c.d) return;
-    const Row row = row_of(a, r);
-    const int64_t slot = a.slots[row.token];
-    T y[VEC];
-    if ((uint64_t)slot < (uint64_t)a.c.n_pages << a.c.page_shift) {
-        const int64_t page = slot >> a.c.page_shift, place = slot & ((1ll << a.c.page_shift) - 1);
-        const int8_t* p =
-            (row.value ? a.c.v : a.c.k) + page * a.c.page_stride + row.head * a.c.head_stride + place * a.c.token_stride;
-        const uint2 u = *reinterpret_cast<const uint2*>(p + at);
-        const float d =
-            (row.value ? a.c.v_scale : a.c.k_scale)[page * a.c.scale_page_stride + row.head * a.c.scale_head_stride + place];
+    const uint32_t first = (blockIdx.x * THREADS + threadIdx.x) / LANES, step = gridDim.x * (THREADS / LANES),
+                   at = (threadIdx.x & (LANES - 1)) * VEC;
+    if (at >= a.c.d) return;
+    Row row[PER];
+    int64_t slot[PER];
+    bool ok[PER];
+    uint2 u[PER];
+    float d[PER];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) from_f32(y[i], (float)(int8_t)((i < 4 ? u.x : u.y) >> (8 * (i & 3))) * d);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) from_f32(y[i], 0.0f);
+    for (int i = 0; i < PER; ++i) {
+        const uint32_t r = first + i * step;
+        row[i] = row_of(a, r < a.rows ? r : a.rows - 1);
+        slot[i] = a.slots[row[i].token];
+        ok[i] = (uint64_t)slot[i] < (uint64_t)a.c.n_pages << a.c.page_shift;
     }
-    T* o = row.value ? (T*)a.v + row.token * a.v_token + row.head * a.v_head
-                     : (T*)a.k + row.token * a.k_token + row.head * a.k_head;
-    store_vec(o + at, y);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {               // a slot outside the cache reads the first one
+        const int64_t in = ok[i] ? slot[i] : 0, page = in >> a.c.page_shift, place = in & ((1ll << a.c.page_shift) - 1);
+        const int8_t* p =
+            (row[i].value ? a.c.v : a.c.k) + page * a.c.page_stride + row[i].head * a.c.head_stride + place * a.c.token_stride;
+        u[i] = *reinterpret_cast<const uint2*>(p + at);
+        d[i] = (row[i].value ? a.c.v_scale : a.c.k_scale)[page * a.c.scale_page_stride + row[i].head * a.c.scale_head_stride + place];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (first + i * step >= a.rows) break;
+        T y[VEC];
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+            const float x = (float)(int8_t)((j < 4 ? u[i].x : u[i].y) >> (8 * (j & 3))) * d[i];
+            from_f32(y[j], ok[i] ? x : 0.0f);
+        }
+        T* o = row[i].value ? (T*)a.v + row[i].token * a.v_token + row[i].head * a.v_head
+                            : (T*)a.k + row[i].token * a.k_token + row[i].head * a.k_head;
+        store_vec<true>(o + at, y);
+    }
 }
 
 template <typename T, bool WRITE>
 int launch_rows(const RowsArgs& a, hipStream_t stream) {
     auto go = [&](auto lanes) {
         constexpr int L = decltype(lanes)::value;
-        const int64_t blocks = ((int64_t)a.rows * L + THREADS - 1) / THREADS;
+        constexpr int64_t PER_BLOCK = THREADS / L;
+        // Reading more rows than threads run at a time: four rows a thread (65536 x 8 x
+        // 128 to bf16 83 us, 4.9 TB/s, and 91 with one; with ordinary stores 88).
+        // Writing gained nothing from it (8192 x 8 x 128 bf16: 13.3 us and 12.8).
+        const bool many = !WRITE && a.rows >= 4 * 2048 * PER_BLOCK;
+        const int64_t blocks = (a.rows + (many ? 4 : 1) * PER_BLOCK - 1) / ((many ? 4 : 1) * PER_BLOCK);
         if (blocks > most_blocks(THREADS)) return (int)MOEQ8_EUNSUPPORTED;
-        auto kernel = WRITE ? k_cache_write<T, L> : k_cache_read<T, L>;
+        void (*kernel)(RowsArgs);
+        if constexpr (WRITE) kernel = k_cache_write<T, L>;
+        else kernel = many ? k_cache_read<T, L, 4> : k_cache_read<T, L, 1>;
         hipLaunchKernelGGL(kernel, dim3((uint32_t)blocks), dim3(THREADS), 0, stream, a);
         return check_launch();
     };
