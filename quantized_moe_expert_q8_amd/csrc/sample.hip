@@ -416,10 +416,9 @@ struct Lds {
     double table[PER_OCTAVE];
     uint64_t hist[256];
     uint64_t sums[WAVES];
-    uint64_t rest, pick_before, pick_unit;
+    uint64_t rest, pick_before;
     uint32_t words[2 * WAVES];
-    uint32_t pick_key, n, seg, hits, from, floor, least;
-    uint32_t limit;
+    uint32_t pick_key, n, seg, hits, from, least;
     uint64_t seg_sum[64];
     uint32_t top[MAX_SEGS];                       // the segments' largest keys
     uint16_t hit[MAX_SEGS];
@@ -472,32 +471,51 @@ __device__ __forceinline__ uint32_t digit_reaching(Lds& s, uint64_t want, uint64
 }
 
 // The key from which on, in falling order, the sum reaches `want` (or the last one),
-// and the sum before it.  each(f) calls f(key, amount) for this thread's part.
+// and the sum before it.  each(f) calls f(key, amount) for this thread's part.  Only
+// the bits in which the keys differ are gone through: a list's share most upper ones.
 template <typename E>
 __device__ __forceinline__ uint32_t select(Lds& s, uint64_t want, uint64_t& before, E each) {
-    uint32_t prefix = 0;
+    const uint32_t wave = threadIdx.x >> 6;
+    uint32_t any = 0, all = ~0u;
+    each([&](uint32_t key, uint64_t) {
+        any |= key;
+        all &= key;
+    });
+    any = wave_or(any);
+    all = wave_or(~all);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) {
+        s.words[wave] = any;
+        s.words[WAVES + wave] = all;
+    }
+    __syncthreads();
+    any = wave_or(s.words[threadIdx.x & (WAVES - 1)]);
+    all = ~wave_or(s.words[WAVES + (threadIdx.x & (WAVES - 1))]);
+    int left = 32 - __builtin_clz((any & ~all) | 1u);            // bits still open
+    uint32_t prefix = (uint32_t)((uint64_t)all >> left << left);
     before = 0;
 #pragma unroll 1
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        __syncthreads();
+    while (left > 0) {
+        const int from = left > 8 ? left - 8 : 0;
         if (threadIdx.x < 256) s.hist[threadIdx.x] = 0;
         __syncthreads();
         each([&](uint32_t key, uint64_t amount) {
-            if (shift == 24 || (key ^ prefix) >> (shift + 8) == 0)
-                atomicAdd((unsigned long long*)&s.hist[key >> shift & 255], (unsigned long long)amount);
+            if ((uint64_t)(key ^ prefix) >> left == 0)
+                atomicAdd((unsigned long long*)&s.hist[key >> from & 255], (unsigned long long)amount);
         });
         __syncthreads();
-        if (threadIdx.x < 64) {
+        if (wave == 0) {
             uint64_t at = before;
             const uint32_t digit = digit_reaching(s, want, at);
             if (threadIdx.x == 0) {
-                s.pick_key = prefix | digit << shift;
+                s.pick_key = prefix | digit << from;
                 s.pick_before = at;
             }
         }
         __syncthreads();
         prefix = s.pick_key;
         before = s.pick_before;
+        left = from;
     }
     return prefix;
 }
@@ -891,12 +909,13 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
         if (r.k) bin_count += a.bin_count[(row * a.tiles + t) * BINS + tid];
     }
     uint32_t held = ~0u;                          // the bin in the list
-    if (tid == 0) {
-        s.floor = 0;
-        s.limit = vocab;
-        s.pick_before = ~0ull;                    // the ties
-        s.n = 0;
-    }
+    uint32_t floor = 0, limit = vocab;
+    uint64_t ties = ~0ull, unit = 0;              // of the keys equal to `floor`, and the weight of each
+    auto shared = [&](auto f) {                   // the list by the block: here it has up to thousands
+#pragma unroll 1
+        for (uint32_t e = tid; e < s.n; e += THREADS) f(s.key[e], s.index[e], s.weight[e]);
+    };
+    if (tid == 0) s.n = 0;
     // top-k by the counts, then top-p by the masses, then min-p, whose bin the list has
     // to hold unless what it drops is in the last bin
 #pragma unroll 1
@@ -920,7 +939,7 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
             if (r.rest() && bin == BINS - 1) continue;           // min-p cuts above
         } else {
             __syncthreads();
-            if (s.least <= s.floor) continue;     // the others cut above
+            if (s.least <= floor) continue;       // the others cut above
             bin = (uint32_t)bin_of(w, logit_of(s.least));
         }
         if (bin != held) {
@@ -936,36 +955,56 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
             __syncthreads();
             if (!gather(s.from, s.pick_key)) return false;
         }
-        if (wave == 0) {
-            uint32_t floor = bin == held ? s.floor : 0;
-            uint64_t ties = bin == held ? s.pick_before : ~0ull, unit = bin == held ? s.pick_unit : 0, equal;
-            if (step == 0) cut_by_count(want, floor, ties, before);
-            else if (step == 1) cut_by_mass(want - before, floor, ties, unit);
-            else {
-                floor = s.least;                  // all that are equal to it
-                ties = ~0ull;
-            }
-            const uint64_t mass = mass_of(floor, equal, unit);
-            const uint32_t limit = last_tie(floor, ties, equal);
-            ties = ties < equal ? ties : equal;
-            if (lane == 0) {
-                s.floor = floor;
-                s.limit = limit;
-                s.pick_before = ties;
-                s.pick_unit = unit;
-                s.rest = mass + ties * unit;
-            }
+        const uint32_t old = bin == held ? floor : 0;
+        const uint64_t old_ties = ties, old_unit = bin == held ? unit : 0;
+        uint64_t in_bin;
+        if (step == 0) {
+            floor = select(s, want - before, in_bin, [&](auto add) { shared([&](uint32_t key, uint32_t, uint64_t) { add(key, 1); }); });
+            ties = want - before - in_bin;
+        } else if (step == 1) {
+            floor = select(s, want - before, in_bin, [&](auto add) {
+                shared([&](uint32_t key, uint32_t, uint64_t u) { if (key > old) add(key, u); });
+                if (old_unit && tid == 0) add(old, old_ties * old_unit);
+            });
+        } else {
+            floor = s.least;                      // all that are equal to it
+            ties = ~0ull;
+        }
+        uint64_t mass = 0, equal = 0;
+        shared([&](uint32_t key, uint32_t, uint64_t u) {
+            mass += key > floor ? u : 0;
+            equal += key == floor;
+        });
+        mass = block_sum(mass, s);
+        equal = block_sum(equal, s);
+        unit = equal ? w.units(logit_of(floor), a.bits) : 0;
+        if (step == 1) {
+            const uint64_t n = unit ? (want - before - in_bin + unit - 1) / unit : ~0ull;
+            ties = floor == old && old_ties < n ? old_ties : n;
+        }
+        limit = vocab;
+        if (ties < equal) {
+            uint64_t none;
+            limit = 0xffffffu - select(s, ties, none, [&](auto add) {
+                shared([&](uint32_t key, uint32_t i, uint64_t) { if (key == floor) add(0xffffffu - i, 1); });
+            });
+        } else {
+            ties = equal;
         }
         __syncthreads();
         held = bin;
+        const uint64_t left = mass + ties * unit;
         // the bins' masses without what is dropped
-        bin_mass = tid < bin ? bin_mass : (tid == bin ? s.rest : 0);
+        bin_mass = tid < bin ? bin_mass : (tid == bin ? left : 0);
     }
     __syncthreads();
     // where min-p cuts above the others: all that are equal to its key, of the bins all but the last
-    const bool by_least = r.rest() && s.least > s.floor;
-    const uint32_t floor = by_least ? s.least : s.floor, limit = by_least ? vocab : s.limit;
-    if (by_least) held = BINS - 1;
+    const bool by_least = r.rest() && s.least > floor;
+    if (by_least) {
+        floor = s.least;
+        limit = vocab;
+        held = BINS - 1;
+    }
     const float above = floor ? logit_of(floor) : -__builtin_inff();
     auto drawn = [&](float v, uint32_t i) -> uint64_t {
         return v > above || (floor && v == above && i <= limit) ? w.units(v, a.bits) : 0;
@@ -979,7 +1018,7 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
 #pragma unroll 4
         for (uint32_t b = lane; b < BINS; b += 64) sum += b < held ? a.bin_mass[(row * a.tiles + wave) * BINS + b] : 0;
         const uint32_t n = held == ~0u || by_least ? 0 : s.n, first = wave * a.tile_segs * SEG, past = first + a.tile_segs * SEG;
-#pragma unroll 1
+#pragma unroll 4
         for (uint32_t e = lane; e < n; e += 64) {
             const uint32_t key = s.key[e], i = s.index[e];
             if (i >= first && i < past && (key > floor || (key == floor && i <= limit))) sum += s.weight[e];
