@@ -732,40 +732,38 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
                 seg[i] = __builtin_amdgcn_readfirstlane(s.hit[h + i * WAVES < hits ? h + i * WAVES : h]);
                 e[i].load(z, seg[i], vocab);
             }
+            // A bit for each of the lane's candidates.  These are few and far between:
+            // each lane writes its own, and what is written is the index alone.
+            uint32_t in = 0;
 #pragma unroll
             for (uint32_t i = 0; i < AHEAD; ++i) {
-                if (h + i * WAVES >= hits) break;
                 float v[8];
                 e[i].values(v, seg[i], vocab);
-                uint64_t in[8];                   // lanes with a candidate
-                uint32_t n = 0;
+                if (h + i * WAVES >= hits) break;
 #pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) {
-                    in[j] = __ballot(v[j] >= least && v[j] < past);
-                    n += (uint32_t)__popcll(in[j]);
-                }
-                if (!n) continue;
-                uint32_t at = 0;
-                if (lane == 0) at = atomicAdd(&s.n, n);
-                at = __builtin_amdgcn_readfirstlane(at);
-#pragma unroll
-                for (uint32_t j = 0; j < 8; ++j) {
-                    if (in[j] >> lane & 1) {
-                        const uint32_t to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(in[j] >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)in[j], 0));
-                        if (to < CAP) {
-                            s.key[to] = key_of(v[j]);
-                            s.index[to] = e[i].first + j;
-                        }
-                    }
-                    at += (uint32_t)__popcll(in[j]);
-                }
+                for (uint32_t j = 0; j < 8; ++j) in |= v[j] >= least && v[j] < past ? 1u << (8 * i + j) : 0u;
+            }
+            if (!__any(in)) continue;
+            const uint32_t mine = (uint32_t)__builtin_popcount(in), up_to = wave_scan32(mine);
+            uint32_t at = 0;
+            if (lane == 63) at = atomicAdd(&s.n, up_to);
+            at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63) + up_to - mine;
+            for (; in; in &= in - 1, ++at) {
+                const uint32_t b = (uint32_t)__builtin_ctz(in), i = b / 8;
+                static_assert(AHEAD == 4, "the choice below");
+                const uint32_t first = i < 2 ? (i == 0 ? e[0].first : e[1].first) : (i == 2 ? e[2].first : e[3].first);
+                if (at < CAP) s.index[at] = first + b % 8;
             }
         }
         __syncthreads();
         const uint32_t n = s.n;
         if (n > CAP) return false;
 #pragma unroll 1
-        for (uint32_t e = tid; e < n; e += THREADS) s.weight[e] = w.units(logit_of(s.key[e]), a.bits);
+        for (uint32_t e = tid; e < n; e += THREADS) {
+            const float v = to_f32(z[s.index[e]]);
+            s.key[e] = key_of(v);
+            s.weight[e] = w.units(v, a.bits);
+        }
         __syncthreads();
         return true;
     };
