@@ -164,7 +164,7 @@ struct Eight {
     uint32_t first;
     __device__ __forceinline__ void load(const T* z, uint32_t seg, uint32_t vocab) {
         const uint32_t at = seg * SEG + (threadIdx.x & 63) * 8;
-        first = at + 8 <= vocab ? at : vocab - 8;
+        first = at <= vocab - 8 ? at : vocab - 8;  // in bounds for any seg, whatever a shared workspace held
         if (vocab >= 8) {
             load_vec(raw, z + first);
         } else {
@@ -885,12 +885,13 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
         total = wave_sum(total);
         uint64_t target = (uint64_t)((double)uf * (double)total);
         if (target >= total) target = total - 1;
-        const uint32_t token = 0xffffffu - wave_select(s, target + 1, before, [&](auto add) {
+        uint32_t token = 0xffffffu - wave_select(s, target + 1, before, [&](auto add) {
             listed([&](uint32_t key, uint32_t i, uint64_t u) {
                 const uint64_t d = drawn(key, i, u);
                 if (d) add(0xffffffu - i, d);
             });
         });
+        token = token < vocab ? token : vocab - 1;
         if (lane == 0) {
             a.token[row] = (int32_t)token;
             if (a.logprob)
