@@ -644,7 +644,8 @@ typedef struct moeq8_kv_cache {
  *   k, v   dtype [n_tokens][n_heads][d], at token and head strides in elements
  *   slots  int64 [n_tokens]; a token whose slot is outside the cache is skipped
  * A slot that comes twice holds bytes of either token.  The cache must not
- * overlap k and v.  `cache` is read on the host, during the call. */
+ * overlap k and v, nor its keys its values.  `cache` is read on the host, during
+ * the call. */
 int kv_cache_write_i8(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
                       int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
                       const int64_t* slots, const moeq8_kv_cache* cache, void* stream);
@@ -673,7 +674,7 @@ int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t 
  *             close bound is faster.  The results' roundings depend on it too.
  *   scale     finite; the inner products' factor (commonly d^-0.5)
  * n_q_heads is a multiple of n_heads, 1 <= n_cols <= MOEQ8_MAX_COLS, max_visible <
- * 2^30.  Scores and sums are fp32; fp32 queries and the weights of fp32 and fp16
+ * 2^30, token_stride <= 2^26.  Scores and sums are fp32; fp32 queries and the weights of fp32 and fp16
  * outputs go through the matrix cores as two fp16 parts (22 bits), bf16 outputs'
  * weights as one (11 bits).  Codes outside of what is seen do not matter, nor do
  * their scales; a scale or query that is not finite follows IEEE arithmetic in the

@@ -159,6 +159,8 @@ int cache_rows(const void* k, int64_t k_token, int64_t k_head, const void* v, in
     if (const int s = check_cache(cache, a.c)) return s;
     if (n_tokens == 0) return MOEQ8_OK;
     if (!k || !v || !slots) return MOEQ8_EINVAL;
+    // one array for both: a race of the rows written
+    if (WRITE ? a.c.k == a.c.v || a.c.k_scale == a.c.v_scale : k == v) return MOEQ8_EINVAL;
     const int64_t heads = a.c.n_heads, d = a.c.d, es = dtype_bytes(dtype);
     for (const int64_t s : {k_head, v_head})
         if (heads > 1 && s < d) return MOEQ8_EINVAL;

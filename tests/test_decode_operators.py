@@ -111,6 +111,9 @@ def test_cache_rows_validation():
     assert write(k=Q + 2) == write(v=R + 1, dt=2) == write(slots=S + 4) == -2
     assert write(k=P + 16) == write(v=P + 0x300000 - 64) == -1                   # over the cache
     assert write(n=1 << 30) == -3
+    assert L.kv_cache_write_i8(Q, 64, 32, R, 64, 32, 0, 3, S, cache(v=P), None) == -1             # values over keys
+    assert L.kv_cache_write_i8(Q, 64, 32, R, 64, 32, 0, 3, S, cache(v_scale=P + 0x100000), None) == -1
+    assert L.kv_cache_read_i8(cache(), S, 3, 0, Q, 64, 32, Q, 64, 32, None) == -1
     assert write(n=0) == write(n=0, k=None, v=None, slots=None) == 0
     assert L.kv_cache_write_i8(Q, 64, 32, R, 64, 32, 0, 3, S, None, None) == -1
 
@@ -132,6 +135,7 @@ def test_attention_validation():
     assert call(out=Q) == call(out=Q + 512) == call(out=P) == -1                  # over q, over the cache
     assert call(q=Q + 2) == call(out=R + 1, dt=1) == call(pages=S + 2) == call(vis=S + 1) == -2
     assert call(most=1 << 30) == -3
+    assert call(c=cache(token_stride=1 << 27, head_stride=1 << 31, page_stride=1 << 33)) == -3
     assert call(seqs=0) == 0
     need = L.paged_attention_workspace_bytes(2, 1, 4, 2, 32, 1 << 16)
     assert need > 0 and L.paged_attention_workspace_bytes(2, 1, 4, 2, 32, 64) == 0

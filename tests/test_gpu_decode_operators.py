@@ -544,6 +544,48 @@ def test_sample_broad_distributions(rules, dtype):
     check_sample(z, u, TYPES[dtype], **rules)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sample_few_segments_with_a_logit(dtype):
+    """A grammar that leaves a stretch of the vocabulary: fewer segments than k."""
+    z, u = some_logits(4, 60011, 32, 1.0)
+    z[0, 5000:] = -np.inf
+    z[1, :40000] = -np.inf
+    z[1, 52000:] = -np.inf
+    z[2, 600:59990] = -np.inf
+    for rules in (dict(top_k=50), dict(top_k=20, top_p=0.9), dict(top_k=50, top_p=0.8, min_p=0.05), dict(top_p=0.9), dict()):
+        check_sample(z, u, TYPES[dtype], **rules)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_sample_vocabulary_past_the_segments(dtype):
+    z, u = some_logits(2, 530001, 33, 1.5)
+    z[1] = np.round(z[1])
+    for rules in (dict(), dict(top_k=40, top_p=0.9), dict(top_p=0.5), dict(min_p=0.1), dict(temperature=0.0)):
+        check_sample(z, u, TYPES[dtype], **rules)
+
+
+def test_sample_largest_vocabulary_of_the_segments():
+    z, u = some_logits(1, 524288, 34, 1.5)
+    for rules in (dict(), dict(top_k=600), dict(top_k=900, top_p=0.9), dict(top_p=0.7)):
+        check_sample(z, u, torch.bfloat16, **rules)
+
+
+def test_sample_many_rows():
+    """More rows than run at a time, with as many rules: all like each row alone."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    rand = lambda *s: torch.rand(s, generator=g, device=DEV)
+    rows, vocab = 1500, 5000
+    z = (2 * torch.randn(rows, vocab, generator=g, device=DEV)).to(torch.bfloat16)
+    u = rand(rows)
+    rules = dict(temperature=0.3 + rand(rows), top_k=(rand(rows) * 60 - 20).int(), top_p=0.3 + rand(rows), min_p=0.2 * rand(rows) - 0.1)
+    token, logprob = moeq8.logits_sample(z, u, **rules)
+    for r in (0, 1, 700, 1023, 1024, 1499):
+        t, l = moeq8.logits_sample(z[r:r + 1], u[r:r + 1], **{k: v[r:r + 1].contiguous() for k, v in rules.items()})
+        assert torch.equal(t, token[r:r + 1]) and torch.equal(l, logprob[r:r + 1])
+        want, _ = ref.sample_row(z[r].float().cpu().numpy(), float(u[r]), *(rules[k][r].item() for k in ("temperature", "top_k", "top_p", "min_p")))
+        assert int(token[r]) == want
+
+
 def test_sample_frequencies_follow_the_weights():
     """Equally spaced numbers draw each token as often as its weight says, to one each side."""
     z = np.log([4.0, 1.0, 0.0 + 1e-30, 3.0, 2.0])
