@@ -213,42 +213,42 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
     for (int c = 0; c < NC; ++c) k_at[c] = n * stride + (64u * c + 16u * g < a.c.d ? 64u * c + 16u * g : 0u);
     const uint32_t v_at = 4 * g * stride + ((uint32_t)(DV * n) < a.c.d ? DV * n : 0u);
 
-    // a tile: its pages and, of K and V, the operands and scales
+    // a tile: where its two rows of 16 positions lie, and, of K and V, the operands and scales
     struct Place {
-        uint32_t page[2];
+        int64_t row[2], scale[2];
         bool ok[2];
     };
+    const int64_t head_row = head * a.c.head_stride, head_scale = head * a.c.scale_head_stride;
     auto place_of = [&](uint32_t at, uint32_t from) {
         Place p;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            p.page[h] = (uint32_t)__builtin_amdgcn_readlane((int)page, (int)((at - from) / 16 + h));
-            p.ok[h] = p.page[h] < a.c.n_pages;
-            p.page[h] = p.ok[h] ? p.page[h] : 0u;
+            uint32_t n = (uint32_t)__builtin_amdgcn_readlane((int)page, (int)((at - from) / 16 + h));
+            p.ok[h] = n < a.c.n_pages;
+            n = p.ok[h] ? n : 0u;
+            const uint32_t place = (at + 16 * h) & in_page;
+            p.row[h] = n * a.c.page_stride + head_row + (int64_t)place * stride;
+            p.scale[h] = n * a.c.scale_page_stride + head_scale + place;
         }
         return p;
     };
     u32x4 kq[2][NC];
     uint32_t vq[8][NC];
     f32x4 kd[2], vd[2];
-    auto load_k = [&](uint32_t at, const Place& p) {
+    auto load_k = [&](const Place& p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t place = (at + 16 * h) & in_page;
-            const int8_t* k = a.c.k + (p.page[h] * a.c.page_stride + head * a.c.head_stride + place * a.c.token_stride);
+            const int8_t* k = a.c.k + p.row[h];
 #pragma unroll
             for (int c = 0; c < NC; ++c) kq[h][c] = *reinterpret_cast<const u32x4*>(k + k_at[c]);
-            const float* d = a.c.k_scale + (p.page[h] * a.c.scale_page_stride + head * a.c.scale_head_stride + place);
-            kd[h] = *reinterpret_cast<const f32x4*>(d + 4u * g);
+            kd[h] = *reinterpret_cast<const f32x4*>(a.c.k_scale + p.scale[h] + 4u * g);
         }
     };
-    auto load_v = [&](uint32_t at, const Place& p) {
+    auto load_v = [&](const Place& p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t place = (at + 16 * h) & in_page;
-            const int8_t* v = a.c.v + (p.page[h] * a.c.page_stride + head * a.c.head_stride + place * a.c.token_stride);
-            const float* d = a.c.v_scale + (p.page[h] * a.c.scale_page_stride + head * a.c.scale_head_stride + place);
-            vd[h] = *reinterpret_cast<const f32x4*>(d + 4u * g);
+            const int8_t* v = a.c.v + p.row[h];
+            vd[h] = *reinterpret_cast<const f32x4*>(a.c.v_scale + p.scale[h] + 4u * g);
 #pragma unroll
             for (int j = 0; j < 4; ++j, v += stride) {
                 if constexpr (NC == 1) {
@@ -280,8 +280,8 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
     // the first tile is on its way while the queries are written
     Place here = place_of(begin + TILE * wave, begin);
     if (begin + TILE * wave < end) {
-        load_k(begin + TILE * wave, here);
-        load_v(begin + TILE * wave, here);
+        load_k(here);
+        load_v(here);
     }
     lds_barrier();
     float factor[NT];
@@ -300,8 +300,8 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
             page = page_of(from);
             here = place_of(from + TILE * wave, from);
             if (from + TILE * wave < to) {
-                load_k(from + TILE * wave, here);
-                load_v(from + TILE * wave, here);
+                load_k(here);
+                load_v(here);
             }
         }
         for (uint32_t at = from + TILE * wave; at < to; at += TILE * waves) {
@@ -341,7 +341,7 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[t][i] = s[t][i / 4][i % 4] * kd[i / 4][i % 4];
-            load_k(next, then);                   // K's registers are free again
+            load_k(then);                         // K's registers are free again
 
             float ve[8];                          // the value scales, past the length 0, whatever is there
 #pragma unroll
@@ -441,7 +441,7 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
                             o[t][4 * d4 + i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[p][t], o[t][4 * d4 + i], 0, 0, 0);
                 }
             }
-            load_v(next, then);
+            load_v(then);
             here = then;
         }
     }
@@ -592,12 +592,21 @@ Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_
     p.tiles = (int)std::min(tiles, most);
     p.parts = (tiles + p.tiles - 1) / p.tiles;
     const int64_t pairs = seqs * heads * p.parts;
-        const int64_t fill = 768;
-    p.waves = p.chunks * p.tiles > 4 || pairs * ((limit + 1023) / 1024) >= fill ? 4 : 8;
+        // Blocks of 8 waves where one a CU is all there is, and of 4 where several fit and
+    // the loads of one go on under the ends of another: from two pairs a CU (64 x 1 x 500
+    // bf16, 8 key heads of 128: 15 us, with 8 waves 19) or 768 spans of 1024 positions on
+    // (64 x 1 x 8192: 142 us; but 32 x 1 x 2000 25 with 8 and 29 with 4), and for row
+    // tiles whose registers leave room for one wave a SIMD.
+    p.waves = p.chunks * p.tiles > 4 || pairs >= 512 || pairs * ((limit + 1023) / 1024) >= 768 ? 4 : 8;
     if (p.waves == 8) {
+        // a block for each of 256 CUs, of at least one round of its waves' tiles (1 x 1 x
+        // 1500: 9.1 us, with spans of 512 10.7); two rounds are no longer than the join
+        // (1 x 1 x 300: 7.0 us, split 9.0)
         const int64_t want = std::max<int64_t>(1, 256 / pairs);
-        p.span = limit <= 1024 ? 1024 : std::max<int64_t>(512, ((limit + want - 1) / want + 255) / 256 * 256);
+        p.span = limit <= 512 ? 512 : std::max<int64_t>(256, ((limit + want - 1) / want + 255) / 256 * 256);
     } else {
+        // 8 blocks a CU, so that short and long sequences even out (64 x 1 x 8192, from a
+        // quarter of that on: spans of 512 154 us, 1024 and 2048 142, 4096 149)
         const int64_t want = std::max<int64_t>(1, 2048 / pairs);
         p.span = std::max<int64_t>(512, ((limit + want - 1) / want + 127) / 128 * 128);
     }
