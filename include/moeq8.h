@@ -708,8 +708,10 @@ int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q_col_stride
  *   logprob      fp32 [n_rows] or NULL: log(w / kept mass) of the token drawn; -inf
  *                for a row without
  * A temperature that is negative or NaN counts as 0; a NaN of the others, or of u,
- * as their NULL or 0.  Weights are held to 2^-63 of the row's largest sum, and sums
- * are exact, so a result does not depend on the number of rows or on the form taken.
+ * as their NULL or 0.  Sums are exact, of weights rounded to 2^-S, with S from 33 to
+ * 51 as a row's sum stays below 2^63; a row without top-k, top-p and min-p takes its
+ * draw over sums of 512 logits, joined in 64-bit floats in the order of the indexes.
+ * A result does not depend on the number of rows or on their other arguments.
  * vocab < 2^30.
  *   workspace  at least logits_sample_workspace_bytes() bytes, 16-byte aligned, as
  *             above. */

@@ -31,6 +31,17 @@
 //
 // Spans: one sequence and key head rarely fill the card, so positions are split
 // over blocks; each writes its rows' sums, maximum and total, and k_join adds them.
+//
+// What bounds it: for large batches memory (64 sequences of 2048 to 8192 positions, 8
+// key heads of 128, bf16: 142 us and 5 for the join, 4.9 TB/s; a wave keeps one tile
+// of 8.4 KB on its way while it works on another).  For one sequence in a long context a
+// block's start and end, about 5 of 18 us, around the reading (5 columns, 32768
+// positions: 18 + 4 us).  For short ones the chain of loads and of the join (777
+// positions 9.0 us in a graph).  With more than 16 rows or fp32 the arithmetic: a tile
+// of 32 positions takes 350 vector instructions for d = 128 and one row tile, half of
+// them the conversion of its codes, which the rows of a wave share (16 x 8 x 4096, d =
+// 256, 64 rows in 4 parts, f32: 36 us).  Row tiles of 16 for d > 128: two of them left
+// registers for one wave a SIMD (51 us).
 #include "moeq8_cache.hpp"
 #include "moeq8_lds.hpp"
 
@@ -139,7 +150,7 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
     // Units of work, a span of a sequence for a key head: heads fastest, then the
     // sequence, the span slowest.  Blocks go to the 8 XCDs in turn: with the spans
     // fastest, the XCDs that got short sequences' last spans had nothing to do (64 x 1 x
-    // 8192: 170 and 143 us).  The blocks of a unit that have different rows are 8 apart,
+    // 8192: 171 and 149 us).  The blocks of a unit that have different rows are 8 apart,
     // and find its keys and values in their XCD's L2.
     const uint32_t eight = blockIdx.x / 8, part = eight % a.parts;
     uint32_t id = eight / a.parts * 8 + blockIdx.x % 8;
@@ -307,7 +318,7 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
         for (uint32_t at = from + TILE * wave; at < to; at += TILE * waves) {
             // the next tile's loads are issued whether there is one or not (then this one's
             // again): under a branch, what is waited for before would be unknown, and
-            // every wait would be for all of them (64 x 1 x 8192: 157 us and not 187)
+            // every wait would be for all of them (64 x 1 x 8192: 187 us and not 171)
             const uint32_t next = at + TILE * waves < to ? at + TILE * waves : at;
             const Place then = place_of(next, from);
 

@@ -19,10 +19,19 @@
 //
 // Candidates: for top-k the logits from the k-th largest of the segments' largest
 // keys on, found in the k segments that have them; for min-p the segments whose
-// largest passes it; else the bin that the threshold falls into.  The draw takes the
-// segment first, then its logits in order.  Rows with more candidates than LDS holds
+// largest passes it; else the bin that the threshold falls into.  Among bins the draw
+// takes a tile of k_bins first, then a segment, then its logits in order; in a list it
+// is one more selection, over the indexes.  Rows with more candidates than LDS holds
 // (equal logits by the thousand), with infinite logits, or of over 524288 logits go
-// the slow way: selections over the whole row.
+// the slow way: selections over the whole row, some 100 us for 131072 logits.
+//
+// What bounds it: for few rows the chain of three launches and of a block's
+// dependent steps (1 x 32000 f32 with top-k 16 us: 4 + 3 + 10; 5 x 131072 with top-p
+// and min-p 21), in which instructions that run once are fetched from memory: code
+// that is not unrolled is faster here.  For many rows k_scan is bound by memory (256 x
+// 131072 bf16 with top-k 13.9 us, 4.8 TB/s; 42 where every row needs its masses, by
+// the arithmetic of 64 bits) and k_pick by what one CU issues for one row: 19 us with
+// top-k = 50, 38 with rules of all kinds, 56 with top-p alone on normal logits.
 #include "moeq8_cache.hpp"
 #include "moeq8_lds.hpp"
 
@@ -34,7 +43,6 @@ constexpr int MAX_SEGS = 1024;                    // more: the slow way
 constexpr int BINS = 1024, PER_OCTAVE = 64;       // steps of the exponent's table; a bin is 4 of them
 constexpr int CAP = 4096;                         // candidates that k_pick holds
 constexpr int THREADS = 1024, WAVES = THREADS / 64;
-constexpr int FEW_HITS = 96;                      // segments that pass min-p: candidates at once
 
 struct SampleArgs {
     const void* z; int64_t z_stride;
@@ -78,8 +86,9 @@ struct Rules {
 };
 __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int64_t row) {
     Rules r;
-    // a rule that is left out reads u's bits instead: loads under a branch each would
-    // be waited for one after another (2 us of the 20 that a row took)
+    // a rule that is left out reads u's bits instead: loads under a branch each are
+    // waited for one after another (what comes before a row's first decision took 5.7
+    // us with them and a computed table of powers, and takes 1.5)
     const float* none = a.u;
     float t = (a.temperature ? a.temperature : none)[row], p = (a.top_p ? a.top_p : none)[row], least = (a.min_p ? a.min_p : none)[row];
     const int32_t k = (a.top_k ? a.top_k : (const int32_t*)none)[row];
@@ -131,8 +140,7 @@ __device__ __forceinline__ int bin_of(int i) {    // i <= 0
 }
 __device__ __forceinline__ int bin_of(const Weigh& w, float z) { return bin_of((int)rint(w.steps(z))); }
 
-// 2^(j / 64), correctly rounded.  From memory into LDS: a kernel that computed them
-// spent half a microsecond on that.
+// 2^(j / 64), correctly rounded.
 __device__ const double POWERS[PER_OCTAVE] = {
     0x1.0000000000000p+0, 0x1.02c9a3e778061p+0, 0x1.059b0d3158574p+0, 0x1.0874518759bc8p+0,
     0x1.0b5586cf9890fp+0, 0x1.0e3ec32d3d1a2p+0, 0x1.11301d0125b51p+0, 0x1.1429aaea92de0p+0,
@@ -349,8 +357,16 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, const Rules& r, int64
     else if (o.top == KEY_INF) o.way = SLOW;
     else if (r.pure()) o.way = PURE;
     else if (segs <= CAP / SEG) o.way = LIST;
+    // A list costs by its candidates, bins the same for all (8 x 131072 f32, 256 segments,
+    // normal logits, list and bins: k = 20 19 and 32 us, 150 24 and 34, 250 40 and 36; 16 x
+    // 32000, 63 segments, k = 60 21 and 29).  Of many segments a k near their number
+    // would bring more candidates than the list holds.  Of min-p's candidates their number
+    // is estimated from the segments without one, exp(-candidates / segments) of all;
+    // up to 1024 make a list (min_p = 0.1 19 and 28 us, 0.05 25 and 28, 0.02 40 and 29; 64 x
+    // 131072 bf16 24 and 54, 33 and 54, 56 and 54; 16 x 32000 14, 16 and 23 us, and 21).
     else if (r.k) o.way = r.k <= (segs <= 256 ? segs : segs * 3 / 4) ? LIST : BY_BINS;
-    else if (r.least > 0.0f && hits <= FEW_HITS) o.way = LIST;
+    else if (r.least > 0.0f &&
+             segs - hits + 0.5f >= segs * __expf(-1024.0f / segs)) o.way = LIST;
     else o.way = BY_BINS;
     return o;
 }
@@ -520,8 +536,7 @@ __device__ __forceinline__ uint32_t select(Lds& s, uint64_t want, uint64_t& befo
     return prefix;
 }
 
-// The same by one wave, which needs no barriers: a list of a few hundred takes half a
-// microsecond where the block takes five.
+// The same by one wave, which needs no barriers: for lists of a few hundred.
 template <typename E>
 __device__ __forceinline__ uint32_t wave_select(Lds& s, uint64_t want, uint64_t& before, E each) {
     const uint32_t lane = threadIdx.x & 63;
