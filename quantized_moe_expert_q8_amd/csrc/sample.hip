@@ -26,8 +26,8 @@
 // the slow way: selections over the whole row, some 100 us for 131072 logits.
 //
 // What bounds it: for few rows the chain of three launches and of a block's
-// dependent steps (1 x 32000 f32 with top-k 16 us: 4 + 3 + 10; 5 x 131072 with top-p
-// and min-p 21), in which instructions that run once are fetched from memory: code
+// dependent steps (1 x 32000 f32 with top-k, and 5 x 131072 with top-p and min-p, 16
+// us in a graph: 4 + 3 + 10), in which instructions that run once are fetched from memory: code
 // that is not unrolled is faster here.  For many rows k_scan is bound by memory (256 x
 // 131072 bf16 with top-k 13.9 us, 4.8 TB/s; 42 where every row needs its masses, by
 // the arithmetic of 64 bits) and k_pick by what one CU issues for one row: 19 us with
