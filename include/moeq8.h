@@ -680,8 +680,9 @@ int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t 
  * their scales; a scale or query that is not finite follows IEEE arithmetic in the
  * rows that see it and touches no others (infinite sums may come out as NaN).
  *   workspace  at least paged_attention_workspace_bytes() bytes, 16-byte aligned
- *             (NULL where that is 0).  It holds nothing between calls; calls that
- *             may run at the same time need one each.
+ *             (NULL where that is 0), that overlap no other argument.  It holds
+ *             nothing between calls; calls that may run at the same time need one
+ *             each.
  * paged_attention_workspace_bytes: 0 also for arguments that the call refuses. */
 size_t paged_attention_workspace_bytes(int64_t n_seqs, int64_t n_cols, int64_t n_q_heads, int64_t n_heads, int64_t d,
                                        int64_t max_visible);
@@ -714,7 +715,8 @@ int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q_col_stride
  * A result does not depend on the number of rows or on their other arguments.
  * vocab < 2^30.
  *   workspace  at least logits_sample_workspace_bytes() bytes, 16-byte aligned, as
- *             above. */
+ *             above.
+ * Token, logprob and the workspace must not overlap each other or what is read. */
 size_t logits_sample_workspace_bytes(int64_t n_rows, int64_t vocab);
 int logits_sample(const void* logits, int64_t logits_row_stride, int32_t dtype, int64_t n_rows, int64_t vocab,
                   const float* u, const float* temperature, const int32_t* top_k, const float* top_p,

@@ -603,7 +603,7 @@ Plan plan_for(int64_t seqs, int64_t cols, int64_t q_heads, int64_t heads, int64_
     p.tiles = (int)std::min(tiles, most);
     p.parts = (tiles + p.tiles - 1) / p.tiles;
     const int64_t pairs = seqs * heads * p.parts;
-        // Blocks of 8 waves where one a CU is all there is, and of 4 where several fit and
+    // Blocks of 8 waves where one a CU is all there is, and of 4 where several fit and
     // the loads of one go on under the ends of another: from two pairs a CU (64 x 1 x 500
     // bf16, 8 key heads of 128: 15 us, with 8 waves 19) or 768 spans of 1024 positions on
     // (64 x 1 x 8192: 142 us; but 32 x 1 x 2000 25 with 8 and 29 with 4), and for row
@@ -651,7 +651,6 @@ int attend(const AttendArgs& a, const Plan& p, hipStream_t stream) {
         case 10: s = launch_attend<T, 2, 2>(a, p, stream); break;
         case 11: s = launch_attend<T, 2, 3>(a, p, stream); break;
         default: s = launch_attend<T, 4, 1>(a, p, stream); break;
-
     }
     if (s != MOEQ8_OK || p.spans == 1) return s;
     const uint32_t rows = (uint32_t)((int64_t)a.seqs * a.c.n_heads * a.rows), vecs = a.c.d / 4;
@@ -720,6 +719,10 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
     if (p.blocks > most_blocks(p.waves * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MOEQ8_EINVAL;
     if (p.bytes && (uintptr_t)workspace & 15u) return MOEQ8_EALIGN;
+    const int64_t ws_bytes = (int64_t)p.bytes;
+    if (p.bytes && (ranges_overlap(workspace, ws_bytes, q, bytes[0]) || ranges_overlap(workspace, ws_bytes, out, bytes[1]) ||
+                    clashes_with_cache(a.c, workspace, ws_bytes)))
+        return MOEQ8_EINVAL;
     a.q = q; a.q_seq = q_seq_stride; a.q_col = q_col_stride; a.q_head = q_head_stride;
     a.out = out; a.o_seq = out_seq_stride; a.o_col = out_col_stride; a.o_head = out_head_stride;
     a.pages = pages; a.pages_row = pages_row_stride;

@@ -1247,6 +1247,15 @@ extern "C" int logits_sample(const void* logits, int64_t logits_row_stride, int3
     const Plan p = plan_for(n_rows, vocab);
     if (p.bytes && (!workspace || workspace_bytes < (size_t)p.bytes)) return MOEQ8_EINVAL;
     if (p.bytes && (uintptr_t)workspace & 15u) return MOEQ8_EALIGN;
+    // what is written lies apart from itself and from what other blocks still read
+    const int64_t z_bytes = ((n_rows - 1) * logits_row_stride + vocab) * es, n_bytes = 4 * n_rows;
+    const struct { const void* p; int64_t bytes; } all[] = {
+        {workspace, p.bytes}, {token, n_bytes}, {logprob, n_bytes}, {logits, z_bytes}, {u, n_bytes},
+        {temperature, n_bytes}, {top_k, n_bytes}, {top_p, n_bytes}, {min_p, n_bytes}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 9; ++j)
+            if (all[i].p && all[j].p && all[i].bytes && ranges_overlap(all[i].p, all[i].bytes, all[j].p, all[j].bytes))
+                return MOEQ8_EINVAL;
     int bits = 51;
     while (vocab > (1ll << (63 - bits))) --bits;
     uint8_t* ws = (uint8_t*)workspace;

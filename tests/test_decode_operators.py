@@ -163,6 +163,29 @@ def test_sample_validation():
     assert call(rows=0) == 0
 
 
+@cpu_only
+def test_written_arrays_lie_apart():
+    L = moeq8.lib()
+    W = 0x50000000
+    need = L.logits_sample_workspace_bytes(2, 1000)
+
+    def sample(z=Q, rows=2, u=P, k=P + 64, token=R, log=R + 64, ws=W):
+        return L.logits_sample(z, 1000, 0, rows, 1000, u, None, k, None, None, token, log, ws, need, None)
+
+    assert sample(token=Q) == sample(token=Q + 7996) == sample(log=Q + 400) == -1             # in the logits
+    assert sample(token=P) == sample(log=P + 68) == sample(u=R + 4) == sample(k=W + 16) == -1
+    assert sample(log=R) == sample(log=R + 4) == sample(token=W) == sample(log=W + need - 4) == -1
+    assert sample(z=W + need - 16) == sample(ws=Q) == sample(ws=Q - need + 16 * (need % 16 == 0)) == -1
+
+    bytes_ = L.paged_attention_workspace_bytes(2, 1, 4, 2, 32, 1 << 16)
+
+    def attend(ws):
+        return L.paged_attention_i8(Q, 128, 128, 32, 0, 2, 1, 4, cache(), S, 1 << 12, 1 << 12, S, 1 << 16, 1.0, R, 128,
+                                    128, 32, ws, bytes_, None)
+
+    assert attend(Q) == attend(R) == attend(R + 1008) == attend(P) == -1
+
+
 def test_ops_refuse_host_tensors():
     c = ops.kv_cache_i8(2, 2, 16, 32, "cpu")
     x, s = torch.zeros(3, 2, 32), torch.zeros(3, dtype=torch.int64)
