@@ -25,11 +25,15 @@
 // fp16 operands: a row of q is scaled by a power of two to a largest value in
 // [2^13, 2^14), so what its smallest values lose is below 2^-38 of the largest; fp32
 // rows go as two parts (22 bits), and bf16 and fp16 rows are exact in one.  The
-// weights e^(t - m) vd are scaled by a power of two that keeps the largest vd's
-// below 2^14, and go as two parts whatever the outputs' type.  (One part for
-// bf16 outputs, 11 bits, gave 1 to 4 of 100 values as the neighbours of the right ones;
-// the second costs 0.2 of 9.7 us for 777 positions, 0.6 of 20.7 for 5 columns of 32768
-// and nothing for a batch at the rate of memory.)
+// weights e^(t - m) vd of a row are scaled by the power of two that brings the
+// largest of them so far to [2^12, 2^15), so what each loses is below 2^-37 of the
+// largest.  (The largest vd would not do: that of a position of next to no weight
+// pushed the others below fp16.  It is a number for each row and not for all, which
+// costs 1.1 of 22.2 us where a wave has few tiles and two row tiles, 37 x 5 x 1500,
+// and nothing elsewhere.)  They go as two parts whatever the outputs' type.
+// (One part for bf16 outputs, 11 bits, gave 1 to 4 of 100 values as the neighbours of
+// the right ones; the second costs 0.2 of 9.7 us for 777 positions, 0.6 of 20.7 for 5
+// columns of 32768 and nothing for a batch at the rate of memory.)
 //
 // Spans: one sequence and key head rarely fill the card, so positions are split
 // over blocks; each writes its rows' sums, maximum and total, and k_join adds them.
@@ -59,7 +63,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TILE = 32, SEGMENT = 1024;          // positions a tile; positions whose pages a wave holds at a time
-constexpr int WEIGHT_BITS = 13;                   // weights stay below 2^14
+constexpr int WEIGHT_BITS = 12;                   // the largest weight of a row comes to [2^12, 2^13), and may grow to 2^15
 
 struct AttendArgs {
     const void* q; int64_t q_seq, q_col, q_head;
@@ -100,6 +104,13 @@ __device__ __forceinline__ float quad_sum(float v) {
     v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
     const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// The power of two that weights are scaled by, for their largest so far.  For one below
+// 2^-115 it stays: the last place in fp16 is then below that of fp32.
+__device__ __forceinline__ int up_for(float peak) {
+    const int up = 127 + WEIGHT_BITS - (int)(__float_as_uint(peak) >> 23);
+    return up < 127 ? up : 127;
 }
 
 // Largest of lanes 0 to 7, in every lane.
@@ -278,15 +289,16 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
     };
 
     f32x4 o[NT][DV];
-    float m[NT], l[NT];
+    float m[NT], l[NT], peak[NT];                 // of a row: maximum, sum, the weight that up was set for
+    int up[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         m[t] = -__builtin_inff();
-        l[t] = 0.0f;
+        l[t] = peak[t] = 0.0f;
+        up[t] = up_for(0.0f);
 #pragma unroll
         for (int i = 0; i < DV; ++i) o[t][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    int up = 127 + WEIGHT_BITS;                   // weights are scaled by 2^up, for scales below the normal range
 
     // the first tile is on its way while the queries are written
     Place here = place_of(begin + TILE * wave, begin);
@@ -366,30 +378,6 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
                     for (int t = 0; t < NT; ++t) x[t][i] = here.ok[i / 4] && pos < seen[t] ? x[t][i] : -__builtin_inff();
                 }
             }
-            // the power of two that keeps weights in fp16
-            float most = 0.0f;
-            const float bound = ldexpf(1.0f, WEIGHT_BITS + 1 - up);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(ve[i]));
-            if (__any(most >= bound)) {           // infinite ones come here every time, and do not count
-                most = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(ve[i]) < __builtin_inff() ? fabsf(ve[i]) : 0.0f);
-                const uint32_t top = __builtin_amdgcn_readfirstlane(__float_as_uint(quad_max(most)));
-                const int want = WEIGHT_BITS + 127 - (int)(top >> 23);   // 2^want * top in [2^13, 2^14); top >= 0
-                if (want < up) {
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < DV; ++i)
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) o[t][i][r] = ldexpf(o[t][i][r], want - up);
-                    up = want;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ve[i] = ldexpf(ve[i], up);
-
             half8 w[PP][NT];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
@@ -398,35 +386,52 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
                 for (int i = 1; i < 8; ++i) top_t = fmaxf(top_t, x[t][i]);
                 // maxima are of the scores before the factor, which is not negative
                 const float now = fmaxf(m[t], quad_max(top_t)), base = now == -__builtin_inff() ? 0.0f : now * factor[t];
-                if (__any(now > m[t])) {
-                    const float keep = m[t] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[t] * factor[t] - base);
+                float e[8], v[8], sum = 0.0f, most = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    e[i] = __builtin_fmaf(x[t][i], factor[t], -base);
+                    v[i] = ve[i];
+                }
+                if (!whole) {                     // the factor may be 0; a position that others see may have a scale that is not finite
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        e[i] = x[t][i] == -__builtin_inff() ? x[t][i] : e[i];
+                        v[i] = x[t][i] == -__builtin_inff() ? 0.0f : v[i];
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    e[i] = __builtin_amdgcn_exp2f(e[i]);
+                    sum += e[i];
+                    v[i] *= e[i];
+                    most = fmaxf(most, fabsf(v[i]));
+                }
+                // a maximum that grows, or weights past their power of two
+                if (__any(now > m[t] || most >= ldexpf(1.0f, WEIGHT_BITS + 3 - up[t]))) {
+                    if (__any(most == __builtin_inff())) {       // infinite ones do not count
+                        most = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]) < __builtin_inff() ? fabsf(v[i]) : 0.0f);
+                    }
+                    const float was = m[t] == -__builtin_inff() ? m[t] : m[t] * factor[t];
+                    const float fall = now > m[t] ? was - base : 0.0f, keep = __builtin_amdgcn_exp2f(fall);
                     l[t] *= keep;
+                    peak[t] = fmaxf(peak[t] * keep, quad_max(most));
+                    const int next = up_for(peak[t]);
+                    const float by = __builtin_amdgcn_exp2f(fall + (float)(next - up[t]));
 #pragma unroll
-                    for (int i = 0; i < DV; ++i) o[t][i] *= keep;
+                    for (int i = 0; i < DV; ++i) o[t][i] *= by;
                     m[t] = now;
+                    up[t] = next;
                 }
-                float e[8], v[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = __builtin_fmaf(x[t][i], factor[t], -base);
-                if (!whole) {                     // the factor may be 0
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] = x[t][i] == -__builtin_inff() ? x[t][i] : e[i];
-                }
+                l[t] += sum;
+                const float unit = __uint_as_float((uint32_t)(127 + up[t]) << 23);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p = __builtin_amdgcn_exp2f(e[i]);
-                    l[t] += p;
-                    v[i] = p * ve[i];
-                }
-                if (!whole) {                     // a position that others see may have a scale that is not finite
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[i] = x[t][i] == -__builtin_inff() ? 0.0f : v[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const _Float16 hi = (_Float16)v[i];
+                    const float u = v[i] * unit;
+                    const _Float16 hi = (_Float16)u;
                     w[0][t][i] = hi;
-                    w[1][t][i] = (_Float16)(v[i] - (float)hi);
+                    w[1][t][i] = (_Float16)(u - (float)hi);
                 }
             }
 
@@ -485,7 +490,7 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
             for (int i = 0; i < DV; i += 4) {
                 f32x4 v;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = ldexpf(o[t][i + j][r] * keep, -up);
+                for (int j = 0; j < 4; ++j) v[j] = ldexpf(o[t][i + j][r] * keep, -up[t]);
                 sums[(wave * DV + (r * DV + i) / 4) * 64 + lane] = v;
             }
         __syncthreads();

@@ -49,3 +49,69 @@ def test_attention_bf16_outputs_are_rounded_once(n, d):
     err = np.abs(got.float().cpu().numpy() - want)
     say(f"attention of {n}, d {d}: {(err / bound).max():.3f} of the bound, {(err > bound).sum()} of {err.size} past it")
     assert (err <= bound).all()
+
+
+def crafted(scores, value_scale, signs, heads, d, dtype, seqs=1, size=16, seed=0):
+    """Attention over a sequence whose scores are chosen: column c has the scores
+    signs[c] * scores; of seqs alike, which read the same pages.  (got, want, bound).
+
+    A score is one product of 1 and 1 times its scale, so of the bound's terms for
+    inner products nothing is left; parts below the fp16 range lose 2^-37 of the
+    largest weight times its scale and code."""
+    n, cols = len(scores), len(signs)
+    pages = -(-n // size)
+    cache, arrays, _ = make_cache(pages, 1, size, d, seed=seed)
+    k, ks, v, vs = arrays
+    k[:] = 0
+    k[..., 0] = 1
+    ks.reshape(-1)[:n], vs.reshape(-1)[:n] = scores, value_scale
+    for t, a in zip(cache, arrays):
+        t.copy_(torch.from_numpy(a))
+    q = np.zeros((1, cols, heads, d), np.float32)
+    q[..., 0] = np.asarray(signs)[None, :, None]
+    table, visible = np.arange(pages, dtype=np.int32)[None], np.full((1, cols), n, np.int32)
+    alike = lambda a: torch.from_numpy(np.repeat(a, seqs, 0)).to(DEV)
+    got = moeq8.paged_attention_i8(alike(q).to(dtype), cache, alike(table), alike(visible), scale=1.0)
+    assert torch.equal(got, got[:1].expand_as(got))
+    want, sizes = ref.attention(q, *arrays, table, visible, 1.0)
+    t = np.asarray(signs, np.float64)[:, None] * ks.reshape(-1)[:n].astype(np.float64)
+    w = np.exp(t - t.max(1, keepdims=True))
+    top = (w / w.sum(1, keepdims=True) * vs.reshape(-1)[:n]).max(1)
+    bound = attention_bound(want, (sizes[0], 0 * sizes[1], *sizes[2:]), dtype, d) + (n * 2.0**-37 * 127 * top)[None, :, None, None]
+    return got[:1].float().cpu().numpy(), want, bound
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("heads,d,seqs", [(2, 64, 1), (20, 128, 1), (40, 64, 1), (3, 256, 1), (2, 64, 2100), (20, 64, 2100), (3, 256, 2100)])
+@pytest.mark.parametrize("where", ["one", "first", "falling", "last"])
+def test_attention_loud_scales_of_positions_that_do_not_count(where, heads, d, seqs, dtype):
+    """Value scales far above the others' where the weight is next to nothing, seen
+    before, among or after those that count; where there are many sequences a wave
+    goes through many tiles."""
+    rng = np.random.default_rng(7)
+    n = 700
+    scores, vs = rng.uniform(-1, 1, n), rng.uniform(0.005, 0.03, n)
+    if where == "one":
+        scores[350], vs[350] = -60, 1e12
+    elif where == "first":
+        scores[:64], vs[:64] = -80, 1e12
+    elif where == "last":
+        scores[-40:], vs[-40:] = -80, 1e12
+    else:                                                   # the maximum grows a little every time, the scales fall
+        scores = np.linspace(-80, 0, n)
+        vs = 0.01 * np.exp(np.linspace(60, 0, n))
+    got, want, bound = crafted(scores.astype(np.float32), vs.astype(np.float32), [1.0], heads, d, TYPES[dtype], seqs)
+    err = np.abs(got - want)
+    say(f"loud scales {where} {heads} {d} {seqs} {dtype}: {(err / bound).max():.3f} of the bound")
+    assert (err <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,d", [(2, 64), (20, 64), (3, 128)])
+def test_attention_a_scale_that_counts_in_one_row_alone(heads, d, dtype):
+    """The loud position has all the weight of one column and none of the other's."""
+    rng = np.random.default_rng(8)
+    scores, vs = rng.uniform(-1, 1, 300), rng.uniform(0.005, 0.03, 300)
+    scores[99], vs[99] = -70, 1e12
+    got, want, bound = crafted(scores.astype(np.float32), vs.astype(np.float32), [1.0, -1.0], heads, d, TYPES[dtype])
+    assert (np.abs(got - want) <= bound).all()
