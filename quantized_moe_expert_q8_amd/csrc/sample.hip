@@ -108,7 +108,8 @@ __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int64_t row) {
 struct Weigh {
     double top, c;                                // the largest logit; table steps a logit
     const double* table;                          // 2^(j / 64)
-    __device__ __forceinline__ double steps(float z) const { return fmax(((double)z - top) * c, -64.0 * PER_OCTAVE); }
+    // held where a weight is 0 in 64 bits, and not before: the plain draw takes weights as they are
+    __device__ __forceinline__ double steps(float z) const { return fmax(((double)z - top) * c, -1100.0 * PER_OCTAVE); }
     __device__ __forceinline__ double at(double t, int& i) const {
         const double n = rint(t), x = (t - n) * (0.69314718055994531 / PER_OCTAVE);
         i = (int)n;

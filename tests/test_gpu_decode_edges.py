@@ -115,3 +115,27 @@ def test_attention_a_scale_that_counts_in_one_row_alone(heads, d, dtype):
     scores[99], vs[99] = -70, 1e12
     got, want, bound = crafted(scores.astype(np.float32), vs.astype(np.float32), [1.0, -1.0], heads, d, TYPES[dtype])
     assert (np.abs(got - want) <= bound).all()
+
+
+# ---- sampling ----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [1500, 5003])
+def test_sample_never_draws_what_weighs_nothing(vocab, dtype):
+    """u = 0 next to logits masked with finite values: their weights are 0 in 64 bits."""
+    t = TYPES[dtype]
+    rng = np.random.default_rng(vocab)
+    z, zv = typed(rng.standard_normal((4, vocab)), t)
+    z[0, :700] = torch.finfo(t).min
+    z[1, :1030] = -1e4
+    z[2, :512] = -800.0
+    z[3, :600] = -60.0                                      # e^-60 is something
+    u = torch.zeros(4, device=DEV)
+    token, logprob = moeq8.logits_sample(z.to(DEV), u)
+    zv = z.float().numpy()
+    for r in range(4):
+        want, log = ref.sample_row(zv[r], 0.0)
+        assert int(token[r]) == want and abs(float(logprob[r]) - log) <= 2.0**-23 * abs(log)
+    # at a temperature under which they weigh something after all
+    token, _ = moeq8.logits_sample(z[1:3].to(DEV), u[:2], temperature=torch.full((2,), 50.0, device=DEV))
+    assert token.tolist() == [ref.sample_row(r, 0.0, 50.0)[0] for r in zv[1:3]]
