@@ -663,7 +663,7 @@ int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t 
  * n_heads); a column that sees nothing gives zeros.  The scales of k_i and v_i
  * multiply the finished product and the weight.
  *   q, out    dtype [n_seqs][n_cols][n_q_heads][d], at strides in elements; out
- *             must not overlap q or the cache
+ *             must not overlap anything that the call reads
  *   pages     int32 [n_seqs][pages_row_stride]: position i lies in page
  *             pages[s][i / page_size]; n_table entries a sequence.  The positions
  *             of a page outside the cache are not seen.

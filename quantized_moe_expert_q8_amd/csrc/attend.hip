@@ -52,6 +52,7 @@
 #include "moeq8_lds.hpp"
 
 #include <type_traits>
+#include <utility>
 
 namespace moeq8 {
 namespace {
@@ -719,15 +720,20 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
     }
     if (((uintptr_t)q | (uintptr_t)out) & (uintptr_t)(es - 1) || ((uintptr_t)pages | (uintptr_t)visible) & 3u) return MOEQ8_EALIGN;
     if (a.c.token_stride > (1ll << 26)) return MOEQ8_EUNSUPPORTED;        // a lane's offsets have 32 bits
-    if (ranges_overlap(q, bytes[0], out, bytes[1]) || clashes_with_cache(a.c, out, bytes[1])) return MOEQ8_EINVAL;
     const Plan p = plan_for(n_seqs, n_cols, n_q_heads, heads, d, max_visible);
     if (p.blocks > most_blocks(p.waves * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MOEQ8_EINVAL;
     if (p.bytes && (uintptr_t)workspace & 15u) return MOEQ8_EALIGN;
+    // what is written lies apart from itself and from what other blocks and the join still read
     const int64_t ws_bytes = (int64_t)p.bytes;
-    if (p.bytes && (ranges_overlap(workspace, ws_bytes, q, bytes[0]) || ranges_overlap(workspace, ws_bytes, out, bytes[1]) ||
-                    clashes_with_cache(a.c, workspace, ws_bytes)))
-        return MOEQ8_EINVAL;
+    const int64_t page_bytes = 4 * ((n_seqs > 1 ? (n_seqs - 1) * pages_row_stride : 0) + n_table), seen_bytes = 4 * n_seqs * n_cols;
+    for (const auto& [at, n] : {std::pair<const void*, int64_t>{out, bytes[1]}, {workspace, ws_bytes}}) {
+        if (n == 0) continue;
+        if (ranges_overlap(at, n, q, bytes[0]) || ranges_overlap(at, n, visible, seen_bytes) ||
+            (n_table && ranges_overlap(at, n, pages, page_bytes)) || clashes_with_cache(a.c, at, n))
+            return MOEQ8_EINVAL;
+    }
+    if (p.bytes && ranges_overlap(workspace, ws_bytes, out, bytes[1])) return MOEQ8_EINVAL;
     a.q = q; a.q_seq = q_seq_stride; a.q_col = q_col_stride; a.q_head = q_head_stride;
     a.out = out; a.o_seq = out_seq_stride; a.o_col = out_col_stride; a.o_head = out_head_stride;
     a.pages = pages; a.pages_row = pages_row_stride;
