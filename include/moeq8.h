@@ -643,16 +643,17 @@ typedef struct moeq8_kv_cache {
 /* Keys and values of n_tokens tokens into their slots:
  *   k, v   dtype [n_tokens][n_heads][d], at token and head strides in elements
  *   slots  int64 [n_tokens]; a token whose slot is outside the cache is skipped
- * A slot that comes twice holds bytes of either token.  The cache must not
- * overlap k and v, nor its keys its values.  `cache` is read on the host, during
- * the call. */
+ * A slot that comes twice holds bytes of either token.  The cache must overlap
+ * neither k, v and slots nor, its keys, values and their scales, itself: they may
+ * take turns in one buffer.  `cache` is read on the host, during the call. */
 int kv_cache_write_i8(const void* k, int64_t k_token_stride, int64_t k_head_stride, const void* v,
                       int64_t v_token_stride, int64_t v_head_stride, int32_t dtype, int64_t n_tokens,
                       const int64_t* slots, const moeq8_kv_cache* cache, void* stream);
 
 /* Rows of the cache as values: out = dtype(fp32(code * scale)), zeros for a slot
- * outside the cache.  Arguments as above, k_out and v_out the outputs; slots may
- * come more than once. */
+ * outside the cache.  Arguments as above, k_out and v_out the outputs, which overlap
+ * neither each other (they may take turns in one buffer) nor what is read; slots
+ * may come more than once. */
 int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t n_tokens, int32_t dtype,
                      void* k_out, int64_t k_token_stride, int64_t k_head_stride, void* v_out,
                      int64_t v_token_stride, int64_t v_head_stride, void* stream);

@@ -159,8 +159,6 @@ int cache_rows(const void* k, int64_t k_token, int64_t k_head, const void* v, in
     if (const int s = check_cache(cache, a.c)) return s;
     if (n_tokens == 0) return MOEQ8_OK;
     if (!k || !v || !slots) return MOEQ8_EINVAL;
-    // one array for both: a race of the rows written
-    if (WRITE ? a.c.k == a.c.v || a.c.k_scale == a.c.v_scale : k == v) return MOEQ8_EINVAL;
     const int64_t heads = a.c.n_heads, d = a.c.d, es = dtype_bytes(dtype);
     for (const int64_t s : {k_head, v_head})
         if (heads > 1 && s < d) return MOEQ8_EINVAL;
@@ -171,6 +169,16 @@ int cache_rows(const void* k, int64_t k_token, int64_t k_head, const void* v, in
     const int64_t k_bytes = ((n_tokens - 1) * k_token + (heads > 1 ? (heads - 1) * k_head : 0) + d) * es;
     const int64_t v_bytes = ((n_tokens - 1) * v_token + (heads > 1 ? (heads - 1) * v_head : 0) + d) * es;
     if (clashes_with_cache(a.c, k, k_bytes) || clashes_with_cache(a.c, v, v_bytes)) return MOEQ8_EINVAL;
+    // what is written lies apart from itself and from the slots, which other rows still read
+    const int64_t slot_bytes = 8 * n_tokens;
+    if (WRITE) {
+        if (overlaps_itself(a.c) || clashes_with_cache(a.c, slots, slot_bytes)) return MOEQ8_EINVAL;
+    } else {
+        const Pieces ko{k, d * es, {n_tokens, heads, 1}, {k_token * es, k_head * es, 0}};
+        const Pieces vo{v, d * es, {n_tokens, heads, 1}, {v_token * es, v_head * es, 0}};
+        if (pieces_overlap(ko, vo) || ranges_overlap(slots, slot_bytes, k, k_bytes) || ranges_overlap(slots, slot_bytes, v, v_bytes))
+            return MOEQ8_EINVAL;
+    }
     a.k = const_cast<void*>(k); a.k_token = k_token; a.k_head = k_head;
     a.v = const_cast<void*>(v); a.v_token = v_token; a.v_head = v_head;
     a.slots = slots;

@@ -45,4 +45,16 @@ inline bool clashes_with_cache(const Cache& c, const void* p, int64_t bytes) {
            ranges_overlap(p, bytes, c.k_scale, scales) || ranges_overlap(p, bytes, c.v_scale, scales);
 }
 
+// Whether any two of the cache's four arrays overlap.
+inline bool overlaps_itself(const Cache& c) {
+    const int64_t pages = c.n_pages, heads = c.n_heads, places = 1ll << c.page_shift;
+    auto codes = [&](const void* p) { return Pieces{p, c.d, {pages, heads, places}, {c.page_stride, c.head_stride, c.token_stride}}; };
+    auto scales = [&](const void* p) { return Pieces{p, 4 * places, {pages, heads, 1}, {4 * c.scale_page_stride, 4 * c.scale_head_stride, 0}}; };
+    const Pieces all[] = {codes(c.k), codes(c.v), scales(c.k_scale), scales(c.v_scale)};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (pieces_overlap(all[i], all[j])) return true;
+    return false;
+}
+
 }  // namespace moeq8

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <numeric>
 
 #include "../../include/moeq8.h"
 
@@ -38,6 +39,37 @@ inline bool rows_clash(const void* p, int64_t p_stride, const void* o, int64_t o
     if (p_stride != o_stride) return true;
     const int64_t apart = ((const uint8_t*)o - (const uint8_t*)p) % p_stride, behind = apart < 0 ? apart + p_stride : apart;
     return behind < bytes || p_stride - behind < bytes;
+}
+
+// Pieces of `bytes` bytes at p + i stride[0] + j stride[1] + l stride[2], each index below its count.
+struct Pieces {
+    const void* p;
+    int64_t bytes, count[3], stride[3];
+};
+
+// Bytes from the first to the last of them, along the dimensions that `without` has no bit for.
+inline int64_t extent(const Pieces& x, int without = 0) {
+    int64_t n = x.bytes;
+    for (int i = 0; i < 3; ++i)
+        if (!(without >> i & 1) && x.count[i] > 1) n += (x.count[i] - 1) * x.stride[i];
+    return n;
+}
+
+// Whether pieces of two arrays overlap.  Arrays that take turns in one buffer do not:
+// steps along some of the dimensions leave a place's remainder by the greatest
+// common divisor of their strides as it is, and where the remainders that the other
+// dimensions reach lie apart, so do the arrays.
+inline bool pieces_overlap(const Pieces& a, const Pieces& b) {
+    if (!ranges_overlap(a.p, extent(a), b.p, extent(b))) return false;
+    for (int outer = 1; outer < 8; ++outer) {
+        int64_t g = 0;
+        for (int i = 0; i < 3; ++i)
+            if (outer >> i & 1) g = std::gcd(g, std::gcd(a.count[i] > 1 ? a.stride[i] : 0, b.count[i] > 1 ? b.stride[i] : 0));
+        if (g == 0) continue;
+        const int64_t apart = ((const uint8_t*)b.p - (const uint8_t*)a.p) % g, behind = apart < 0 ? apart + g : apart;
+        if (behind >= extent(a, outer) && g - behind >= extent(b, outer)) return false;
+    }
+    return true;
 }
 
 }  // namespace moeq8

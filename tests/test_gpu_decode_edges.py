@@ -139,3 +139,32 @@ def test_sample_never_draws_what_weighs_nothing(vocab, dtype):
     # at a temperature under which they weigh something after all
     token, _ = moeq8.logits_sample(z[1:3].to(DEV), u[:2], temperature=torch.full((2,), 50.0, device=DEV))
     assert token.tolist() == [ref.sample_row(r, 0.0, 50.0)[0] for r in zv[1:3]]
+
+
+# ---- cache -------------------------------------------------------------------------
+
+def test_cache_arrays_that_take_turns_in_a_buffer():
+    """Keys, values and their scales of each page together; outputs [token][head][k or v]."""
+    pages, heads, size, d = 5, 3, 16, 48
+    codes, scales = heads * size * d, heads * size * 4
+    buf = torch.zeros(pages, 2 * codes + 2 * scales, dtype=torch.int8, device=DEV)
+    k, v = (buf[:, i * codes:(i + 1) * codes].view(pages, heads, size, d) for i in range(2))
+    ks, vs = (buf.view(torch.float32)[:, (2 * codes + i * scales) // 4:][:, :heads * size].view(pages, heads, size) for i in range(2))
+    cache = moeq8.KVCacheI8(k, ks, v, vs)
+    rng = np.random.default_rng(3)
+    slots = rng.permutation(pages * size)[:50].astype(np.int64)
+    x = rng.standard_normal((2, 50, heads, d)).astype(np.float32)
+    arrays = [t.cpu().numpy().copy() for t in cache]
+    moeq8.kv_cache_write_i8(*(torch.from_numpy(y).to(DEV) for y in x), cache, torch.from_numpy(slots).to(DEV))
+    for i in range(2):
+        ref.cache_write(arrays[2 * i], arrays[2 * i + 1], x[i], slots)
+    assert all(np.array_equal(t.cpu().numpy(), a) for t, a in zip(cache, arrays))
+    out = torch.zeros(50, heads, 2, d, device=DEV)
+    moeq8.kv_cache_read_i8(cache, torch.from_numpy(slots).to(DEV), k_out=out[:, :, 0], v_out=out[:, :, 1])
+    for i in range(2):
+        assert np.array_equal(out[:, :, i].cpu().numpy(), ref.cache_read(arrays[2 * i], arrays[2 * i + 1], slots))
+    with pytest.raises(moeq8.MoeQ8Error):
+        moeq8.kv_cache_read_i8(cache, torch.from_numpy(slots[:40]).to(DEV), k_out=out[:40, :, 0], v_out=out[10:, :, 0])
+    with pytest.raises(moeq8.MoeQ8Error):
+        moeq8.kv_cache_write_i8(torch.zeros(1, heads, d, device=DEV), torch.zeros(1, heads, d, device=DEV),
+                                cache._replace(v=k[1:], k=k[:-1], k_scale=ks[1:], v_scale=vs[1:]), torch.zeros(1, dtype=torch.int64, device=DEV))
