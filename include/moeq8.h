@@ -675,7 +675,7 @@ int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t 
  *             close bound is faster.  The results' roundings depend on it too.
  *   scale     finite; the inner products' factor (commonly d^-0.5)
  * n_q_heads is a multiple of n_heads, 1 <= n_cols <= MOEQ8_MAX_COLS, max_visible <
- * 2^30, token_stride <= 2^26.  Scores and sums are fp32; fp32 queries and the
+ * 2^30, n_table < 2^31, token_stride <= 2^26.  Scores and sums are fp32; fp32 queries and the
  * weights go through the matrix cores as two fp16 parts (22 bits), less what is
  * below 2^-38 of a row's largest |q| and below 2^-37 of its largest weight times
  * value scale.  Codes outside of what is seen do not matter, nor do their scales; a

@@ -719,7 +719,7 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
         bytes[i] *= es;
     }
     if (((uintptr_t)q | (uintptr_t)out) & (uintptr_t)(es - 1) || ((uintptr_t)pages | (uintptr_t)visible) & 3u) return MOEQ8_EALIGN;
-    if (a.c.token_stride > (1ll << 26)) return MOEQ8_EUNSUPPORTED;        // a lane's offsets have 32 bits
+    if (a.c.token_stride > (1ll << 26) || n_table >= (1ll << 31)) return MOEQ8_EUNSUPPORTED;     // a lane's offsets have 32 bits
     const Plan p = plan_for(n_seqs, n_cols, n_q_heads, heads, d, max_visible);
     if (p.blocks > most_blocks(p.waves * 64) || n_seqs * n_q_heads * n_cols > most_blocks(256)) return MOEQ8_EUNSUPPORTED;
     if (p.bytes && (!workspace || workspace_bytes < p.bytes)) return MOEQ8_EINVAL;

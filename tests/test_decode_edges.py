@@ -85,3 +85,15 @@ def test_cache_arrays_written_lie_apart():
     # slots in the cache
     assert write(cache(), slots=P + 8) == write(cache(), slots=P + 0x300000 + 504) == write(cache(), slots=P - 32) == -1
     assert write(cache(), slots=P + 4096) == write(cache(), slots=P - 40) == fine
+
+
+@cpu_only
+def test_attention_tables_past_what_positions_count():
+    """Entries times the page's size would pass 64 bits: refused before anything is made of them."""
+    L = moeq8.lib()
+    for n in (1 << 31, 1 << 40, (1 << 59) + 1, 1 << 62):
+        assert L.paged_attention_i8(Q, 128, 128, 32, 0, 1, 1, 4, cache(), S, n, n, 0x70000000, 64, 1.0, R, 128, 128, 32, None, 0,
+                                    None) == -3
+    big = cache(page_size=1 << 20, head_stride=32 << 20, page_stride=64 << 20, scale_head_stride=1 << 20, scale_page_stride=2 << 20)
+    assert L.paged_attention_i8(Q, 128, 128, 32, 0, 1, 1, 4, big, 0x60000000, 1 << 44, 1 << 44, 0x70000000, 64, 1.0, R, 128, 128, 32,
+                                None, 0, None) == -3
