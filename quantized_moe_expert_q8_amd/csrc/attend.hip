@@ -76,7 +76,7 @@ struct AttendArgs {
     float2* stats;
     uint32_t cols, group, rows, limit;            // rows: cols * group; limit: what visible is taken within
     uint32_t span, spans, seqs, parts;            // parts: of the rows, 16 * NT each
-    float factor;                                 // |scale| * log2(e)
+    double factor;                                // |scale| * log2(e): fp32 holds it with a row's power of two
     uint32_t flip;                                // the scale's sign bit, which the queries take
 };
 
@@ -203,7 +203,7 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
         }
         m = quad_max(m);
         const int up = m > 0.0f && m < __builtin_inff() ? 14 - __builtin_amdgcn_frexp_expf(m) : 0;
-        if (g == 0) factors[16 * t + n] = ldexpf(a.factor, -up);
+        if (g == 0) factors[16 * t + n] = (float)fmin(__builtin_ldexp(a.factor, -up), (double)__FLT_MAX__);
 #pragma unroll
         for (int c = 0; c < NC; ++c)
 #pragma unroll
@@ -744,7 +744,7 @@ extern "C" int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q
     const int64_t positions = n_table << a.c.page_shift;
     a.limit = (uint32_t)std::min(max_visible, positions);
     a.span = (uint32_t)p.span; a.spans = (uint32_t)p.spans; a.seqs = (uint32_t)n_seqs; a.parts = (uint32_t)p.parts;
-    a.factor = (float)(std::abs(scale) * 1.4426950408889634);
+    a.factor = std::abs(scale) * 1.4426950408889634;
     a.flip = scale < 0.0 ? 0x80000000u : 0u;
     switch (dtype) {
         case MOEQ8_F32: return attend<float>(a, p, (hipStream_t)stream);

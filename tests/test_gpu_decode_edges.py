@@ -117,6 +117,23 @@ def test_attention_a_scale_that_counts_in_one_row_alone(heads, d, dtype):
     assert (np.abs(got - want) <= bound).all()
 
 
+@pytest.mark.parametrize("up,loud,scale", [(-135, 0, 2.0**134), (-140, 0, 3e41), (100, 60, 2.0**-162), (120, 70, 2.0**-192), (-100, -60, 2.0**158)])
+def test_attention_factors_past_fp32(up, loud, scale):
+    """Queries of 2^up, key scales of 2^loud and a factor that fp32 does not hold, for scores around 1."""
+    rng = np.random.default_rng(12)
+    cache, arrays, _ = make_cache(4, 1, 16, 64, seed=12)
+    arrays[1][:] = np.ldexp(arrays[1], loud)
+    cache.k_scale.copy_(torch.from_numpy(arrays[1]))
+    table = np.arange(4, dtype=np.int32)[None]
+    q = np.ldexp(rng.standard_normal((1, 1, 2, 64)).astype(np.float32), up).astype(np.float32)
+    q[0, 0, 1] = 0                                          # all alike, whatever the factor
+    got = moeq8.paged_attention_i8(torch.from_numpy(q).to(DEV), cache, torch.from_numpy(table).to(DEV),
+                                   torch.full((1, 1), 60, dtype=torch.int32, device=DEV), scale=scale).cpu().numpy()
+    want, sizes = ref.attention(q, *arrays, table, [[60]], scale)
+    assert 0.05 < sizes[2][0, 0, 0] < 50
+    assert (np.abs(got - want) <= attention_bound(want, sizes, torch.float32, 64)).all()
+
+
 # ---- sampling ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", list(TYPES))
