@@ -21,9 +21,13 @@
 // keys on, found in the k segments that have them; for min-p the segments whose
 // largest passes it; else the bin that the threshold falls into.  Among bins the draw
 // takes a tile of k_bins first, then a segment, then its logits in order; in a list it
-// is one more selection, over the indexes.  Rows with more candidates than LDS holds
-// (equal logits by the thousand), with infinite logits, or of over 524288 logits go
-// the slow way: selections over the whole row, some 100 us for 131072 logits.
+// is one more selection, over the indexes.  A list that gets more candidates than LDS
+// holds (a vocabulary in the order of its frequencies: the segments' largest say little)
+// goes on by bins, which the row's block then makes itself (8 x 131072 f32, k = 50: 75
+// us, by the whole row 270).  Rows with more than that in one bin (equal logits by the
+// thousand; normal logits of a third of the temperature), with infinite logits, or of
+// over 524288 logits go the slow way: selections over the whole row, 220 to 620 us for
+// 131072 logits, since few digits take the additions of most logits.
 //
 // What bounds it: for few rows the chain of three launches and of a block's
 // dependent steps (1 x 32000 f32 with top-k, and 5 x 131072 with top-p and min-p, 16
@@ -374,6 +378,28 @@ __device__ __forceinline__ Row row_of(const SampleArgs& a, const Rules& r, int64
 
 // ---- bins --------------------------------------------------------------------------
 
+// A wave's logits of a segment into the bins, but for those of the last bin that weigh
+// nothing (-inf and NaN among them): no cut is made there, and logits masked with a
+// finite value would take turns at it by the thousand (64 x 131072, k = 50 of 10000
+// unmasked: 91 us by bins, and 45).
+template <typename T>
+__device__ __forceinline__ void add_to_bins(const SampleArgs& a, const Rules& r, const Weigh& w, const Eight<T>& e, uint32_t seg,
+                                            unsigned long long* mass, uint32_t* count) {
+    float v[8];
+    e.values(v, seg, (uint32_t)a.vocab);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        int n;
+        const double real = w.at(w.steps(v[j]), n);          // fmax takes a NaN for the least
+        const uint64_t u = Weigh::rounded(real, n, a.bits);
+        // what min-p drops counts for top-p, behind all others
+        const int b = r.rest() && __builtin_ldexp(real, n >> 6) < (double)r.least ? BINS - 1 : bin_of(n);
+        if (u == 0 && b == BINS - 1) continue;
+        atomicAdd(&mass[b], (unsigned long long)u);
+        if (r.k) atomicAdd(&count[b], 1u);
+    }
+}
+
 template <typename T>
 __global__ __launch_bounds__(256) void k_bins(SampleArgs a) {
     __shared__ double table[PER_OCTAVE];
@@ -403,19 +429,7 @@ __global__ __launch_bounds__(256) void k_bins(SampleArgs a) {
 #pragma unroll
         for (uint32_t i = 0; i < AHEAD; ++i) {
             if (seg + 4 * i >= last) break;
-            float v[8];
-            e[i].values(v, seg + 4 * i, vocab);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (!(v[j] > -__builtin_inff())) continue;
-                int n;
-                const double real = w.at(w.steps(v[j]), n);
-                const uint64_t u = Weigh::rounded(real, n, a.bits);
-                // what min-p drops counts for top-p, behind all others
-                const int b = r.rest() && __builtin_ldexp(real, n >> 6) < (double)r.least ? BINS - 1 : bin_of(n);
-                atomicAdd(&mass[b], (unsigned long long)u);
-                if (r.k) atomicAdd(&count[b], 1u);
-            }
+            add_to_bins(a, r, w, e[i], seg + 4 * i, mass, count);
         }
     }
     __syncthreads();
@@ -874,46 +888,69 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
             uint32_t from = KEY_FIRST;
             if (of_lane((uint64_t)wave_scan32(some), 63) >= (uint64_t)r.k)
                 from = wave_select(s, (uint64_t)r.k, before, [&](auto add) { tops([&](uint32_t key) { add(key, 1); }); });
+            // logits that weigh nothing, masked with a finite value say, need not be there
+            if (bin_of(w, logit_of(from)) == BINS - 1)
+                from = first_key((double)top - (4.0 * BINS - 4.5) / w.c, [&](float v) { return bin_of(w, v) < BINS - 1; });
             if (lane == 0) s.from = from;
         }
         __syncthreads();
-        if (!gather(r.k ? s.from : s.least, KEY_INF)) return false;
-        if (wave != 0) return true;
-        uint32_t floor = 0;
-        uint64_t ties = ~0ull, before, unit, equal;
-        if (r.k && (uint64_t)r.k < s.n) cut_by_count((uint64_t)r.k, floor, ties);
-        if (r.p < 1.0f) {
-            uint64_t have = mass_of(floor, equal, unit);
-            have += unit ? ties * unit : 0;
-            const uint64_t want = part_of(by_least ? (uint64_t)rint(__builtin_ldexp(all, a.bits)) : have);
-            if (have >= want) cut_by_mass(want, floor, ties, unit);       // else min-p cuts above top-p
-        }
-        uint32_t limit = vocab;
-        if (floor) {
-            mass_of(floor, equal, unit);
-            limit = last_tie(floor, ties, equal);
-        }
-        // the draw: by index, the first up to which there is more than the target
-        const uint32_t least = s.least;
-        auto drawn = [&](uint32_t key, uint32_t i, uint64_t u) { return key >= least && (key > floor || (key == floor && i <= limit)) ? u : 0; };
-        uint64_t total = 0;
-        listed([&](uint32_t key, uint32_t i, uint64_t u) { total += drawn(key, i, u); });
-        total = wave_sum(total);
-        uint64_t target = (uint64_t)((double)uf * (double)total);
-        if (target >= total) target = total - 1;
-        uint32_t token = 0xffffffu - wave_select(s, target + 1, before, [&](auto add) {
-            listed([&](uint32_t key, uint32_t i, uint64_t u) {
-                const uint64_t d = drawn(key, i, u);
-                if (d) add(0xffffffu - i, d);
+        if (gather(r.k ? s.from : s.least, KEY_INF)) {
+            if (wave != 0) return true;
+            uint32_t floor = 0;
+            uint64_t ties = ~0ull, before, unit, equal;
+            if (r.k && (uint64_t)r.k < s.n) cut_by_count((uint64_t)r.k, floor, ties);
+            if (r.p < 1.0f) {
+                uint64_t have = mass_of(floor, equal, unit);
+                have += unit ? ties * unit : 0;
+                const uint64_t want = part_of(by_least ? (uint64_t)rint(__builtin_ldexp(all, a.bits)) : have);
+                if (have >= want) cut_by_mass(want, floor, ties, unit);       // else min-p cuts above top-p
+            }
+            uint32_t limit = vocab;
+            if (floor) {
+                mass_of(floor, equal, unit);
+                limit = last_tie(floor, ties, equal);
+            }
+            // the draw: by index, the first up to which there is more than the target
+            const uint32_t least = s.least;
+            auto drawn = [&](uint32_t key, uint32_t i, uint64_t u) { return key >= least && (key > floor || (key == floor && i <= limit)) ? u : 0; };
+            uint64_t total = 0;
+            listed([&](uint32_t key, uint32_t i, uint64_t u) { total += drawn(key, i, u); });
+            total = wave_sum(total);
+            uint64_t target = (uint64_t)((double)uf * (double)total);
+            if (target >= total) target = total - 1;
+            uint32_t token = 0xffffffu - wave_select(s, target + 1, before, [&](auto add) {
+                listed([&](uint32_t key, uint32_t i, uint64_t u) {
+                    const uint64_t d = drawn(key, i, u);
+                    if (d) add(0xffffffu - i, d);
+                });
             });
-        });
-        token = token < vocab ? token : vocab - 1;
-        if (lane == 0) {
-            a.token[row] = (int32_t)token;
-            if (a.logprob)
-                a.logprob[row] = (float)(((double)to_f32(z[token]) - (double)top) * r.per_nat - log(__builtin_ldexp((double)total, -a.bits)));
+            token = token < vocab ? token : vocab - 1;
+            if (lane == 0) {
+                a.token[row] = (int32_t)token;
+                if (a.logprob)
+                    a.logprob[row] = (float)(((double)to_f32(z[token]) - (double)top) * r.per_nat - log(__builtin_ldexp((double)total, -a.bits)));
+            }
+            return true;
         }
-        return true;
+        // more than the list holds: on by bins, which k_bins has not made
+        static_assert(THREADS == BINS && CAP >= BINS, "a thread a bin, in the list's place");
+        unsigned long long* const mass = (unsigned long long*)s.weight;
+#pragma unroll 1
+        for (uint32_t t = 0; t < a.tiles; ++t) {
+            mass[tid] = s.key[tid] = 0;
+            __syncthreads();
+            const uint32_t first = t * a.tile_segs, last = first + a.tile_segs < a.segs ? first + a.tile_segs : a.segs;
+#pragma unroll 1
+            for (uint32_t seg = first + wave; seg < last; seg += WAVES) {
+                Eight<T> e;
+                e.load(z, seg, vocab);
+                add_to_bins(a, r, w, e, seg, mass, s.key);
+            }
+            __syncthreads();
+            a.bin_mass[(row * a.tiles + t) * BINS + tid] = mass[tid];
+            if (r.k) a.bin_count[(row * a.tiles + t) * BINS + tid] = s.key[tid];
+        }
+        __syncthreads();
     }
 
     // ---- by bins: thread b has bin b ----
@@ -951,11 +988,12 @@ __device__ __forceinline__ bool pick_fast(const SampleArgs& a, const Rules& r, i
             __syncthreads();
             bin = s.seg;
             before = s.rest;
-            if (r.rest() && bin == BINS - 1) continue;           // min-p cuts above
+            if (bin == BINS - 1) continue;        // min-p cuts above, or what is cut there weighs nothing
         } else {
             __syncthreads();
             if (s.least <= floor) continue;       // the others cut above
             bin = (uint32_t)bin_of(w, logit_of(s.least));
+            if (bin == BINS - 1) continue;
         }
         if (bin != held) {
             if (wave == 0) {

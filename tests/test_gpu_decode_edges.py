@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 import quantized_moe_expert_q8_amd as moeq8  # noqa: E402
 from oracle import decode_ref as ref  # noqa: E402
 from _gpu import DEV, say  # noqa: E402
-from test_gpu_decode_operators import TYPES, attention_bound, make_cache, typed  # noqa: E402
+from test_gpu_decode_operators import TYPES, attention_bound, check_sample, make_cache, typed  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -156,6 +156,81 @@ def test_sample_never_draws_what_weighs_nothing(vocab, dtype):
     # at a temperature under which they weigh something after all
     token, _ = moeq8.logits_sample(z[1:3].to(DEV), u[:2], temperature=torch.full((2,), 50.0, device=DEV))
     assert token.tolist() == [ref.sample_row(r, 0.0, 50.0)[0] for r in zv[1:3]]
+
+
+def masked_rows(rows, vocab, kept, value, seed):
+    rng = np.random.default_rng(seed)
+    z = np.full((rows, vocab), value)
+    z[:, 5000:5000 + kept] = 2 * rng.standard_normal((rows, kept))
+    return z, rng.uniform(0, 1, rows)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("kept", [1, 300, 2000, 10000, 40000])
+def test_sample_masks_of_finite_values(kept, dtype):
+    """Most of a vocabulary masked with a value whose weight is 0: fewer tokens, or
+    segments, than k that have one.
+
+    Weights are held to 2^-47 for this vocabulary: with rules, one below 2^-48 is 0 and
+    not drawn by u = 0 either.  Those rank behind all others, so leaving them out
+    changes nothing of what the rules keep of the others."""
+    vocab, t = 60011, TYPES[dtype]
+    for value in (-1e4, float(torch.finfo(t).min)):
+        z, u = masked_rows(3, vocab, kept, value, kept)
+        u[0] = 0
+        zt, zv = typed(z, t)
+        u = u.astype(np.float32)
+        for rules in (dict(top_k=50), dict(top_k=500), dict(top_k=5000), dict(top_k=50, top_p=0.9), dict(top_k=500, min_p=0.02),
+                      dict(top_k=500, top_p=0.8, min_p=0.01), dict(top_k=500, top_p=0.8, min_p=1e-25), dict(top_k=70, temperature=0.05),
+                      dict(top_p=0.9), dict(min_p=0.02), dict(top_p=0.9, min_p=1e-25), dict(top_p=0.9, min_p=1e-25, top_k=20000)):
+            as_f32 = {k: np.float32(v).item() if k != "top_k" else v for k, v in rules.items()}
+            vectors = {k: torch.full((3,), v, dtype=torch.int32 if k == "top_k" else torch.float32, device=DEV) for k, v in rules.items()}
+            token, logprob = moeq8.logits_sample(zt.to(DEV), torch.from_numpy(u).to(DEV), **vectors)
+            for r in range(3):
+                weight = np.exp((zv[r].astype(np.float64) - zv[r].max()) / as_f32.get("temperature", 1.0))
+                want, log = ref.sample_row(np.where(weight < 2.0**-48, -np.inf, zv[r]), float(u[r]), **as_f32)
+                assert int(token[r]) == want, (value, rules, r)
+                assert abs(float(logprob[r]) - log) <= 2.0**-23 * max(abs(log), 1e-7), (value, rules, r)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rules", [dict(top_k=100), dict(top_k=100, top_p=0.9), dict(top_k=100, min_p=0.3), dict(top_k=90, top_p=0.7, min_p=0.05),
+                                   dict(min_p=1e-3), dict(min_p=1e-4, top_p=0.97), dict(min_p=1e-3, top_p=0.3)],
+                         ids=lambda r: "-".join(f"{k}{v}" for k, v in r.items()))
+def test_sample_more_candidates_than_a_list_holds(rules, dtype):
+    """A vocabulary in the order of its frequencies: the largest logits of its segments
+    say little of the largest of all; and logits that nearly all pass min-p."""
+    rng = np.random.default_rng(41)
+    z, u = rng.standard_normal((4, 60011)), rng.uniform(0, 1, 4)
+    z[0] -= np.arange(60011) / 2000
+    z[1] += np.arange(60011) / 2000
+    z[2] = np.round(8 * (z[2] - np.abs(np.arange(60011) - 30000) / 3000)) / 8
+    z[3] *= 1.5
+    check_sample(z, u, TYPES[dtype], **rules)
+
+
+def test_sample_masks_of_finite_values_cost_no_more():
+    """Masked with -1e4 a row takes about as long as masked with -inf, and not a
+    selection over all of it (ten times as long)."""
+    times = {}
+    for value in (-1e4, -float("inf")):
+        z, u = masked_rows(8, 131072, 10000, value, 1)
+        z, u = torch.from_numpy(z).float().to(DEV), torch.from_numpy(u).float().to(DEV)
+        k = torch.full((8,), 50, dtype=torch.int32, device=DEV)
+        run = lambda: moeq8.logits_sample(z, u, top_k=k)
+        run()
+        taken = []
+        for _ in range(5):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            for _ in range(50):
+                run()
+            end.record()
+            end.synchronize()
+            taken.append(begin.elapsed_time(end) * 20)
+        times[value] = sorted(taken)[2]
+    say(f"masked: {times}")
+    assert times[-1e4] < 3 * times[-float("inf")]
 
 
 # ---- cache -------------------------------------------------------------------------
