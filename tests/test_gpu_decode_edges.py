@@ -14,7 +14,7 @@ torch = pytest.importorskip("torch")
 import quantized_moe_expert_q8_amd as moeq8  # noqa: E402
 from oracle import decode_ref as ref  # noqa: E402
 from _gpu import DEV, say  # noqa: E402
-from test_gpu_decode_operators import TYPES, attention_bound, check_sample, make_cache, typed  # noqa: E402
+from test_gpu_decode_operators import TYPES, attention_bound, check_cache, check_sample, make_cache, typed  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -260,3 +260,98 @@ def test_cache_arrays_that_take_turns_in_a_buffer():
     with pytest.raises(moeq8.MoeQ8Error):
         moeq8.kv_cache_write_i8(torch.zeros(1, heads, d, device=DEV), torch.zeros(1, heads, d, device=DEV),
                                 cache._replace(v=k[1:], k=k[:-1], k_scale=ks[1:], v_scale=vs[1:]), torch.zeros(1, dtype=torch.int64, device=DEV))
+
+
+# ---- the forms that larger calls take ------------------------------------------------
+
+# Row tiles of 16, values in 64s, blocks of four waves; the lengths with one span and with several.
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("seqs,cols,heads,kv,d,longest", [
+    (67, 1, 32, 8, 64, 300), (67, 1, 32, 8, 64, 1300), (67, 5, 32, 8, 64, 1300), (67, 5, 64, 8, 64, 1300),
+    (67, 1, 32, 8, 128, 300), (67, 1, 32, 8, 128, 1300), (67, 3, 64, 8, 128, 1300), (9, 5, 64, 8, 128, 1300),
+    (67, 8, 8, 8, 80, 700), (67, 1, 16, 8, 256, 1300), (40, 8, 32, 8, 256, 700), (33, 8, 64, 8, 128, 900)])
+def test_attention_batches(seqs, cols, heads, kv, d, longest, dtype):
+    rng = np.random.default_rng(seqs + cols + d)
+    size, t = 16, TYPES[dtype]
+    lengths = rng.integers(1, longest + 1, seqs)
+    lengths[[0, 5]], lengths[[1, 7]], lengths[2], lengths[-1] = 0, longest, 1, longest - 1
+    count = -(-lengths // size)
+    pages = int(count.sum()) + 2
+    g = torch.Generator(device=DEV).manual_seed(seqs)
+    codes = lambda: torch.randint(-127, 128, (pages, kv, size, d), generator=g, device=DEV, dtype=torch.int8)
+    scale = lambda: 0.005 + 0.025 * torch.rand((pages, kv, size), generator=g, device=DEV)
+    cache = moeq8.KVCacheI8(codes(), scale(), codes(), scale())
+    free, table = rng.permutation(pages).astype(np.int32), np.full((seqs, int(count.max()) + 1), -1, np.int32)
+    at = np.concatenate([[0], np.cumsum(count)])
+    for s in range(seqs):
+        table[s, :count[s]] = free[at[s]:at[s + 1]]
+    visible = np.maximum(lengths[:, None] - (cols - 1 - np.arange(cols))[None], 0).astype(np.int32)
+    q, qv = typed(1.5 * rng.standard_normal((seqs, cols, heads, d)), t)
+    got = moeq8.paged_attention_i8(q.to(DEV), cache, torch.from_numpy(table).to(DEV), torch.from_numpy(visible).to(DEV),
+                                   max_visible=longest).float().cpu().numpy()
+    arrays = [x.cpu().numpy() for x in cache]
+    some = [0, 1, 2, 7, int(rng.integers(8, seqs)), seqs - 1]
+    want, sizes = ref.attention(qv[some], *arrays, table[some], visible[some], d ** -0.5)
+    worst = float((np.abs(got[some] - want) / attention_bound(want, sizes, t, d)).max())
+    say(f"attention {seqs}x{cols}x{longest} heads {heads}/{kv} d {d} {dtype}: {worst:.3f} of the bound")
+    assert worst <= 1.0 and not got[[0, 5]].any()
+    assert np.isfinite(got).all()
+    # each sequence as it comes out in a smaller call of the same split, whose blocks lie elsewhere
+    whole = torch.from_numpy(got)
+    half = moeq8.paged_attention_i8(q[1:].to(DEV), cache, torch.from_numpy(table[1:]).to(DEV),
+                                    torch.from_numpy(visible[1:]).to(DEV), max_visible=longest).float().cpu()
+    near = torch.from_numpy(2 * attention_bound(got[1:].astype(np.float64), (np.full(got[1:].shape, 4.0), *(
+        np.full(got[1:].shape[:3], float(x.max())) for x in sizes[1:])), t, d))
+    assert ((whole[1:] - half).abs() <= near).all()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("tokens,heads,d", [(8201, 8, 128), (16391, 8, 64), (4099, 8, 256), (5501, 6, 176), (32773, 4, 48)])
+def test_cache_rows_of_a_long_prefix(tokens, heads, d, dtype):
+    check_cache(tokens, heads, d, 64, TYPES[dtype], special=True, seed=tokens)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("rows,vocab", [(1700, 5003), (1000, 9001), (4100, 2000)])
+def test_sample_large_batches(rows, vocab, dtype):
+    """Some rows as the definition has them, and all as in smaller batches."""
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    rand = lambda *s: torch.rand(s, generator=g, device=DEV)
+    z = (2 * torch.randn(rows, vocab, generator=g, device=DEV)).to(TYPES[dtype])
+    z[3::50, vocab // 3:] = -float("inf")
+    u = rand(rows)
+    some = lambda x, off: torch.where(rand(rows) < 0.5, x, off)
+    rules = dict(temperature=(0.3 + rand(rows)) * (rand(rows) > 0.05), top_k=some((rand(rows) * 700).int(), 0).int(),
+                 top_p=some(0.3 + 0.69 * rand(rows), 1.0), min_p=some(0.2 * rand(rows), 0.0))
+    token, logprob = moeq8.logits_sample(z, u, **rules)
+    plain, _ = moeq8.logits_sample(z, u)
+    for at in range(0, rows, 300):
+        part = slice(at, min(at + 300, rows))
+        t, l = moeq8.logits_sample(z[part], u[part], **{k: v[part] for k, v in rules.items()})
+        assert torch.equal(t, token[part]) and torch.equal(l, logprob[part])
+        assert torch.equal(moeq8.logits_sample(z[part], u[part])[0], plain[part])
+    host = z.float().cpu().numpy()
+    for r in [0, 3, 53, rows - 1, *np.random.default_rng(1).integers(0, rows, 20)]:
+        want, log = ref.sample_row(host[r], float(u[r]), *(rules[k][r].item() for k in ("temperature", "top_k", "top_p", "min_p")))
+        assert int(token[r]) == want and abs(float(logprob[r]) - log) <= 2.0**-23 * max(abs(log), 1e-7)
+        assert int(plain[r]) == ref.sample_row(host[r], float(u[r]))[0]
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_over_other_orders_of_heads_and_columns(dtype):
+    """Queries and outputs [seqs][heads][cols], and rows of a projection with the keys behind them."""
+    rng = np.random.default_rng(5)
+    seqs, cols, heads, kv, d = 3, 4, 6, 2, 48
+    cache, arrays, _ = make_cache(24, kv, 16, d, seed=5)
+    q, qv = typed(1.5 * rng.standard_normal((seqs, cols, heads, d)), TYPES[dtype])
+    table = torch.from_numpy(rng.permutation(24).astype(np.int32).reshape(seqs, 8)).to(DEV)
+    visible = torch.tensor([[60, 61, 62, 63], [0, 0, 1, 2], [120, 121, 7, 128]], dtype=torch.int32, device=DEV)
+    plain = moeq8.paged_attention_i8(q.to(DEV), cache, table, visible)
+    want, sizes = ref.attention(qv, *arrays, table.cpu().numpy(), visible.cpu().numpy(), d ** -0.5)
+    assert (np.abs(plain.float().cpu().numpy() - want) <= attention_bound(want, sizes, TYPES[dtype], d)).all()
+    turned = torch.empty(seqs, heads, cols, d, dtype=q.dtype, device=DEV).transpose(1, 2)
+    moeq8.paged_attention_i8(q.to(DEV).transpose(1, 2).contiguous().transpose(1, 2), cache, table, visible, out=turned)
+    rows = torch.zeros(seqs * cols, (heads + 2 * kv) * d + 3, dtype=q.dtype, device=DEV)
+    inside = rows[:, :heads * d].view(seqs, cols, heads, d)
+    inside.copy_(q)
+    assert torch.equal(turned, plain) and torch.equal(moeq8.paged_attention_i8(inside, cache, table, visible), plain)
