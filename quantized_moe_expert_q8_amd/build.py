@@ -38,7 +38,7 @@ COMMON_FLAGS = [
     "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wall",
-    "-Wno-unused-function",
+    "-Werror=unused-function",
 ]
 
 

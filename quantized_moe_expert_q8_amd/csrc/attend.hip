@@ -84,14 +84,6 @@ __device__ __forceinline__ uint32_t seen_by(const AttendArgs& a, uint32_t seq, u
     const int32_t n = a.visible[(int64_t)seq * a.cols + col];
     return n < 0 ? 0u : ((uint32_t)n < a.limit ? (uint32_t)n : a.limit);
 }
-__device__ __forceinline__ uint32_t seen_by_any(const AttendArgs& a, uint32_t seq) {
-    uint32_t n = 0;
-    for (uint32_t c = 0; c < a.cols; ++c) {
-        const uint32_t s = seen_by(a, seq, c);
-        n = s > n ? s : n;
-    }
-    return n;
-}
 
 // Over the four lanes that have a row (or a position of the other product): l, l ^ 16, l ^ 32, l ^ 48.
 __device__ __forceinline__ float quad_max(float v) {
