@@ -134,6 +134,63 @@ def test_attention_factors_past_fp32(up, loud, scale):
     assert (np.abs(got - want) <= attention_bound(want, sizes, torch.float32, 64)).all()
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_attention_scores_of_minus_infinity(dtype):
+    """They have no weight; a row that has no others gives zeros, as one that sees nothing."""
+    rng = np.random.default_rng(6)
+    cache, arrays, _ = make_cache(4, 1, 16, 64, seed=6)
+    arrays[0][..., 0] = 1 + np.abs(arrays[0][..., 0])
+    arrays[0][..., 1:] = 0
+    arrays[1].reshape(-1)[:40] = np.inf
+    for x, a in zip(cache, arrays):
+        x.copy_(torch.from_numpy(a))
+    q = torch.zeros(1, 3, 2, 64, dtype=TYPES[dtype], device=DEV)
+    q[..., 0] = -1.5
+    table = torch.arange(4, dtype=torch.int32, device=DEV)[None]
+    got = moeq8.paged_attention_i8(q, cache, table, torch.tensor([[40, 7, 64]], dtype=torch.int32, device=DEV)).float().cpu().numpy()
+    assert not got[:, :2].any()
+    arrays[1].reshape(-1)[:40] = 1e30                       # as good as -inf, where the definition has numbers
+    want, sizes = ref.attention(q.float().cpu().numpy(), *arrays, [[0, 1, 2, 3]], [[40, 7, 64]], 0.125)
+    some = np.full(sizes[2].shape, 64 * 1.5 * 127 * 0.03 / 8)
+    bound = attention_bound(want, (sizes[0], some, some, sizes[3]), TYPES[dtype], 64)
+    assert (np.abs(got - want)[:, 2] <= bound[:, 2]).all()
+
+
+def test_attention_without_a_table():
+    """A table of no entries: no column sees anything."""
+    cache, _, _ = make_cache(2, 2, 16, 32, seed=7)
+    q = torch.randn(2, 3, 4, 32, device=DEV)
+    out = moeq8.paged_attention_i8(q, cache, torch.empty(2, 0, dtype=torch.int32, device=DEV),
+                                   torch.full((2, 3), 9, dtype=torch.int32, device=DEV), out=torch.full_like(q, 5.0))
+    assert not out.any()
+
+
+def test_calls_at_the_same_time():
+    """Two streams, each with its own workspaces, against calls one after another."""
+    g = torch.Generator(device=DEV).manual_seed(9)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV)
+    cache, _, _ = make_cache(300, 2, 16, 64, seed=9)
+    table = torch.randperm(300, generator=g, device=DEV).int()[None]
+    q, z = [rand(1, 2, 4, 64) for _ in range(2)], [2 * rand(40, 30011) for _ in range(2)]
+    visible = [torch.tensor([[4700 - 900 * i, 4800]], dtype=torch.int32, device=DEV) for i in range(2)]
+    u, p = torch.rand(40, generator=g, device=DEV), torch.full((40,), 0.9, device=DEV)
+    bytes_ = (moeq8.paged_attention_workspace_bytes(1, 2, 4, 2, 64, 4800), moeq8.logits_sample_workspace_bytes(40, 30011))
+    spaces = [[torch.empty(n, dtype=torch.uint8, device=DEV) for n in bytes_] for _ in range(2)]
+    run = lambda i: (moeq8.paged_attention_i8(q[i], cache, table, visible[i], workspace=spaces[i][0]),
+                     *moeq8.logits_sample(z[i], u, top_p=p, workspace=spaces[i][1]))
+    want = [run(i) for i in range(2)]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(i))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for result in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(result, want[i]))
+
+
 # ---- sampling ----------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", list(TYPES))
@@ -306,7 +363,8 @@ def test_attention_batches(seqs, cols, heads, kv, d, longest, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
-@pytest.mark.parametrize("tokens,heads,d", [(8201, 8, 128), (16391, 8, 64), (4099, 8, 256), (5501, 6, 176), (32773, 4, 48)])
+@pytest.mark.parametrize("tokens,heads,d", [(8201, 8, 128), (16391, 8, 64), (4099, 8, 256), (5501, 6, 176), (32773, 4, 48),
+                                            (32771, 8, 32), (65541, 8, 16)])
 def test_cache_rows_of_a_long_prefix(tokens, heads, d, dtype):
     check_cache(tokens, heads, d, 64, TYPES[dtype], special=True, seed=tokens)
 
