@@ -680,7 +680,8 @@ int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t 
  * below 2^-38 of a row's largest |q| and below 2^-37 of its largest weight times
  * value scale.  Codes outside of what is seen do not matter, nor do their scales; a
  * scale or query that is not finite follows IEEE arithmetic in the rows that see it
- * and touches no others (infinite sums may come out as NaN).
+ * and touches no others (infinite sums may come out as NaN), but a row whose scores
+ * are all -inf gives zeros.
  *   workspace  at least paged_attention_workspace_bytes() bytes, 16-byte aligned
  *             (NULL where that is 0), that overlap no other argument.  It holds
  *             nothing between calls; calls that may run at the same time need one
@@ -712,8 +713,11 @@ int paged_attention_i8(const void* q, int64_t q_seq_stride, int64_t q_col_stride
  *                for a row without
  * A temperature that is negative or NaN counts as 0; a NaN of the others, or of u,
  * as their NULL or 0.  Sums are exact, of weights rounded to 2^-S, with S from 33 to
- * 51 as a row's sum stays below 2^63; a row without top-k, top-p and min-p takes its
- * draw over sums of 512 logits, joined in 64-bit floats in the order of the indexes.
+ * 51 as a row's sum stays below 2^63; what rounds to 0 is not drawn.  Two sums may be
+ * joined in 64-bit floats, in a fixed order, from exact ones of 512 logits each, of
+ * weights rounded to 2^-51 of the largest among them: what a row without top-k, top-p
+ * and min-p draws from, and the mass that top-p is a part of in a row with min-p and
+ * without top-k.
  * A result does not depend on the number of rows or on their other arguments.
  * vocab < 2^30.
  *   workspace  at least logits_sample_workspace_bytes() bytes, 16-byte aligned, as
