@@ -30,7 +30,7 @@
 // largest.  (The largest vd would not do: that of a position of next to no weight
 // pushed the others below fp16.  It is a number for each row and not for all, which
 // costs 1.1 of 22.2 us where a wave has few tiles and two row tiles, 37 x 5 x 1500,
-// and nothing elsewhere.)  They go as two parts whatever the outputs' type.
+// and 0.3 or less elsewhere.)  They go as two parts whatever the outputs' type.
 // (One part for bf16 outputs, 11 bits, gave 1 to 4 of 100 values as the neighbours of
 // the right ones; the second costs 0.1 of 9.1 us for 777 positions, 1.5 of 21.0 for 5
 // columns of 32768 and nothing for a batch at the rate of memory.)
@@ -45,8 +45,9 @@
 // positions: 20 + 5 us).  For short ones the chain of loads and of the join (777
 // positions 9.2 us in a graph).  With more than 16 rows or fp32 the arithmetic: a tile
 // of 32 positions takes 340 vector instructions for d = 128 and one row tile (and 56
-// where a row's maximum grows), half of them the conversion of its codes, which the rows of a wave share (16 x 8 x 4096, d =
-// 256, 64 rows in 4 parts, f32: 36 us).  Row tiles of 16 for d > 128: two of them left
+// where a row's maximum grows), half of them the conversion of its codes, which the
+// rows of a wave share (16 x 8 x 4096, d = 256, 64 rows in 4 parts, f32: 36 us).  Row
+// tiles of 16 for d > 128: two of them left
 // registers for one wave a SIMD (51 us).  What the rules of the split leave: from 129 to
 // 255 pairs of sequence and key head get a span each, one block a CU (37 x 5 x 1500, 148
 // pairs: 23 us, 108 CUs without work and up to six rounds a wave), and four row tiles
