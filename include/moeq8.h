@@ -678,10 +678,11 @@ int kv_cache_read_i8(const moeq8_kv_cache* cache, const int64_t* slots, int64_t 
  * 2^30, n_table < 2^31, token_stride <= 2^26.  Scores and sums are fp32; fp32
  * queries and the weights go through the matrix cores as two fp16 parts (22 bits),
  * less what is below 2^-38 of a row's largest |q| and below 2^-37 of its largest
- * weight times value scale.  Codes outside of what is seen do not matter, nor do
- * their scales; a scale or query that is not finite follows IEEE arithmetic in the
- * rows that see it and touches no others (infinite sums may come out as NaN), but a
- * row whose scores are all -inf gives zeros.
+ * weight times value scale; key scales from 2^99 on may give infinite scores.
+ * Codes outside of what is seen do not matter, nor do their scales; a scale or
+ * query that is not finite follows IEEE arithmetic in the rows that see it and
+ * touches no others (infinite sums may come out as NaN), but a row whose scores
+ * are all -inf gives zeros.
  *   workspace  at least paged_attention_workspace_bytes() bytes, 16-byte aligned
  *             (NULL where that is 0), that overlap no other argument.  It holds
  *             nothing between calls; calls that may run at the same time need one

@@ -68,6 +68,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int TILE = 32, SEGMENT = 1024;          // positions a tile; positions whose pages a wave holds at a time
+constexpr float STEEP = 0x1p20f;                  // maxima whose last place is not small
 constexpr int WEIGHT_BITS = 12;                   // the largest weight of a row comes to [2^12, 2^13), and may grow to 2^15
 
 struct AttendArgs {
@@ -375,23 +376,33 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
                     for (int t = 0; t < NT; ++t) x[t][i] = here.ok[i / 4] && pos < seen[t] ? x[t][i] : -__builtin_inff();
                 }
             }
-            half8 w[PP][NT];
+            // maxima are of the scores before the factor, which is not negative
+            float now[NT], base[NT];
+            bool plain = whole;                   // nothing of what the tile's rows see needs another look
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 float top_t = x[t][0];
 #pragma unroll
                 for (int i = 1; i < 8; ++i) top_t = fmaxf(top_t, x[t][i]);
-                // maxima are of the scores before the factor, which is not negative
-                const float now = fmaxf(m[t], quad_max(top_t)), base = now == -__builtin_inff() ? 0.0f : now * factor[t];
+                now[t] = fmaxf(m[t], quad_max(top_t));
+                base[t] = now[t] == -__builtin_inff() ? 0.0f : now[t] * factor[t];
+                plain = plain && !__any(fabsf(base[t]) >= STEEP);
+            }
+            half8 w[PP][NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
                 float e[8], v[8], sum = 0.0f, most = 0.0f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    e[i] = __builtin_fmaf(x[t][i], factor[t], -base);
+                    e[i] = __builtin_fmaf(x[t][i], factor[t], -base[t]);
                     v[i] = ve[i];
                 }
-                if (!whole) {                     // the factor may be 0; a position that others see may have a scale that is not finite
+                if (!plain) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
+                        // the product as the maximum's was rounded, whose own rounding would count
+                        e[i] = fabsf(base[t]) >= STEEP ? x[t][i] * factor[t] - base[t] : e[i];
+                        // the factor may be 0; a position that others see may have a scale that is not finite
                         e[i] = x[t][i] == -__builtin_inff() ? x[t][i] : e[i];
                         v[i] = x[t][i] == -__builtin_inff() ? 0.0f : v[i];
                     }
@@ -404,21 +415,21 @@ __global__ __launch_bounds__(W * 64, (W == 8 ? 2 : min_waves<NC, NT>())) void k_
                     most = fmaxf(most, fabsf(v[i]));
                 }
                 // a maximum that grows, or weights past their power of two
-                if (__any(now > m[t] || most >= ldexpf(1.0f, WEIGHT_BITS + 3 - up[t]))) {
+                if (__any(now[t] > m[t] || most >= ldexpf(1.0f, WEIGHT_BITS + 3 - up[t]))) {
                     if (__any(most == __builtin_inff())) {       // infinite ones do not count
                         most = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) most = fmaxf(most, fabsf(v[i]) < __builtin_inff() ? fabsf(v[i]) : 0.0f);
                     }
                     const float was = m[t] == -__builtin_inff() ? m[t] : m[t] * factor[t];
-                    const float fall = now > m[t] ? was - base : 0.0f, keep = __builtin_amdgcn_exp2f(fall);
+                    const float fall = now[t] > m[t] ? was - base[t] : 0.0f, keep = __builtin_amdgcn_exp2f(fall);
                     l[t] *= keep;
                     peak[t] = fmaxf(peak[t] * keep, quad_max(most));
                     const int next = up_for(peak[t]);
                     const float by = __builtin_amdgcn_exp2f(fall + (float)(next - up[t]));
 #pragma unroll
                     for (int i = 0; i < DV; ++i) o[t][i] *= by;
-                    m[t] = now;
+                    m[t] = now[t];
                     up[t] = next;
                 }
                 l[t] += sum;

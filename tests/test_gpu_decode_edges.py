@@ -77,7 +77,8 @@ def crafted(scores, value_scale, signs, heads, d, dtype, seqs=1, size=16, seed=0
     t = np.asarray(signs, np.float64)[:, None] * ks.reshape(-1)[:n].astype(np.float64)
     w = np.exp(t - t.max(1, keepdims=True))
     top = (w / w.sum(1, keepdims=True) * vs.reshape(-1)[:n]).max(1)
-    bound = attention_bound(want, (sizes[0], 0 * sizes[1], *sizes[2:]), dtype, d) + (n * 2.0**-37 * 127 * top)[None, :, None, None]
+    with np.errstate(all="ignore"):                         # no bound for scores past what fp32 tells apart
+        bound = attention_bound(want, (sizes[0], 0 * sizes[1], *sizes[2:]), dtype, d) + (n * 2.0**-37 * 127 * top)[None, :, None, None]
     return got[:1].float().cpu().numpy(), want, bound
 
 
@@ -115,6 +116,24 @@ def test_attention_a_scale_that_counts_in_one_row_alone(heads, d, dtype):
     scores[99], vs[99] = -70, 1e12
     got, want, bound = crafted(scores.astype(np.float32), vs.astype(np.float32), [1.0, -1.0], heads, d, TYPES[dtype])
     assert (np.abs(got - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,d,seqs", [(2, 64, 1), (20, 128, 1), (3, 256, 2100)])
+@pytest.mark.parametrize("size", [1e5, 1e8, 3e9, 1e20, 3e29])
+def test_attention_scores_past_what_fp32_tells_apart(size, heads, d, seqs, dtype):
+    """Scores that lie far apart however they round: the largest has all the weight, of one
+    column the first of them and of the other the last.
+
+    Inner products are held times a power of two that brings the row's largest |q| below
+    2^14, so key scales, the scores here, are good below 2^128 / (2^14 127 d) = 2^99."""
+    rng = np.random.default_rng(11)
+    scores, vs = size * rng.uniform(-1, 1, 300), rng.uniform(0.005, 0.03, 300)
+    scores[[7, 299]] = [1.5 * size, -1.6 * size]
+    got, want, _ = crafted(scores.astype(np.float32), vs.astype(np.float32), [1.0, -1.0], heads, d, TYPES[dtype], seqs)
+    # a weight of 1 times scale in two fp16 parts (2^-22), the product and the sum's division
+    fine = np.abs(want) * 2.0**-20
+    assert (np.abs(got - want) <= fine + half_step(np.abs(want) + fine, TYPES[dtype])).all()
 
 
 @pytest.mark.parametrize("up,loud,scale", [(-135, 0, 2.0**134), (-140, 0, 3e41), (100, 60, 2.0**-162), (120, 70, 2.0**-192), (-100, -60, 2.0**158)])
